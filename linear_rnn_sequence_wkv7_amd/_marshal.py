@@ -1,0 +1,86 @@
+"""Checks and calls shared by the bindings of the per-channel operators (ssm,
+shortconv, groupnorm): argument marshalling only."""
+from __future__ import annotations
+
+import torch
+
+from .wkv7 import Wkv7Error, load_library
+
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
+_NAMES = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def dtype_code(t) -> int:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}; use float32 or bfloat16")
+    return code
+
+
+def dtype_named(name, default):
+    """The torch dtype of "f32" / "bf16" (None: the default)."""
+    if name is None:
+        return default
+    if name not in _NAMES:
+        raise ValueError(f"y_dtype must be one of {sorted(_NAMES)}")
+    return _NAMES[name]
+
+
+def check(name, t, shape, dtype, dev):
+    """t is a contiguous tensor of this shape (a tuple) and dtype on dev."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and on {dev}")
+
+
+def check_if(name, t, shape, dtype, dev):
+    if t is not None:
+        check(name, t, shape, dtype, dev)
+
+
+def gpu(name, t, dims):
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
+    if t.device.type != "cuda":
+        raise ValueError("inputs must be on a GPU device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and on {t.device}")
+    return t.device
+
+
+def ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def size(fn, *args) -> int:
+    """A size query of the library."""
+    n = fn(*args)
+    if n < 0:
+        raise Wkv7Error(int(-n), fn.__name__, load_library().wkv7_last_error().decode())
+    return int(n)
+
+
+def scratch(workspace, need, dev):
+    """The caller's workspace, or one of the needed size, as (pointer, bytes, tensor)."""
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def call(fn, dev, *args):
+    """fn(*args, stream) on dev's current stream, with dev the current device."""
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream)
+    if rc:
+        raise Wkv7Error(rc, fn.__name__, load_library().wkv7_last_error().decode())

@@ -10,9 +10,10 @@
 #include <cstdio>
 #include <cstring>
 
+#include "wkv7_host.h"
 #include "wkv7_internal.h"
 
-namespace {
+namespace wkv7 {
 
 thread_local char g_last_error[512] = "";
 
@@ -23,15 +24,6 @@ int fail(int code, const char* fmt, ...) {
     va_end(ap);
     return code;
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// A named device range [p, p + bytes) for the workspace overlap checks.
-struct Span {
-    const void* p;
-    int64_t bytes;
-    const char* name;
-};
 
 bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
     if (!a || !b || na <= 0 || nb <= 0) return false;
@@ -47,6 +39,12 @@ int check_workspace_disjoint(const void* ws, int64_t need, const Span* spans, in
             return fail(WKV7_EINVAL, "workspace overlaps %s", spans[i].name);
     return WKV7_OK;
 }
+
+}  // namespace wkv7
+
+namespace {
+
+using namespace wkv7;
 
 // Byte sizes of the arrays of one wkv7 call.
 struct Sizes {
@@ -64,7 +62,9 @@ Sizes sizes_of(const wkv7::Params& p) {
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_arch_state[kMaxDevices];
 
-int check_device() {
+}  // namespace
+
+int wkv7::check_device() {
     int dev = -1;
     if (hipGetDevice(&dev) != hipSuccess || dev < 0)
         return fail(WKV7_EDEVICE, "hipGetDevice failed");
@@ -83,6 +83,8 @@ int check_device() {
     if (st != 1) return fail(WKV7_EDEVICE, "device %d is not gfx950", dev);
     return WKV7_OK;
 }
+
+namespace {
 
 // Validate the descriptor and fill the size/mode fields of Params.
 int check_desc(const wkv7_desc* d, wkv7::Params* p) {
@@ -160,12 +162,16 @@ int64_t workspace_bytes(const wkv7::Params& p, int algo) {
     return wkv7::twopass128_workspace_bytes(p.B, p.H, p.T);
 }
 
-int finish_launch(hipError_t e, const char* what) {
+}  // namespace
+
+int wkv7::finish_launch(hipError_t e, const char* what) {
     if (e != hipSuccess) return fail(WKV7_ELAUNCH, "%s launch failed: %s", what, hipGetErrorString(e));
     e = hipGetLastError();
     if (e != hipSuccess) return fail(WKV7_ELAUNCH, "%s launch failed: %s", what, hipGetErrorString(e));
     return WKV7_OK;
 }
+
+namespace {
 
 // How a forward call gets the two-pass form's workspace.
 enum class WsMode { kNone, kCaller, kStatic };

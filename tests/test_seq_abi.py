@@ -1,0 +1,232 @@
+"""The C ABI of the scan, the convolution and the group norm: exported symbols,
+structure layouts, size queries and refusals before any device is touched (CPU
+only); and the refusals of their Python bindings."""
+import ctypes
+import os
+import re
+import subprocess
+
+import pytest
+
+from linear_rnn_sequence_wkv7_amd import groupnorm as N
+from linear_rnn_sequence_wkv7_amd import shortconv as K
+from linear_rnn_sequence_wkv7_amd import ssm as S
+from linear_rnn_sequence_wkv7_amd import wkv7 as W
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+pytestmark = pytest.mark.skipif(not os.path.exists(W.lib_path()), reason="libwkv7.so not built")
+
+SP = 1 << 26          # 64 MiB between fake arrays: disjoint unless a test makes them overlap
+BASE = 1 << 36        # never dereferenced: every case below fails validation, or has nothing to do
+
+
+def declared(header):
+    src = open(os.path.join(ROOT, "include", header)).read()
+    src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
+    return set(re.findall(r"^\s*(?:int|int64_t)\s+(\w+)\s*\(", src, flags=re.M))
+
+
+@pytest.mark.parametrize("header,mod", [("ssm.h", S), ("shortconv.h", K), ("groupnorm.h", N)])
+def test_every_declared_symbol_is_exported(header, mod):
+    names = declared(header)
+    assert names == set(mod.EXPORTED_SYMBOLS)
+    lib = W.load_library()
+    for n in names:
+        assert hasattr(lib, n), n
+
+
+def test_structures_match_the_headers(tmp_path):
+    """Sizes and offsets as a C compiler sees them."""
+    prog = tmp_path / "layout.c"
+    fields = {"ssm": S.SsmDesc, "shortconv": K.ShortconvDesc, "groupnorm": N.GroupnormDesc}
+    lines = ['#include <stdio.h>', '#include <stddef.h>']
+    lines += [f'#include "{n}.h"' for n in fields]
+    lines.append("int main(void) {")
+    for n, st in fields.items():
+        lines.append(f'printf("{n} %zu\\n", sizeof({n}_desc));')
+        lines += [f'printf("{n}.{f[0]} %zu\\n", offsetof({n}_desc, {f[0]}));' for f in st._fields_]
+    lines.append("return 0; }")
+    prog.write_text("\n".join(lines))
+    exe = tmp_path / "layout"
+    subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), str(prog), "-o", str(exe)], check=True)
+    out = dict(l.split() for l in subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.splitlines())
+    for n, st in fields.items():
+        assert int(out[n]) == ctypes.sizeof(st)
+        for f in st._fields_:
+            assert int(out[f"{n}.{f[0]}"]) == getattr(st, f[0]).offset, f
+
+
+# ---- calls with fake pointers -------------------------------------------------
+
+CALLS = {
+    # function: (descriptor maker, pointer names in order, optional ones, written ones)
+    "ssm_forward": ("ssm", "x dt A Bm Cm D dt_bias z state_in y state_out checkpoints", "D dt_bias z state_in state_out checkpoints",
+                    "y state_out checkpoints"),
+    "ssm_step": ("ssm", "x dt A Bm Cm D dt_bias z state state_index y", "D dt_bias z state_index", "state y"),
+    "ssm_backward": ("ssm", "x dt A Bm Cm D dt_bias z state_in dy dstate_out checkpoints dx ddt dA dBm dCm dD ddt_bias dz dstate_in workspace",
+                     "D dt_bias z state_in dstate_out checkpoints dD ddt_bias dz dstate_in",
+                     "dx ddt dA dBm dCm dD ddt_bias dz dstate_in workspace"),
+    "shortconv_forward": ("conv", "x w bias state_in y state_out", "bias state_in state_out", "y state_out"),
+    "shortconv_step": ("conv", "x w bias state state_index y", "bias state_index", "state y"),
+    "shortconv_backward": ("conv", "x w bias state_in dy dstate_out dx dw dbias dstate_in workspace",
+                           "bias state_in dstate_out dbias dstate_in", "dx dw dbias dstate_in workspace"),
+    "groupnorm_forward": ("norm", "x weight bias gate y mean rstd workspace", "weight bias gate mean rstd", "y mean rstd workspace"),
+    "groupnorm_backward": ("norm", "x weight bias gate dy mean rstd dx dweight dbias dgate workspace",
+                           "weight bias gate dweight dbias dgate", "dx dweight dbias dgate workspace"),
+}
+# gradients that go with an input
+PAIRS = {"ssm_backward": {"D": "dD", "dt_bias": "ddt_bias", "z": "dz"}, "shortconv_backward": {"bias": "dbias"},
+         "groupnorm_backward": {"weight": "dweight", "bias": "dbias", "gate": "dgate"}, "groupnorm_forward": {"mean": "rstd"}}
+
+
+def desc(kind, step=False, **kw):
+    T = 1 if step else 70
+    if kind == "ssm":
+        d = dict(B=2, T=T, C=64, N=16, G=1, in_dtype=1, y_dtype=1, dt_softplus=1, S=5)
+        return S.SsmDesc(**{**d, **kw})
+    if kind == "conv":
+        d = dict(B=2, T=T, C=64, K=4, in_dtype=1, y_dtype=1, act=1, S=5)
+        return K.ShortconvDesc(**{**d, **kw})
+    d = dict(B=2, T=T, C=64, G=4, in_dtype=1, y_dtype=1, act=1, eps=1e-5)
+    return N.GroupnormDesc(**{**d, **kw})
+
+
+def call(fn, d=None, **over):
+    kind, names, _, _ = CALLS[fn]
+    S._lib(), K._lib(), N._lib()
+    lib = W.load_library()
+    d = desc(kind, fn.endswith("_step")) if d is None else d
+    args = []
+    for i, n in enumerate(names.split()):
+        args.append(over[n] if n in over else BASE + i * SP)
+        if n == "workspace":
+            args.append(over.get("ws_bytes", SP))
+    return getattr(lib, fn)(None if over.get("no_desc") else ctypes.byref(d), *args, None)
+
+
+def message():
+    return W.load_library().wkv7_last_error().decode()
+
+
+@pytest.mark.parametrize("fn", CALLS)
+def test_pointers(fn):
+    _, names, optional, _ = CALLS[fn]
+    assert call(fn, no_desc=True) == W.WKV7_EINVAL
+    for n in names.split():
+        if n not in optional.split():
+            assert call(fn, **{n: None}) == W.WKV7_EINVAL, n
+            assert f"{n} is NULL" in message()
+        odd = BASE + 2 if n == "state_index" else BASE + 4
+        assert call(fn, **{n: odd}) == W.WKV7_EINVAL, n
+        assert f"{n} is not" in message(), n
+    for a, b in PAIRS.get(fn, {}).items():
+        assert call(fn, **{b: None}) == W.WKV7_EINVAL
+        assert b in message()
+
+
+@pytest.mark.parametrize("fn", CALLS)
+def test_written_arrays_share_no_byte(fn):
+    _, names, _, written = CALLS[fn]
+    names = names.split()
+    at = {n: BASE + i * SP for i, n in enumerate(names)}
+    for w in written.split():
+        for o in names:
+            if o == w or (fn.startswith("groupnorm_forward") and {w, o} == {"mean", "rstd"}):
+                continue
+            if {w, o} == {"state_in", "state_out"}:
+                continue   # in place is allowed
+            assert call(fn, **{w: at[o]}) == W.WKV7_EINVAL, (w, o)
+            assert "overlaps" in message(), (w, o)
+    if "state_out" in names and "state_in" in names:   # in place, but not half
+        assert call(fn, state_out=at["state_in"] + 16) == W.WKV7_EINVAL
+        assert "overlaps" in message()
+
+
+@pytest.mark.parametrize("fn", [f for f in CALLS if "workspace" in CALLS[f][1]])
+def test_workspace_sizes(fn):
+    kind = CALLS[fn][0]
+    d = desc(kind)
+    lib = W.load_library()
+    S._lib(), K._lib(), N._lib()
+    need = {"ssm_backward": lambda: lib.ssm_backward_workspace_bytes(ctypes.byref(d), 0),
+            "shortconv_backward": lambda: lib.shortconv_backward_workspace_bytes(ctypes.byref(d)),
+            "groupnorm_forward": lambda: lib.groupnorm_workspace_bytes(ctypes.byref(d)),
+            "groupnorm_backward": lambda: lib.groupnorm_backward_workspace_bytes(ctypes.byref(d))}[fn]()
+    assert need > 0
+    assert call(fn, ws_bytes=need - 1) == W.WKV7_EINVAL
+    assert f"{need} needed" in message()
+    if fn == "ssm_backward":   # without checkpoints it needs room for them too
+        more = lib.ssm_backward_workspace_bytes(ctypes.byref(d), 1)
+        assert more >= need + lib.ssm_checkpoint_bytes(ctypes.byref(d))
+        assert call(fn, checkpoints=None, ws_bytes=more - 1) == W.WKV7_EINVAL
+        assert f"{more} needed" in message()
+
+
+BAD = {
+    "ssm": [(dict(B=-1), 1), (dict(T=-1), 1), (dict(C=-1), 1), (dict(G=-1), 1), (dict(N=0), 1), (dict(N=65), 2), (dict(G=3), 1),
+            (dict(in_dtype=2), 1), (dict(y_dtype=-1), 1), (dict(dt_softplus=2), 1), (dict(reserved=1), 1), (dict(lengths=BASE + 2), 1),
+            (dict(B=1 << 30, C=1 << 20), 2), (dict(T=2147483647), 2)],
+    "conv": [(dict(B=-1), 1), (dict(T=-1), 1), (dict(C=-1), 1), (dict(K=0), 1), (dict(K=1), 2), (dict(K=5), 2), (dict(in_dtype=2), 1),
+             (dict(y_dtype=5), 1), (dict(act=2), 1), (dict(lengths=BASE + 1), 1), (dict(B=1 << 30, C=1 << 20), 2)],
+    "norm": [(dict(B=-1), 1), (dict(T=-1), 1), (dict(C=-1), 1), (dict(G=0), 1), (dict(G=5), 1), (dict(in_dtype=2), 1), (dict(y_dtype=5), 1),
+             (dict(act=-1), 1), (dict(eps=0.0), 1), (dict(eps=float("nan")), 1), (dict(eps=float("inf")), 1), (dict(lengths=BASE + 3), 1),
+             (dict(B=1 << 30, C=1 << 20, G=1), 2)],
+}
+
+
+@pytest.mark.parametrize("fn", CALLS)
+def test_descriptors(fn):
+    kind = CALLS[fn][0]
+    step = fn.endswith("_step")
+    for kw, code in BAD[kind]:
+        if step and "T" in kw:
+            code = W.WKV7_EINVAL
+        assert call(fn, desc(kind, step, **kw)) == code, kw
+        assert message()
+    if step:
+        assert call(fn, desc(kind, True, T=2)) == W.WKV7_EINVAL
+        assert call(fn, desc(kind, True, lengths=BASE)) == W.WKV7_EINVAL
+        assert call(fn, desc(kind, True, S=-1)) == W.WKV7_EINVAL
+        assert call(fn, desc(kind, True, S=1), state_index=None) == W.WKV7_EINVAL
+        assert "state_index" in message()
+
+
+def test_size_queries():
+    assert S.ssm_checkpoint_bytes(2, 65, 64, 16) == 2 * 2 * 64 * 16 * 4
+    assert S.ssm_checkpoint_bytes(2, 0, 64, 16) == 0
+    assert S.ssm_backward_workspace_bytes(0, 10, 64, 16) == 0
+    assert K.shortconv_backward_workspace_bytes(2, 0, 64, 4) == 0
+    assert N.groupnorm_workspace_bytes(2, 0, 64, 4) == 0
+    for q in (lambda: S.ssm_checkpoint_bytes(2, -1, 64, 16), lambda: S.ssm_backward_workspace_bytes(2, 1, 64, 65),
+              lambda: K.shortconv_backward_workspace_bytes(2, 1, 64, 9), lambda: N.groupnorm_workspace_bytes(2, 1, 64, 5),
+              lambda: N.groupnorm_backward_workspace_bytes(2, 1, 64, 0)):
+        with pytest.raises(W.Wkv7Error):
+            q()
+
+
+def test_nothing_to_do_needs_no_device():
+    assert call("ssm_forward", desc("ssm", B=0)) == W.WKV7_OK
+    assert call("ssm_forward", desc("ssm", T=0), state_out=None) == W.WKV7_OK
+    assert call("ssm_step", desc("ssm", True, B=0)) == W.WKV7_OK
+    assert call("shortconv_forward", desc("conv", B=0)) == W.WKV7_OK
+    assert call("shortconv_step", desc("conv", True, B=0)) == W.WKV7_OK
+    assert call("groupnorm_forward", desc("norm", B=0)) == W.WKV7_OK
+    assert call("shortconv_backward", desc("conv", C=0)) == W.WKV7_OK
+    assert call("groupnorm_backward", desc("norm", C=0, G=1)) == W.WKV7_OK
+
+
+def test_python_bindings_refuse_wrong_tensors():
+    """Shapes, types and devices are checked before the library is called."""
+    import torch
+    x = torch.zeros(2, 3, 8)
+    A, Bm = torch.zeros(8, 4), torch.zeros(2, 3, 1, 4)
+    with pytest.raises(ValueError, match="GPU"):
+        S.ssm_forward(x, x, A, Bm, Bm)
+    with pytest.raises(ValueError, match="dimensions"):
+        S.ssm_forward(x[0], x, A, Bm, Bm)
+    with pytest.raises(ValueError, match="dimensions"):
+        S.ssm_step(x, x, A, Bm, Bm, torch.zeros(2, 8, 4))
+    with pytest.raises(ValueError, match="GPU"):
+        K.shortconv_forward(x, torch.zeros(8, 4))
+    with pytest.raises(ValueError, match="GPU"):
+        N.groupnorm_forward(x, 2)
