@@ -12,7 +12,8 @@
 // are loaded once and, in the backward, a thread sums its channels' parameter
 // gradients over its rows.
 //
-// Otherwise three passes: partial (mean, sum of squared differences) of 64
+// T = 1, other groups of up to 1024 or, even, 2048 channels: the same with one wave
+// to a group.  Otherwise three passes: partial (mean, sum of squared differences) of 64
 // positions of a channel slot (8 channels of one group, or 1), formed block by
 // block in registers around the block's own mean and joined by the parallel
 // variance formula; their join per group; and the elementwise pass.  The backward
@@ -32,7 +33,6 @@ namespace {
 
 constexpr int NTG = 256;
 constexpr int V8 = 8;
-constexpr int PR = 64;   // positions of one partial sum
 
 // Sum over aligned groups of n lanes (a power of two up to 64); every lane gets it.
 template <int LG>
@@ -46,6 +46,24 @@ __device__ __forceinline__ float sum_lanes(float x) {
     return x;
 }
 
+// weight and bias of V channels (c a multiple of V).
+template <int V>
+__device__ __forceinline__ void channel_params(const NormParams& g, int c, float* wt, float* bs) {
+    Pack<float, V> w, b;
+    #pragma unroll
+    for (int j = 0; j < V; ++j) {
+        w.e[j] = 1.f;
+        b.e[j] = 0.f;
+    }
+    if (g.weight) w = ld_pack<V>(g.weight + c, true, V);
+    if (g.bias) b = ld_pack<V>(g.bias + c, true, V);
+    #pragma unroll
+    for (int j = 0; j < V; ++j) {
+        wt[j] = w.e[j];
+        bs[j] = b.e[j];
+    }
+}
+
 struct Rows {
     int slots;   // 8-channel slots of a row
     int cols;    // slots of a workgroup: threads are (row, slot), slots fastest
@@ -54,7 +72,7 @@ struct Rows {
 };
 
 // Forward and backward of rows by themselves, groups of 8 LG channels.
-template <typename Tin, int LG, bool BWD>
+template <typename Tin, typename Ty, int LG, bool BWD>
 __global__ __launch_bounds__(NTG) void norm_rows_kernel(NormParams g, Rows r, float* part) {
     const int at_once = NTG / r.cols;
     const int ry = threadIdx.x / r.cols, sx = threadIdx.x % r.cols;
@@ -63,11 +81,7 @@ __global__ __launch_bounds__(NTG) void norm_rows_kernel(NormParams g, Rows r, fl
     const bool in = ry < at_once && slot < r.slots;
     const int c = in ? slot * V8 : 0;
     float wt[V8], bs[V8], dw[V8] = {}, db[V8] = {};
-    #pragma unroll
-    for (int j = 0; j < V8; ++j) {
-        wt[j] = g.weight ? g.weight[c + j] : 1.f;
-        bs[j] = g.bias ? g.bias[c + j] : 0.f;
-    }
+    channel_params<V8>(g, c, wt, bs);
     const Tin *xp = static_cast<const Tin*>(g.x), *gp = static_cast<const Tin*>(g.gate);
     constexpr float inv = 1.f / (8 * LG);
     for (int64_t row = wg_row * at_once + ry; in && row < g.B; row += r.nrow * at_once) {
@@ -76,7 +90,9 @@ __global__ __launch_bounds__(NTG) void norm_rows_kernel(NormParams g, Rows r, fl
         const bool there = seq_length(g.lengths, row, 1) > 0;
         const Pack<Tin, V8> xr = ld_pack<V8>(xp + e, true, V8);
         Pack<Tin, V8> gr;
+        Pack<Ty, V8> dyr;
         if (g.gate) gr = ld_pack<V8>(gp + e, true, V8);
+        if constexpr (BWD) dyr = ld_pack<V8>(static_cast<const Ty*>(g.dy) + e, true, V8);
         float x[V8], pre[V8], xh[V8], out[V8];
         #pragma unroll
         for (int j = 0; j < V8; ++j) x[j] = widen(xr.e[j]);
@@ -115,8 +131,7 @@ __global__ __launch_bounds__(NTG) void norm_rows_kernel(NormParams g, Rows r, fl
             }
             st_pack_as<V8>(g.y, e, g.y_bf16, out, true, V8);
         } else {
-            float dy[V8], dxh[V8], s1 = 0.f, s2 = 0.f;
-            ld_pack_as<V8>(g.dy, e, g.y_bf16, dy, true, V8);
+            float dxh[V8], s1 = 0.f, s2 = 0.f;
             #pragma unroll
             for (int j = 0; j < V8; ++j) {
                 float act = pre[j], da = 1.f;
@@ -125,7 +140,7 @@ __global__ __launch_bounds__(NTG) void norm_rows_kernel(NormParams g, Rows r, fl
                     act = pre[j] * sg;
                     da = sg * fmaf(pre[j], 1.f - sg, 1.f);
                 }
-                float d = dy[j];
+                float d = widen(dyr.e[j]);
                 out[j] = there ? d * act : 0.f;
                 if (g.gate) d *= widen(gr.e[j]);
                 const float dpre = there ? d * da : 0.f;
@@ -165,20 +180,141 @@ __global__ __launch_bounds__(NTG) void norm_rows_kernel(NormParams g, Rows r, fl
     }
 }
 
-// dweight and dbias: column sums of [rows][2][C]; 16 columns a workgroup, 16 threads to each.
-__global__ __launch_bounds__(256) void norm_sum_kernel(NormParams g, const float* part, int64_t rows) {
-    const int64_t m = int64_t(blockIdx.x) * 16 + (threadIdx.x & 15), M = 2 * int64_t(g.C);
-    const int y = threadIdx.x >> 4;
+// Rows by themselves, any group of up to 64 K V channels: one wave a row and group, V neighbouring
+// channels in each of K runs of 64 lanes.  Wave (chunk, group) takes the rows chunk, chunk + nrow ..
+template <typename Tin, typename Ty, int K, int V, bool BWD>
+__global__ __launch_bounds__(NTG) void norm_wave_kernel(NormParams g, int64_t nrow, float* part) {
+    const int64_t wave = int64_t(blockIdx.x) * (NTG / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, grp = int(wave % g.G), Cg = g.C / g.G;
+    const int64_t chunk = wave / g.G;
+    if (chunk >= nrow) return;
+    const int c0 = grp * Cg + lane * V;
+    bool in[K];
+    float wt[K][V], bs[K][V], dw[K][V] = {}, db[K][V] = {};
+    #pragma unroll
+    for (int k = 0; k < K; ++k) {
+        in[k] = (k * 64 + lane) * V < Cg;
+        #pragma unroll
+        for (int v = 0; v < V; ++v) {
+            wt[k][v] = in[k] && g.weight ? g.weight[c0 + k * 64 * V + v] : 1.f;
+            bs[k][v] = in[k] && g.bias ? g.bias[c0 + k * 64 * V + v] : 0.f;
+        }
+    }
+    const float inv = 1.f / float(Cg);
+    for (int64_t row = chunk; row < g.B; row += nrow) {
+        const int64_t e = row * g.C + c0, st = row * g.G + grp;
+        const bool there = seq_length(g.lengths, row, 1) > 0;
+        float x[K][V], gt[K][V];
+        #pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const Pack<Tin, V> r = ld_pack<V>(static_cast<const Tin*>(g.x) + e + k * 64 * V, false, in[k] ? V : 0);
+            Pack<Tin, V> q;
+            if (g.gate) q = ld_pack<V>(static_cast<const Tin*>(g.gate) + e + k * 64 * V, false, in[k] ? V : 0);
+            #pragma unroll
+            for (int v = 0; v < V; ++v) {
+                x[k][v] = widen(r.e[v]);
+                gt[k][v] = g.gate ? widen(q.e[v]) : 1.f;
+            }
+        }
+        float mean, rstd;
+        if constexpr (!BWD) {
+            float s = 0.f, q = 0.f;
+            #pragma unroll
+            for (int k = 0; k < K; ++k)
+                #pragma unroll
+                for (int v = 0; v < V; ++v) s += x[k][v];
+            mean = sum_lanes<64>(s) * inv;
+            #pragma unroll
+            for (int k = 0; k < K; ++k)
+                #pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const float d = in[k] ? x[k][v] - mean : 0.f;
+                    q = fmaf(d, d, q);
+                }
+            rstd = 1.f / __builtin_sqrtf(fmaf(sum_lanes<64>(q), inv, g.eps));
+            if (!there) {
+                mean = 0.f;
+                rstd = 1.f / __builtin_sqrtf(g.eps);
+            }
+            if (g.mean && lane == 0) {
+                g.mean[st] = mean;
+                g.rstd[st] = rstd;
+            }
+        } else {
+            mean = g.mean[st];
+            rstd = g.rstd[st];
+        }
+        float out[K][V], dxh[K][V], s1 = 0.f, s2 = 0.f;
+        #pragma unroll
+        for (int k = 0; k < K; ++k) {
+            float dy[V];
+            if constexpr (BWD) {
+                const Pack<Ty, V> r = ld_pack<V>(static_cast<const Ty*>(g.dy) + e + k * 64 * V, false, in[k] ? V : 0);
+                #pragma unroll
+                for (int v = 0; v < V; ++v) dy[v] = widen(r.e[v]);
+            }
+            #pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float xh = (x[k][v] - mean) * rstd, pre = fmaf(xh, wt[k][v], bs[k][v]);
+                float act = pre, da = 1.f;
+                if (g.silu) {
+                    const float sg = sigmoidf_(pre);
+                    act = pre * sg;
+                    da = sg * fmaf(pre, 1.f - sg, 1.f);
+                }
+                if constexpr (!BWD) {
+                    out[k][v] = there ? act * gt[k][v] : 0.f;
+                } else {
+                    const bool on = there && in[k];
+                    out[k][v] = on ? dy[v] * act : 0.f;
+                    const float dpre = on ? dy[v] * gt[k][v] * da : 0.f;
+                    x[k][v] = on ? xh : 0.f;
+                    db[k][v] += dpre;
+                    dw[k][v] = fmaf(dpre, x[k][v], dw[k][v]);
+                    dxh[k][v] = dpre * wt[k][v];
+                    s1 += dxh[k][v];
+                    s2 = fmaf(dxh[k][v], x[k][v], s2);
+                }
+            }
+            if constexpr (!BWD) st_pack_as<V>(g.y, e + k * 64 * V, g.y_bf16, out[k], false, in[k] ? V : 0);
+            else if (g.gate) st_pack<V>(static_cast<Tin*>(g.dgate) + e + k * 64 * V, out[k], false, in[k] ? V : 0);
+        }
+        if constexpr (BWD) {
+            s1 = sum_lanes<64>(s1) * inv;
+            s2 = sum_lanes<64>(s2) * inv;
+            #pragma unroll
+            for (int k = 0; k < K; ++k) {
+                #pragma unroll
+                for (int v = 0; v < V; ++v) out[k][v] = there ? (dxh[k][v] - s1 - x[k][v] * s2) * rstd : 0.f;
+                st_pack<V>(static_cast<Tin*>(g.dx) + e + k * 64 * V, out[k], false, in[k] ? V : 0);
+            }
+        }
+    }
+    if constexpr (BWD) {
+        #pragma unroll
+        for (int k = 0; k < K; ++k) {
+            st_pack<V>(part + chunk * 2 * g.C + c0 + k * 64 * V, dw[k], false, in[k] ? V : 0);
+            st_pack<V>(part + (chunk * 2 + 1) * g.C + c0 + k * 64 * V, db[k], false, in[k] ? V : 0);
+        }
+    }
+}
+
+// dweight and dbias: column sums of [rows][2][C]; 32 columns a workgroup, 32 threads to each.
+__global__ __launch_bounds__(1024) void norm_sum_kernel(NormParams g, const float* part, int64_t rows) {
+    const int64_t m = int64_t(blockIdx.x) * 32 + (threadIdx.x & 31), M = 2 * int64_t(g.C);
+    const int y = threadIdx.x >> 5;
     float s = 0.f;
-    if (m < M)
-        for (int64_t i = y; i < rows; i += 16) s += part[i * M + m];
-    __shared__ float sm[16][16];
-    sm[y][threadIdx.x & 15] = s;
+    if (m < M) {
+        #pragma unroll 4
+        for (int64_t i = y; i < rows; i += 32) s += part[i * M + m];
+    }
+    __shared__ float sm[32][32];
+    sm[y][threadIdx.x & 31] = s;
     __syncthreads();
     if (y != 0 || m >= M) return;
     s = 0.f;
     #pragma unroll
-    for (int i = 0; i < 16; ++i) s += sm[i][threadIdx.x & 15];
+    for (int i = 0; i < 32; ++i) s += sm[i][threadIdx.x & 31];
     float* out = m < g.C ? g.dweight : g.dbias;
     if (out) out[m < g.C ? m : m - g.C] = s;
 }
@@ -195,14 +331,14 @@ __device__ __forceinline__ Stats join(Stats a, Stats b) {
     return {n, fmaf(d, f, a.mean), a.m2 + b.m2 + d * d * a.n * f};
 }
 
-// Thread (sequence, run of PR positions, slot of V channels), slots fastest: [B][runs][slots][2].
+// Thread (sequence, run of run_len positions (a multiple of 8), slot of V channels), slots fastest: [B][runs][slots][2].
 template <typename Tin, int V>
-__global__ __launch_bounds__(NTG) void norm_stats_kernel(NormParams g, int slots, int runs, float* part) {
+__global__ __launch_bounds__(NTG) void norm_stats_kernel(NormParams g, int slots, int runs, int run_len, float* part) {
     const int64_t id = int64_t(blockIdx.x) * NTG + threadIdx.x;
     const int slot = int(id % slots), run = int(id / slots % runs);
     const int64_t b = id / slots / runs;
     if (b >= g.B) return;
-    const int len = seq_length(g.lengths, b, g.T), t0 = run * PR, t1 = min(t0 + PR, len);
+    const int len = seq_length(g.lengths, b, g.T), t0 = run * run_len, t1 = min(t0 + run_len, len);
     constexpr int U = 8;
     Stats st{0.f, 0.f, 0.f};
     for (int t = t0; t < t1; t += U) {
@@ -233,17 +369,17 @@ __global__ __launch_bounds__(NTG) void norm_stats_kernel(NormParams g, int slots
 }
 
 // One workgroup per (sequence, group): the join of its partials, in a fixed order.
-__global__ __launch_bounds__(NTG) void norm_join_kernel(NormParams g, int slots, int runs, int V, const float* part,
+__global__ __launch_bounds__(NTG) void norm_join_kernel(NormParams g, int slots, int runs, int run_len, int V, const float* part,
                                                         float* mean, float* rstd) {
     const int64_t b = blockIdx.x / g.G;
     const int grp = int(blockIdx.x % g.G);
     const int len = seq_length(g.lengths, b, g.T);
-    const int gs = slots / g.G, used = (len + PR - 1) / PR;
+    const int gs = slots / g.G, used = (len + run_len - 1) / run_len;
     Stats st{0.f, 0.f, 0.f};
     for (int64_t i = threadIdx.x; i < int64_t(used) * gs; i += NTG) {
         const int run = int(i / gs), s = grp * gs + int(i % gs);
         const int64_t id = (b * runs + run) * slots + s;
-        st = join(st, Stats{float(min(PR, len - run * PR) * V), part[2 * id], part[2 * id + 1]});
+        st = join(st, Stats{float(min(run_len, len - run * run_len) * V), part[2 * id], part[2 * id + 1]});
     }
     __shared__ Stats sm[NTG];
     sm[threadIdx.x] = st;
@@ -260,17 +396,16 @@ __global__ __launch_bounds__(NTG) void norm_join_kernel(NormParams g, int slots,
 // The value before the activation and what follows from it, for one slot of one position.
 template <typename Tin, int V>
 struct Slot {
-    float xh[V], act[V], da[V], gate[V], wt[V];
-    __device__ __forceinline__ void load(const NormParams& g, int64_t e, int c, float mean, float rstd) {
+    float xh[V], act[V], da[V], gate[V];
+    __device__ __forceinline__ void load(const NormParams& g, int64_t e, const float* wt, const float* bs, float mean, float rstd) {
         const Pack<Tin, V> x = ld_pack<V>(static_cast<const Tin*>(g.x) + e, true, V);
         Pack<Tin, V> gt;
         if (g.gate) gt = ld_pack<V>(static_cast<const Tin*>(g.gate) + e, true, V);
         #pragma unroll
         for (int j = 0; j < V; ++j) {
-            wt[j] = g.weight ? g.weight[c + j] : 1.f;
             gate[j] = g.gate ? widen(gt.e[j]) : 1.f;
             xh[j] = (widen(x.e[j]) - mean) * rstd;
-            const float pre = fmaf(xh[j], wt[j], g.bias ? g.bias[c + j] : 0.f);
+            const float pre = fmaf(xh[j], wt[j], bs[j]);
             act[j] = pre;
             da[j] = 1.f;
             if (g.silu) {
@@ -282,61 +417,69 @@ struct Slot {
     }
 };
 
-// Elementwise passes; BWD: dx and dgate, with the two means of each group in m12.
+// Elementwise passes; BWD: dx and dgate, with the two means of each group in m12.  A thread keeps its
+// channels and goes over `per` positions of a sequence, `at_once` apart.
 template <typename Tin, int V, bool BWD>
-__global__ __launch_bounds__(NTG) void norm_apply_kernel(NormParams g, int slots, const float* mean, const float* rstd,
-                                                         const float* m12) {
-    const int64_t n = int64_t(g.B) * g.T * slots;
-    for (int64_t id = int64_t(blockIdx.x) * NTG + threadIdx.x; id < n; id += int64_t(gridDim.x) * NTG) {
-        const int slot = int(id % slots), c = slot * V;
-        const int64_t row = id / slots, b = row / g.T, e = row * g.C + c;
-        const int64_t bg = b * g.G + c / (g.C / g.G);
-        float out[V] = {};
-        const bool there = row - b * g.T < seq_length(g.lengths, b, g.T);
-        if constexpr (!BWD) {
-            if (there) {
-                Slot<Tin, V> s;
-                s.load(g, e, c, mean[bg], rstd[bg]);
+__global__ __launch_bounds__(NTG) void norm_apply_kernel(NormParams g, int slots, int cols, int ncol, int per, const float* mean,
+                                                         const float* rstd, const float* m12) {
+    const int at_once = NTG / cols, ry = threadIdx.x / cols;
+    const int slot = int(blockIdx.x % ncol) * cols + threadIdx.x % cols, c = slot * V;
+    const unsigned rest = blockIdx.x / ncol, chunks = (g.T + per * at_once - 1) / (per * at_once);
+    const int64_t b = rest / chunks;
+    const int t0 = int(rest % chunks) * per * at_once + ry, t1 = min(g.T, t0 - ry + per * at_once);
+    if (ry >= at_once || slot >= slots) return;
+    const int len = seq_length(g.lengths, b, g.T);
+    const int64_t bg = b * g.G + c / (g.C / g.G);
+    const float mu = mean[bg], rs = rstd[bg];
+    const float m1 = BWD ? m12[2 * bg] : 0.f, m2 = BWD ? m12[2 * bg + 1] : 0.f;
+    float wt[V], bs[V];
+    channel_params<V>(g, c, wt, bs);
+    for (int t = t0; t < t1; t += at_once) {
+        const int64_t e = (b * g.T + t) * g.C + c;
+        const bool there = t < len;
+        float out[V] = {}, dg[V] = {};
+        if (there) {
+            Slot<Tin, V> s;
+            s.load(g, e, wt, bs, mu, rs);
+            if constexpr (!BWD) {
                 #pragma unroll
                 for (int j = 0; j < V; ++j) out[j] = s.act[j] * s.gate[j];
-            }
-            st_pack_as<V>(g.y, e, g.y_bf16, out, true, V);
-        } else {
-            float dg[V] = {};
-            if (there) {
-                Slot<Tin, V> s;
-                s.load(g, e, c, mean[bg], rstd[bg]);
+            } else {
                 float dy[V];
                 ld_pack_as<V>(g.dy, e, g.y_bf16, dy, true, V);
-                const float m1 = m12[2 * bg], m2 = m12[2 * bg + 1], rs = rstd[bg];
                 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     dg[j] = dy[j] * s.act[j];
-                    const float dxh = dy[j] * s.gate[j] * s.da[j] * s.wt[j];
+                    const float dxh = dy[j] * s.gate[j] * s.da[j] * wt[j];
                     out[j] = (dxh - m1 - s.xh[j] * m2) * rs;
                 }
             }
+        }
+        if constexpr (!BWD) {
+            st_pack_as<V>(g.y, e, g.y_bf16, out, true, V);
+        } else {
             st_pack<V>(static_cast<Tin*>(g.dx) + e, out, true, V);
             if (g.gate) st_pack<V>(static_cast<Tin*>(g.dgate) + e, dg, true, V);
         }
     }
 }
 
-// Per channel, over PR positions: sums of dpre xh and of dpre, [B][runs][2][C].
+// Per channel, over run_len positions: sums of dpre xh and of dpre, [B][runs][2][C].
 template <typename Tin, int V>
-__global__ __launch_bounds__(NTG) void norm_grad_kernel(NormParams g, int slots, int runs, float* part) {
+__global__ __launch_bounds__(NTG) void norm_grad_kernel(NormParams g, int slots, int runs, int run_len, float* part) {
     const int64_t id = int64_t(blockIdx.x) * NTG + threadIdx.x;
     const int slot = int(id % slots), run = int(id / slots % runs), c = slot * V;
     const int64_t b = id / slots / runs;
     if (b >= g.B) return;
-    const int len = seq_length(g.lengths, b, g.T), t0 = run * PR, t1 = min(t0 + PR, len);
+    const int len = seq_length(g.lengths, b, g.T), t0 = run * run_len, t1 = min(t0 + run_len, len);
     const int64_t bg = b * g.G + c / (g.C / g.G);
     const float mean = g.mean[bg], rstd = g.rstd[bg];
-    float dw[V] = {}, db[V] = {};
+    float dw[V] = {}, db[V] = {}, wt[V], bs[V];
+    channel_params<V>(g, c, wt, bs);
     for (int t = t0; t < t1; ++t) {
         const int64_t e = (b * g.T + t) * g.C + c;
         Slot<Tin, V> s;
-        s.load(g, e, c, mean, rstd);
+        s.load(g, e, wt, bs, mean, rstd);
         float dy[V];
         ld_pack_as<V>(g.dy, e, g.y_bf16, dy, true, V);
         #pragma unroll
@@ -352,10 +495,10 @@ __global__ __launch_bounds__(NTG) void norm_grad_kernel(NormParams g, int slots,
 }
 
 // One workgroup per (sequence, group): the means of dxh and dxh xh from the channels' sums.
-__global__ __launch_bounds__(NTG) void norm_means_kernel(NormParams g, int runs, const float* part, float* m12) {
+__global__ __launch_bounds__(NTG) void norm_means_kernel(NormParams g, int runs, int run_len, const float* part, float* m12) {
     const int64_t b = blockIdx.x / g.G;
     const int Cg = g.C / g.G, c0 = int(blockIdx.x % g.G) * Cg;
-    const int len = seq_length(g.lengths, b, g.T), used = (len + PR - 1) / PR;
+    const int len = seq_length(g.lengths, b, g.T), used = (len + run_len - 1) / run_len;
     float s1 = 0.f, s2 = 0.f;
     for (int64_t i = threadIdx.x; i < int64_t(used) * Cg; i += NTG) {
         const int run = int(i / Cg), c = c0 + int(i % Cg);
@@ -387,44 +530,81 @@ int row_lanes(const NormParams& p) {
     const int lg = Cg / 8;
     return lg <= 64 && (lg & (lg - 1)) == 0 ? lg : 0;
 }
-Rows rows_of(const NormParams& p) {
+Rows rows_of(const NormParams& p, bool bwd) {
     Rows r;
     r.slots = p.C / V8;
     r.cols = r.slots < NTG ? r.slots : NTG;
     r.ncol = (r.slots + r.cols - 1) / r.cols;
     const int64_t at_once = NTG / r.cols, rows = (p.B + at_once - 1) / at_once;
-    const int64_t most = 2048 / r.ncol > 0 ? 2048 / r.ncol : 1;   // 8 workgroups to a compute unit
+    // Workgroups to a compute unit: 8; in the backward 2, since each leaves a row of sums to be added.
+    const int64_t all = bwd ? 512 : 2048, most = all / r.ncol > 0 ? all / r.ncol : 1;
     r.nrow = rows < most ? rows : most;
     return r;
+}
+// Runs of 64 lanes of the wave form (0: the general form), and its rows of waves.
+int wave_runs(const NormParams& p) {
+    const int Cg = p.C / p.G, V = Cg % 2 == 0 ? 2 : 1;
+    return p.T != 1 ? 0 : Cg <= 64 * 4 * V ? 4 : Cg <= 64 * 16 * V ? 16 : 0;
+}
+int64_t wave_rows(const NormParams& p, bool bwd) {
+    const int64_t all = bwd ? 4096 : 16384, most = all / p.G > 0 ? all / p.G : 1;
+    return p.B < most ? p.B : most;
 }
 int channels_per_thread(const NormParams& p) {
     const int Cg = p.C / p.G;
     return Cg % 8 == 0 ? 8 : Cg % 2 == 0 ? 2 : 1;
 }
-int runs_of(const NormParams& p) { return (p.T + PR - 1) / PR; }
+// Positions of one partial sum: 64, fewer where that leaves less than a wave for every SIMD.
+int run_of(const NormParams& p) {
+    int pr = 64;
+    while (pr > 8 && int64_t(p.B) * ((p.T + pr - 1) / pr) * (p.C / channels_per_thread(p)) < 65536) pr /= 2;
+    return pr;
+}
+int runs_of(const NormParams& p) { return (p.T + run_of(p) - 1) / run_of(p); }
 int64_t up(int64_t x) { return (x + 255) & ~int64_t(255); }
 
 template <typename Tin, int LG>
 hipError_t launch_rows(const NormParams& p, bool bwd, hipStream_t stream) {
-    const Rows r = rows_of(p);
+    const Rows r = rows_of(p, bwd);
     float* part = static_cast<float*>(p.ws);
     const dim3 grid{unsigned(r.nrow * r.ncol)};
     if (!bwd) {
-        hipLaunchKernelGGL((norm_rows_kernel<Tin, LG, false>), grid, dim3(NTG), 0, stream, p, r, part);
+        hipLaunchKernelGGL((norm_rows_kernel<Tin, Tin, LG, false>), grid, dim3(NTG), 0, stream, p, r, part);
         return hipGetLastError();
     }
-    hipLaunchKernelGGL((norm_rows_kernel<Tin, LG, true>), grid, dim3(NTG), 0, stream, p, r, part);
-    hipLaunchKernelGGL(norm_sum_kernel, dim3(unsigned((2 * int64_t(p.C) + 15) / 16)), dim3(256), 0, stream, p, part, r.nrow);
+    if (p.y_bf16) hipLaunchKernelGGL((norm_rows_kernel<Tin, bf16_t, LG, true>), grid, dim3(NTG), 0, stream, p, r, part);
+    else hipLaunchKernelGGL((norm_rows_kernel<Tin, float, LG, true>), grid, dim3(NTG), 0, stream, p, r, part);
+    hipLaunchKernelGGL(norm_sum_kernel, dim3(unsigned((2 * int64_t(p.C) + 31) / 32)), dim3(1024), 0, stream, p, part, r.nrow);
+    return hipGetLastError();
+}
+
+template <typename Tin, int K, int V>
+hipError_t launch_wave(const NormParams& p, bool bwd, hipStream_t stream) {
+    const int64_t nrow = wave_rows(p, bwd), per = NTG / 64;
+    float* part = static_cast<float*>(p.ws);
+    const dim3 grid{unsigned((nrow * p.G + per - 1) / per)};
+    if (!bwd) {
+        hipLaunchKernelGGL((norm_wave_kernel<Tin, Tin, K, V, false>), grid, dim3(NTG), 0, stream, p, nrow, part);
+        return hipGetLastError();
+    }
+    if (p.y_bf16) hipLaunchKernelGGL((norm_wave_kernel<Tin, bf16_t, K, V, true>), grid, dim3(NTG), 0, stream, p, nrow, part);
+    else hipLaunchKernelGGL((norm_wave_kernel<Tin, float, K, V, true>), grid, dim3(NTG), 0, stream, p, nrow, part);
+    hipLaunchKernelGGL(norm_sum_kernel, dim3(unsigned((2 * int64_t(p.C) + 31) / 32)), dim3(1024), 0, stream, p, part, nrow);
     return hipGetLastError();
 }
 
 template <typename Tin, int V>
 hipError_t launch_general(const NormParams& p, bool bwd, hipStream_t stream) {
-    const int slots = p.C / V, runs = runs_of(p);
-    const int64_t threads = int64_t(p.B) * runs * slots, n = int64_t(p.B) * p.T * slots;
+    const int slots = p.C / V, runs = runs_of(p), run_len = run_of(p);
+    const int64_t threads = int64_t(p.B) * runs * slots;
     const dim3 g1{unsigned((threads + NTG - 1) / NTG)}, g2{unsigned(int64_t(p.B) * p.G)};
-    const int64_t nb = (n + NTG - 1) / NTG;
-    const dim3 g3{unsigned(nb < (1 << 20) ? nb : (1 << 20))};
+    const int cols = slots < NTG ? slots : NTG, ncol = (slots + cols - 1) / cols, at_once = NTG / cols;
+    // Positions of a thread: 8, fewer where that leaves less than 16 workgroups to a compute unit
+    // (3 x 1531 x 960 fp32: 18.6 us with 8, 8 with 1).
+    int per = 8;
+    while (per > 1 && int64_t(p.B) * p.T * ncol / (at_once * per) < 4096) per /= 2;
+    const int64_t chunks = (p.T + int64_t(per) * at_once - 1) / (int64_t(per) * at_once);
+    const dim3 g3{unsigned(chunks * p.B * ncol)};
     float* ws = static_cast<float*>(p.ws);
     if (!bwd) {
         float *mean = p.mean, *rstd = p.rstd;
@@ -433,18 +613,18 @@ hipError_t launch_general(const NormParams& p, bool bwd, hipStream_t stream) {
             rstd = ws + int64_t(p.B) * p.G;
         }
         float* part = ws + up(2 * int64_t(p.B) * p.G);
-        hipLaunchKernelGGL((norm_stats_kernel<Tin, V>), g1, dim3(NTG), 0, stream, p, slots, runs, part);
-        hipLaunchKernelGGL(norm_join_kernel, g2, dim3(NTG), 0, stream, p, slots, runs, V, part, mean, rstd);
-        hipLaunchKernelGGL((norm_apply_kernel<Tin, V, false>), g3, dim3(NTG), 0, stream, p, slots, mean, rstd,
+        hipLaunchKernelGGL((norm_stats_kernel<Tin, V>), g1, dim3(NTG), 0, stream, p, slots, runs, run_len, part);
+        hipLaunchKernelGGL(norm_join_kernel, g2, dim3(NTG), 0, stream, p, slots, runs, run_len, V, part, mean, rstd);
+        hipLaunchKernelGGL((norm_apply_kernel<Tin, V, false>), g3, dim3(NTG), 0, stream, p, slots, cols, ncol, per, mean, rstd,
                            static_cast<const float*>(nullptr));
         return hipGetLastError();
     }
     float *m12 = ws, *part = ws + up(2 * int64_t(p.B) * p.G);
-    hipLaunchKernelGGL((norm_grad_kernel<Tin, V>), g1, dim3(NTG), 0, stream, p, slots, runs, part);
-    hipLaunchKernelGGL(norm_means_kernel, g2, dim3(NTG), 0, stream, p, runs, part, m12);
-    hipLaunchKernelGGL(norm_sum_kernel, dim3(unsigned((2 * int64_t(p.C) + 15) / 16)), dim3(256), 0, stream, p, part,
+    hipLaunchKernelGGL((norm_grad_kernel<Tin, V>), g1, dim3(NTG), 0, stream, p, slots, runs, run_len, part);
+    hipLaunchKernelGGL(norm_means_kernel, g2, dim3(NTG), 0, stream, p, runs, run_len, part, m12);
+    hipLaunchKernelGGL(norm_sum_kernel, dim3(unsigned((2 * int64_t(p.C) + 31) / 32)), dim3(1024), 0, stream, p, part,
                        int64_t(p.B) * runs);
-    hipLaunchKernelGGL((norm_apply_kernel<Tin, V, true>), g3, dim3(NTG), 0, stream, p, slots, p.mean, p.rstd, m12);
+    hipLaunchKernelGGL((norm_apply_kernel<Tin, V, true>), g3, dim3(NTG), 0, stream, p, slots, cols, ncol, per, p.mean, p.rstd, m12);
     return hipGetLastError();
 }
 
@@ -460,6 +640,12 @@ hipError_t launch_in(const NormParams& p, bool bwd, hipStream_t stream) {
         case 64: return launch_rows<Tin, 64>(p, bwd, stream);
         default: break;
     }
+    const bool even = p.C / p.G % 2 == 0;
+    switch (wave_runs(p)) {
+        case 4: return even ? launch_wave<Tin, 4, 2>(p, bwd, stream) : launch_wave<Tin, 4, 1>(p, bwd, stream);
+        case 16: return even ? launch_wave<Tin, 16, 2>(p, bwd, stream) : launch_wave<Tin, 16, 1>(p, bwd, stream);
+        default: break;
+    }
     switch (channels_per_thread(p)) {
         case 8: return launch_general<Tin, 8>(p, bwd, stream);
         case 2: return launch_general<Tin, 2>(p, bwd, stream);
@@ -470,13 +656,14 @@ hipError_t launch_in(const NormParams& p, bool bwd, hipStream_t stream) {
 }  // namespace
 
 int64_t groupnorm_workspace(const NormParams& p) {
-    if (int64_t(p.B) * p.T * p.C == 0 || row_lanes(p)) return 0;
+    if (int64_t(p.B) * p.T * p.C == 0 || row_lanes(p) || wave_runs(p)) return 0;
     const int64_t slots = p.C / channels_per_thread(p);
     return up(4 * (up(2 * int64_t(p.B) * p.G) + 2 * int64_t(p.B) * runs_of(p) * slots));
 }
 int64_t groupnorm_backward_workspace(const NormParams& p) {
     if (int64_t(p.B) * p.T * p.C == 0) return 0;
-    if (row_lanes(p)) return up(4 * rows_of(p).nrow * 2 * p.C);
+    if (row_lanes(p)) return up(4 * rows_of(p, true).nrow * 2 * p.C);
+    if (wave_runs(p)) return up(4 * wave_rows(p, true) * 2 * p.C);
     return up(4 * (up(2 * int64_t(p.B) * p.G) + 2 * int64_t(p.B) * runs_of(p) * p.C));
 }
 

@@ -96,6 +96,8 @@ int ssm_desc_check(const ssm_desc* d, bool step, SsmParams* p) {
     if (bt > kMaxElems / 64 / (d->C ? d->C : 1) || bc > kMaxItems || (step && int64_t(d->S) * d->C > kMaxElems / 64) ||
         d->T > INT32_MAX - 4096)
         return fail(WKV7_EUNSUPPORTED, "B=%d, T=%d, C=%d or S=%d too large", d->B, d->T, d->C, d->S);
+    // Offsets within 128 rows are 32-bit.
+    if (d->C >= (1 << 22) || int64_t(G) * d->N >= (1 << 22)) return fail(WKV7_EUNSUPPORTED, "C=%d or G*N=%lld too large", d->C, (long long)(int64_t(G) * d->N));
     *p = SsmParams{};
     p->B = d->B; p->T = d->T; p->C = d->C; p->N = d->N; p->G = G; p->S = d->S;
     p->in_bf16 = d->in_dtype == WKV7_BF16; p->y_bf16 = d->y_dtype == WKV7_BF16; p->softplus = d->dt_softplus;

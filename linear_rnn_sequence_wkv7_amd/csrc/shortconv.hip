@@ -49,14 +49,18 @@ __device__ __forceinline__ void input_row(const ConvParams& g, int64_t b, int t,
     for (int j = 0; j < V; ++j) v[j] = widen(r.e[j]);
 }
 
+// A thread's V x K taps lie one after another.
 template <int K, int V>
 __device__ __forceinline__ void load_taps(const ConvParams& g, int c, float (&w)[K][V], float (&bias)[V]) {
+    const Pack<float, V * K> t = ld_pack<V * K>(g.w + int64_t(c) * K, V >= 4, V * K);
     #pragma unroll
     for (int j = 0; j < V; ++j) {
-        bias[j] = g.bias ? g.bias[c + j] : 0.f;
         #pragma unroll
-        for (int k = 0; k < K; ++k) w[k][j] = g.w[int64_t(c + j) * K + k];
+        for (int k = 0; k < K; ++k) w[k][j] = t.e[j * K + k];
     }
+    const Pack<float, V> b = g.bias ? ld_pack<V>(g.bias + c, true, V) : Pack<float, V>{};
+    #pragma unroll
+    for (int j = 0; j < V; ++j) bias[j] = b.e[j];
 }
 
 template <typename Tin, int K, int V>
@@ -109,39 +113,53 @@ __global__ __launch_bounds__(NTC) void conv_forward_kernel(ConvParams g, Runs r)
     }
 }
 
-template <typename Tin, int K, int V>
+// R rows at once: their loads are in flight together and the taps are loaded once.
+template <typename Tin, int K, int V, int R>
 __global__ __launch_bounds__(NTC) void conv_step_kernel(ConvParams g) {
     const int slots = g.C / V, nsb = (slots + NTC - 1) / NTC;
-    const int b = int(blockIdx.x / nsb), s = int(blockIdx.x % nsb) * NTC + threadIdx.x;
+    const int b0 = int(blockIdx.x / nsb) * R, s = int(blockIdx.x % nsb) * NTC + threadIdx.x;
     const bool in = s < slots;
     const int c = in ? s * V : 0;
-    const int slot = g.index ? g.index[b] : b;
-    bool mine = slot >= 0 && slot < g.S;
-    Tin* st = static_cast<Tin*>(g.s1) + (int64_t(slot) * (K - 1)) * g.C + c;
-    Pack<Tin, V> row[K];
-    row[K - 1] = ld_pack<V>(static_cast<const Tin*>(g.x) + int64_t(b) * g.C + c, true, V);
+    int slot[R];
+    bool mine[R];
+    Pack<Tin, V> row[R][K];
     #pragma unroll
-    for (int k = 0; k < K - 1; ++k) row[k] = mine ? ld_pack<V>(st + int64_t(k) * g.C, true, V) : row[K - 1];
-    float w[K][V], bias[V], y[V];
+    for (int r = 0; r < R; ++r) {
+        const int b = min(b0 + r, g.B - 1);
+        slot[r] = g.index ? g.index[b] : b;
+        mine[r] = b0 + r < g.B && slot[r] >= 0 && slot[r] < g.S;
+        const Tin* st = static_cast<const Tin*>(g.s1) + int64_t(mine[r] ? slot[r] : 0) * (K - 1) * g.C + c;
+        row[r][K - 1] = ld_pack<V>(static_cast<const Tin*>(g.x) + int64_t(b) * g.C + c, true, V);
+        #pragma unroll
+        for (int k = 0; k < K - 1; ++k)
+            if (mine[r]) row[r][k] = ld_pack<V>(st + int64_t(k) * g.C, true, V);
+    }
+    float w[K][V], bias[V];
     load_taps<K, V>(g, c, w, bias);
-    if (g.index && mine) mine = first_of_slot(g.index, b, slot, NTC);
+    if (g.index) first_of_slots<R>(g.index, b0, slot, mine, NTC);
     if (!in) return;
     #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        float pre = bias[j];
+    for (int r = 0; r < R; ++r) {
+        if (b0 + r >= g.B) break;
+        float y[V];
         #pragma unroll
-        for (int k = 0; k < K; ++k) pre = fmaf(w[k][j], widen(row[k].e[j]), pre);
-        y[j] = mine ? act_of(pre, g.silu) : 0.f;
+        for (int j = 0; j < V; ++j) {
+            float pre = bias[j];
+            #pragma unroll
+            for (int k = 0; k < K; ++k) pre = fmaf(w[k][j], widen(row[r][k].e[j]), pre);
+            y[j] = mine[r] ? act_of(pre, g.silu) : 0.f;
+        }
+        st_pack_as<V>(g.y, int64_t(b0 + r) * g.C + c, g.y_bf16, y, true, V);
+        if (!mine[r]) continue;
+        Tin* st = static_cast<Tin*>(g.s1) + int64_t(slot[r]) * (K - 1) * g.C + c;
+        #pragma unroll
+        for (int k = 0; k < K - 1; ++k) *reinterpret_cast<Pack<Tin, V>*>(st + int64_t(k) * g.C) = row[r][k + 1];
     }
-    st_pack_as<V>(g.y, int64_t(b) * g.C + c, g.y_bf16, y, true, V);
-    if (!mine) return;
-    #pragma unroll
-    for (int k = 0; k < K - 1; ++k) *reinterpret_cast<Pack<Tin, V>*>(st + int64_t(k) * g.C) = row[k + 1];
 }
 
 // A workgroup has 64 slots and 4 neighbouring runs of one sequence; its sums of the
 // taps' and the bias' gradients go to one row of the workspace, [rows][K + 1][C].
-template <typename Tin, int K, int V>
+template <typename Tin, typename Ty, int K, int V>
 __global__ __launch_bounds__(NTC) void conv_backward_kernel(ConvParams g, Runs r, float* part) {
     const int nsb = (r.slots + 63) / 64, nrb = (r.runs + 3) / 4;
     const int64_t item = xcd_order(blockIdx.x, gridDim.x);
@@ -156,55 +174,80 @@ __global__ __launch_bounds__(NTC) void conv_backward_kernel(ConvParams g, Runs r
         float w[K][V], bias[V], win[K][V], dp[K][V] = {};
         load_taps<K, V>(g, c, w, bias);
         #pragma unroll
-        for (int k = 0; k < K - 1; ++k) input_row<Tin, V>(g, b, t0 - K + 1 + k, c, win[k + 1]);
+        for (int k = 0; k < K - 1; ++k) {
+            input_row<Tin, V>(g, b, min(t0 - K + 1 + k, g.T - 1), c, win[k + 1]);
+            if (t0 - K + 1 + k >= len) {   // padding: it meets gradients of 0 only, but may be no number
+                #pragma unroll
+                for (int j = 0; j < V; ++j) win[k + 1][j] = 0.f;
+            }
+        }
         // Outputs t0 .. t1 + K - 2; input t - K + 1 is done after output t.  The first run has the state's too.
         const int first = run == 0 ? 1 - K : t0;
-        for (int t = t0; t < t1 + K - 1; ++t) {
-            const bool there = t < len;
-            float xv[V], dy[V];
+        // Rows are loaded a group ahead.
+        constexpr int U = 4;
+        Pack<Tin, V> x_n[U];
+        Pack<Ty, V> dy_n[U];
+        auto load = [&](int tb) {
             #pragma unroll
-            for (int j = 0; j < V; ++j) xv[j] = dy[j] = 0.f;
-            if (there) {
-                input_row<Tin, V>(g, b, t, c, xv);
-                ld_pack_as<V>(g.dy, (b * g.T + t) * g.C + c, g.y_bf16, dy, true, V);
+            for (int i = 0; i < U; ++i) {
+                const int64_t e = (b * g.T + min(tb + i, g.T - 1)) * g.C + c;
+                x_n[i] = ld_pack<V>(static_cast<const Tin*>(g.x) + e, true, V);
+                dy_n[i] = ld_pack<V>(static_cast<const Ty*>(g.dy) + e, true, V);
             }
+        };
+        load(t0);
+        for (int tb = t0; tb < t1 + K - 1; tb += U) {
+            Pack<Tin, V> xr[U];
+            Pack<Ty, V> dyr[U];
             #pragma unroll
-            for (int j = 0; j < V; ++j) {
+            for (int i = 0; i < U; ++i) {
+                xr[i] = x_n[i];
+                dyr[i] = dy_n[i];
+            }
+            load(tb + U);
+            #pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int t = tb + i;
+                if (t >= t1 + K - 1) break;
+                const bool there = t < len;
                 #pragma unroll
-                for (int k = 0; k < K - 1; ++k) {
-                    win[k][j] = win[k + 1][j];
-                    dp[k][j] = dp[k + 1][j];
-                }
-                win[K - 1][j] = xv[j];
-                float pre = bias[j];
-                #pragma unroll
-                for (int k = 0; k < K; ++k) pre = fmaf(w[k][j], win[k][j], pre);
-                const float d = there ? dy[j] * act_grad(pre, g.silu) : 0.f;
-                dp[K - 1][j] = d;
-                if (t < t1 && there) {
-                    db[j] += d;
+                for (int j = 0; j < V; ++j) {
                     #pragma unroll
-                    for (int k = 0; k < K; ++k) dw[k][j] = fmaf(d, win[k][j], dw[k][j]);
+                    for (int k = 0; k < K - 1; ++k) {
+                        win[k][j] = win[k + 1][j];
+                        dp[k][j] = dp[k + 1][j];
+                    }
+                    win[K - 1][j] = there ? widen(xr[i].e[j]) : 0.f;
+                    float pre = bias[j];
+                    #pragma unroll
+                    for (int k = 0; k < K; ++k) pre = fmaf(w[k][j], win[k][j], pre);
+                    const float d = there ? widen(dyr[i].e[j]) * act_grad(pre, g.silu) : 0.f;
+                    dp[K - 1][j] = d;
+                    if (t < t1) {
+                        db[j] += d;
+                        #pragma unroll
+                        for (int k = 0; k < K; ++k) dw[k][j] = fmaf(d, win[k][j], dw[k][j]);
+                    }
                 }
-            }
-            const int ti = t - (K - 1);
-            if (ti < first) continue;
-            float dx[V];
-            #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                dx[j] = 0.f;
+                const int ti = t - (K - 1);
+                if (ti < first) continue;
+                float dx[V];
                 #pragma unroll
-                for (int k = 0; k < K; ++k) dx[j] = fmaf(w[K - 1 - k][j], dp[k][j], dx[j]);
+                for (int j = 0; j < V; ++j) {
+                    dx[j] = 0.f;
+                    #pragma unroll
+                    for (int k = 0; k < K; ++k) dx[j] = fmaf(w[K - 1 - k][j], dp[k][j], dx[j]);
+                }
+                const int k1 = ti - (len - (K - 1));   // its place in state_out
+                if (g.ds1 && k1 >= 0 && k1 < K - 1) {
+                    float s[V];
+                    ld_pack_as<V>(g.ds1, (b * (K - 1) + k1) * g.C + c, false, s, true, V);
+                    #pragma unroll
+                    for (int j = 0; j < V; ++j) dx[j] += s[j];
+                }
+                if (ti >= 0) st_pack<V>(static_cast<Tin*>(g.dx) + (b * g.T + ti) * g.C + c, dx, true, V);
+                else if (g.ds0) st_pack<V>(g.ds0 + (b * (K - 1) + ti + K - 1) * g.C + c, dx, true, V);
             }
-            const int k1 = ti - (len - (K - 1));   // its place in state_out
-            if (g.ds1 && k1 >= 0 && k1 < K - 1) {
-                float s[V];
-                ld_pack_as<V>(g.ds1, (b * (K - 1) + k1) * g.C + c, false, s, true, V);
-                #pragma unroll
-                for (int j = 0; j < V; ++j) dx[j] += s[j];
-            }
-            if (ti >= 0) st_pack<V>(static_cast<Tin*>(g.dx) + (b * g.T + ti) * g.C + c, dx, true, V);
-            else if (g.ds0) st_pack<V>(g.ds0 + (b * (K - 1) + ti + K - 1) * g.C + c, dx, true, V);
         }
     }
     // Sum over the 4 runs, in their order.
@@ -233,21 +276,23 @@ __global__ __launch_bounds__(NTC) void conv_backward_kernel(ConvParams g, Runs r
     }
 }
 
-// Column sums of the workspace rows: 16 columns a workgroup, 16 threads to each.
+// Column sums of the workspace rows: 32 columns a workgroup, 32 threads to each.
 template <int K>
-__global__ __launch_bounds__(256) void conv_sum_kernel(ConvParams g, const float* part, int64_t rows) {
-    const int64_t m = int64_t(blockIdx.x) * 16 + (threadIdx.x & 15), M = int64_t(K + 1) * g.C;
-    const int y = threadIdx.x >> 4;
+__global__ __launch_bounds__(1024) void conv_sum_kernel(ConvParams g, const float* part, int64_t rows) {
+    const int64_t m = int64_t(blockIdx.x) * 32 + (threadIdx.x & 31), M = int64_t(K + 1) * g.C;
+    const int y = threadIdx.x >> 5;
     float s = 0.f;
-    if (m < M)
-        for (int64_t i = y; i < rows; i += 16) s += part[i * M + m];
-    __shared__ float sm[16][16];
-    sm[y][threadIdx.x & 15] = s;
+    if (m < M) {
+        #pragma unroll 4
+        for (int64_t i = y; i < rows; i += 32) s += part[i * M + m];
+    }
+    __shared__ float sm[32][32];
+    sm[y][threadIdx.x & 31] = s;
     __syncthreads();
     if (y != 0 || m >= M) return;
     s = 0.f;
     #pragma unroll
-    for (int i = 0; i < 16; ++i) s += sm[i][threadIdx.x & 15];
+    for (int i = 0; i < 32; ++i) s += sm[i][threadIdx.x & 31];
     const int k = int(m / g.C), c = int(m % g.C);
     if (k < K) g.dw[int64_t(c) * K + k] = s;
     else if (g.dbias) g.dbias[c] = s;
@@ -275,32 +320,49 @@ Runs runs_of(const ConvParams& p, int V) {
     r.runs = (p.T + r.len - 1) / r.len;
     return r;
 }
-int channels_per_thread(const ConvParams& p) { return p.C % 8 == 0 ? 8 : p.C % 2 == 0 ? 2 : 1; }
+// 8 channels of bf16 are a 16-byte load.  The backward's 4 K + 3 registers a channel leave room for two
+// waves to a SIMD with 8 channels, for four with 4 (4 x 2048 x 2048 x 4 bf16: 48 and 36 us).
+int channels_per_thread(const ConvParams& p, bool bwd) {
+    return p.C % 8 == 0 && !bwd ? 8 : p.C % 4 == 0 ? 4 : p.C % 2 == 0 ? 2 : 1;
+}
 
 template <typename Tin, int K, int V>
 hipError_t launch_k(const ConvParams& p, int what, hipStream_t stream) {
+    const Runs r = runs_of(p, V);
+    if constexpr (V == 8) {
+        if (what == 2) return hipErrorInvalidValue;   // channels_per_thread gives 4 at most
+    }
     if (what == 1) {
         const int64_t nsb = (p.C / V + NTC - 1) / NTC;
-        hipLaunchKernelGGL((conv_step_kernel<Tin, K, V>), dim3(unsigned(nsb * p.B)), dim3(NTC), 0, stream, p);
+        // two rows to a workgroup where that leaves one for every compute unit
+        if (nsb * p.B >= 512) {
+            hipLaunchKernelGGL((conv_step_kernel<Tin, K, V, 2>), dim3(unsigned(nsb * ((p.B + 1) / 2))), dim3(NTC), 0, stream, p);
+        } else {
+            hipLaunchKernelGGL((conv_step_kernel<Tin, K, V, 1>), dim3(unsigned(nsb * p.B)), dim3(NTC), 0, stream, p);
+        }
         return hipGetLastError();
     }
-    const Runs r = runs_of(p, V);
     if (what == 0) {
         const int64_t threads = int64_t(p.B) * r.runs * r.slots;
         hipLaunchKernelGGL((conv_forward_kernel<Tin, K, V>), dim3(unsigned((threads + NTC - 1) / NTC)), dim3(NTC), 0, stream, p, r);
         return hipGetLastError();
     }
-    const int64_t nsb = (r.slots + 63) / 64, nrb = (r.runs + 3) / 4;
-    float* part = static_cast<float*>(p.ws);
-    hipLaunchKernelGGL((conv_backward_kernel<Tin, K, V>), dim3(unsigned(nsb * nrb * p.B)), dim3(NTC), 0, stream, p, r, part);
-    hipLaunchKernelGGL((conv_sum_kernel<K>), dim3(unsigned((int64_t(K + 1) * p.C + 15) / 16)), dim3(256), 0, stream, p, part, nrb * p.B);
+    if constexpr (V < 8) {
+        const int64_t nsb = (r.slots + 63) / 64, nrb = (r.runs + 3) / 4;
+        float* part = static_cast<float*>(p.ws);
+        const dim3 grid{unsigned(nsb * nrb * p.B)};
+        if (p.y_bf16) hipLaunchKernelGGL((conv_backward_kernel<Tin, bf16_t, K, V>), grid, dim3(NTC), 0, stream, p, r, part);
+        else hipLaunchKernelGGL((conv_backward_kernel<Tin, float, K, V>), grid, dim3(NTC), 0, stream, p, r, part);
+        hipLaunchKernelGGL((conv_sum_kernel<K>), dim3(unsigned((int64_t(K + 1) * p.C + 31) / 32)), dim3(1024), 0, stream, p, part, nrb * p.B);
+    }
     return hipGetLastError();
 }
 
 template <typename Tin, int K>
 hipError_t launch_v(const ConvParams& p, int what, hipStream_t stream) {
-    switch (channels_per_thread(p)) {
+    switch (channels_per_thread(p, what == 2)) {
         case 8: return launch_k<Tin, K, 8>(p, what, stream);
+        case 4: return launch_k<Tin, K, 4>(p, what, stream);
         case 2: return launch_k<Tin, K, 2>(p, what, stream);
         default: return launch_k<Tin, K, 1>(p, what, stream);
     }
@@ -321,7 +383,7 @@ hipError_t launch(const ConvParams& p, int what, hipStream_t stream) {
 
 int64_t shortconv_backward_workspace(const ConvParams& p) {
     if (int64_t(p.B) * p.T * p.C == 0) return 0;
-    const Runs r = runs_of(p, channels_per_thread(p));
+    const Runs r = runs_of(p, channels_per_thread(p, true));
     return (int64_t(p.B) * ((r.runs + 3) / 4) * (p.K + 1) * p.C * 4 + 255) & ~int64_t(255);
 }
 

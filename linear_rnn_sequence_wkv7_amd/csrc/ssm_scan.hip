@@ -32,325 +32,306 @@ namespace wkv7 {
 namespace {
 
 constexpr int TW = 16;   // tokens of one wave in a round
+constexpr int CH = 16;   // channels of a wave
+constexpr int E = 4;     // channels of a lane where it loads and stores elements
 constexpr int TP = 20;   // LDS row of 16 tokens, padded
 
-// Sum y[t] over the LPC lanes of a channel for LPC tokens; lane q keeps token q.
-template <int LPC>
-__device__ __forceinline__ float sum_transposed(float* y, int lane) {
-    if constexpr (LPC >= 16) {
-        const bool hi = lane & 8;
-        #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = (hi ? y[i + 8] : y[i]) + dpp<kDppRowMirror>(hi ? y[i] : y[i + 8]);
-    }
-    if constexpr (LPC >= 8) {
-        const bool hi = lane & 4;
-        #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = (hi ? y[i + 4] : y[i]) + dpp<kDppRowHalfMirror>(hi ? y[i] : y[i + 4]);
-    }
-    if constexpr (LPC >= 4) {
-        const bool hi = lane & 2;
-        #pragma unroll
-        for (int i = 0; i < 2; ++i) y[i] = (hi ? y[i + 2] : y[i]) + dpp<kDppQuadXor2>(hi ? y[i] : y[i + 2]);
-    }
-    const bool hi = lane & 1;
-    return (hi ? y[1] : y[0]) + dpp<kDppQuadXor1>(hi ? y[0] : y[1]);
-}
-
-template <typename Tin, int LPC, int NPL, int WT>
+// VEC: every row of channels and of states starts on 4 bytes, for each group too, and no lane has
+// only some of its NPL states.
+template <typename Tin, int NPL, int WT, bool VEC>
 __global__ __launch_bounds__(64 * WT) void ssm_scan_kernel(SsmParams g) {
-    constexpr int CH = 64 / LPC, E = CH / 4, NP = LPC * NPL, BN = NP / 4;
-    __shared__ float s_d[WT][CH][TP], s_u[WT][CH][TP];
-    __shared__ float s_b[WT][TW][NP], s_c[WT][TW][NP];
-    __shared__ float s_p[WT > 1 ? 2 : 1][WT][64 * NPL], s_h[WT > 1 ? 2 : 1][WT][64 * NPL];
+    constexpr int ROUND = TW * WT, ES = int(sizeof(Tin));
+    __shared__ float s_d[WT][CH][TP], s_u[WT][CH][TP], s_y[WT][4][CH][TP];
+    __shared__ float s_p[WT > 1 ? 2 : 1][WT][NPL][64], s_h[WT > 1 ? 2 : 1][WT][NPL][64];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
     // The workgroup's sequence, group and channels.
-    const int64_t item = xcd_order(blockIdx.x, gridDim.x);
-    const int Cg = g.C / g.G, ncb = (Cg + CH - 1) / CH;
+    const unsigned item = unsigned(xcd_order(blockIdx.x, gridDim.x));
+    const int Cg = g.C / g.G;
+    const unsigned ncb = (Cg + CH - 1) / CH;
     const int cb = int(item % ncb), grp = int(item / ncb % g.G);
     const int64_t b = item / ncb / g.G;
     const int c0 = grp * Cg + cb * CH, nc = min(CH, Cg - cb * CH);   // first channel, channels there
-    const int len = seq_length(g.lengths, b, g.T);
+    const int len = __builtin_amdgcn_readfirstlane(seq_length(g.lengths, b, g.T));
 
-    // A lane's share of the states ...
-    const int ch = lane / LPC, q = lane % LPC;
+    // A lane's share of the states: channel ch, states n0 .. n0 + NPL ...
+    const int ch = lane & 15, q = lane >> 4, n0 = q * NPL;
     const bool ch_in = ch < nc;
     float A2[NPL], h[NPL];
-    const int64_t srow = (b * g.C + c0 + ch) * g.N + q * NPL;
+    const int64_t srow = (b * g.C + c0 + ch) * g.N + n0;
     #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-        const bool in = ch_in && q * NPL + i < g.N;
-        A2[i] = in ? g.A[int64_t(c0 + ch) * g.N + q * NPL + i] * kLog2e : 0.f;
+        const bool in = ch_in && n0 + i < g.N;
+        A2[i] = in ? g.A[int64_t(c0 + ch) * g.N + n0 + i] * kLog2e : 0.f;
         h[i] = in && g.s0 ? g.s0[srow + i] : 0.f;
     }
-    // ... and of the elements: token lane / 4, channels e0 .. e0 + E.
+    // ... of the elements: token te, channels e0 .. e0 + E; and of B and C: token ch, states n0 .. n0 + NPL.
+    // What a lane makes of channels that are not there no other lane sees.
     const int te = lane >> 2, e0 = (lane & 3) * E, ne = nc - e0;
-    const bool whole = g.vec_c && ne >= E, bwhole = g.vec_n;
-    const int bn0 = (lane & 3) * BN, nb = g.N - bn0;
     float bias[E], Dv[E];
     #pragma unroll
     for (int i = 0; i < E; ++i) {
         bias[i] = g.dt_bias && i < ne ? g.dt_bias[c0 + e0 + i] : 0.f;
         Dv[i] = g.D && i < ne ? g.D[c0 + e0 + i] : 0.f;
     }
-    const Tin *xp = static_cast<const Tin*>(g.x), *dtp = static_cast<const Tin*>(g.dt), *zp = static_cast<const Tin*>(g.z);
-    const Tin *bp = static_cast<const Tin*>(g.Bm), *cp = static_cast<const Tin*>(g.Cm);
 
-    Pack<Tin, E> x_n, dt_n, z_n;
-    Pack<Tin, BN> b_n, c_n;
-    auto load = [&](int t0) {
-        const int64_t t = b * g.T + min(t0 + w * TW + te, g.T - 1);
-        const int64_t e = t * g.C + c0 + e0;
-        x_n = ld_pack<E>(xp + e, whole, ne);
-        dt_n = ld_pack<E>(dtp + e, whole, ne);
-        if (g.z) z_n = ld_pack<E>(zp + e, whole, ne);
-        const int64_t r = (t * g.G + grp) * g.N + bn0;
-        b_n = ld_pack<BN>(bp + r, bwhole, nb);
-        c_n = ld_pack<BN>(cp + r, bwhole, nb);
+    // Rows of a round through descriptors that end with the sequence, at offsets that stay the same:
+    // a padded token's x, z, B and C are 0.
+    const uint32_t eoff = uint32_t((w * TW + te) * g.C + c0 + e0);
+    const uint32_t voff = n0 < g.N ? uint32_t((w * TW + ch) * g.G * g.N + grp * g.N + n0) * ES : 0xfffffff0u;
+    const int64_t erow = int64_t(g.C) * ES, vrow = int64_t(g.G) * g.N * ES, yrow = int64_t(g.C) * (g.y_bf16 ? 2 : 4);
+    const char *xp = static_cast<const char*>(g.x) + b * g.T * erow, *dtp = static_cast<const char*>(g.dt) + b * g.T * erow;
+    const char *zp = g.z ? static_cast<const char*>(g.z) + b * g.T * erow : xp;
+    const char *bp = static_cast<const char*>(g.Bm) + b * g.T * vrow, *cp = static_cast<const char*>(g.Cm) + b * g.T * vrow;
+    char* yp = static_cast<char*>(g.y) + b * g.T * yrow;
+    const int zkeep = g.z ? -1 : 0, ykeep = g.y ? -1 : 0;
+    struct Inputs {
+        Raw<Tin, E, VEC> x, dt, z;
+        Raw<Tin, NPL, VEC> b, c;
+    } nx;
+    int left = len;   // tokens from the next load on
+    auto load = [&]() {
+        const int n = max(0, min(left, ROUND)), eb = n * int(erow), vb = n * int(vrow);
+        nx.dt.load(buf_rsrc(dtp, eb), eoff * ES, ne);
+        nx.x.load(buf_rsrc(xp, eb), eoff * ES, ne);
+        nx.b.load(buf_rsrc(bp, vb), voff, g.N - n0);
+        nx.c.load(buf_rsrc(cp, vb), voff, g.N - n0);
+        nx.z.load(buf_rsrc(zp, eb & zkeep), eoff * ES, ne);
+        dtp += ROUND * erow;
+        xp += ROUND * erow;
+        zp += ROUND * erow;
+        bp += ROUND * vrow;
+        cp += ROUND * vrow;
+        left -= ROUND;
     };
-    if (len > 0) load(0);
-    int par = 0;
-    for (int t0 = 0; t0 < len; t0 += TW * WT) {
-        const Pack<Tin, E> x_c = x_n, z_c = z_n;
-        const int t = t0 + w * TW + te;
-        const bool in = t < len;
-        {   // elements into the wave's LDS; a padded token has d = 0 and B = 0: it leaves the state as it is
-            #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                float d = widen(dt_n.e[i]) + bias[i];
-                if (g.softplus) d = softplusf_(d);
-                d = in ? d : 0.f;
-                s_d[w][e0 + i][te] = d;
-                s_u[w][e0 + i][te] = in ? d * widen(x_c.e[i]) : 0.f;
-            }
-            #pragma unroll
-            for (int i = 0; i < BN; ++i) {
-                s_b[w][te][bn0 + i] = in ? widen(b_n.e[i]) : 0.f;
-                s_c[w][te][bn0 + i] = widen(c_n.e[i]);
-            }
+    auto store_y = [&](int t0, const float* v) {
+        const rsrc_t r = buf_rsrc(yp, (max(0, min(g.T - t0, ROUND)) * int(yrow)) & ykeep);
+        if (g.y_bf16) buf_store<bf16_t, E, VEC>(r, eoff * 2, v, ne);
+        else buf_store<float, E, true>(r, eoff * 4, v, ne);
+        yp += ROUND * yrow;
+    };
+    auto checkpoint = [&](int t, const float* v) {
+        #pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            if (ch_in && n0 + i < g.N) g.ck[((b * g.nck + t / SSM_CHECKPOINT_TOKENS) * g.C + c0 + ch) * g.N + n0 + i] = v[i];
+    };
+    // Step sizes and products d x of a round into LDS; a padded token has d = 0: it leaves the state as it is.
+    const uint32_t soft = g.softplus ? ~0u : 0u;
+    const float no_z = g.z ? 0.f : 1.f;   // the gate's factor without z
+    auto stage = [&](int t0) {
+        const bool in = t0 + w * TW + te < len;
+        const uint32_t keep = in ? ~0u : 0u;
+        #pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const float v = nx.dt.get(i) + bias[i];
+            const float d = __uint_as_float(__float_as_uint(bit_select(soft, softplusf_(v), v)) & keep);
+            s_d[w][e0 + i][te] = d;
+            s_u[w][e0 + i][te] = d * nx.x.get(i);
         }
-        if (t0 + TW * WT < len) load(t0 + TW * WT);
+    };
+    load();
+    int par = 0;
+    for (int t0 = 0; t0 < len; t0 += ROUND) {
+        const auto x_c = nx.x, z_c = nx.z;
+        const int tw = t0 + w * TW;
+        stage(t0);
+        float Bv[NPL], Cv[NPL];
+        #pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            Bv[i] = nx.b.get(i);
+            Cv[i] = nx.c.get(i);
+        }
+        load();
         wave_sync();
 
-        float a[WT > 1 ? TW : 1][NPL];
+        // The wave's tokens from a state: decay(token, state, d) and input(token, state, u).
+        auto run = [&](float* hs, auto&& decay, auto&& input) {
+            static_for<TW / 4>([&](auto t4) {
+                f32x4 d4, u4, y;
+                float hh[4][NPL];
+                if constexpr (WT == 1) {
+                    d4 = *reinterpret_cast<const f32x4*>(&s_d[w][ch][t4 * 4]);
+                    u4 = *reinterpret_cast<const f32x4*>(&s_u[w][ch][t4 * 4]);
+                }
+                static_for<4>([&](auto j_) {
+                    constexpr int j = j_, tt = t4 * 4 + j;
+                    #pragma unroll
+                    for (int i = 0; i < NPL; ++i) {
+                        hh[j][i] = fmaf(decay(tt, i, d4[j]), hs[i], input(j_, t4, i, u4[j]));
+                        hs[i] = hh[j][i];
+                    }
+                });
+                row_dot4<t4 * 4, NPL>(Cv, hh, y);
+                *reinterpret_cast<f32x4*>(&s_y[w][q][ch][t4 * 4]) = y;
+            });
+        };
         if constexpr (WT > 1) {
-            float hl[NPL] = {}, ds = 0.f;
-            #pragma unroll
-            for (int t4 = 0; t4 < TW; t4 += 4) {
-                const f32x4 d4 = *reinterpret_cast<const f32x4*>(&s_d[w][ch][t4]);
-                const f32x4 u4 = *reinterpret_cast<const f32x4*>(&s_u[w][ch][t4]);
-                #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const Pack<float, NPL> Bv = *reinterpret_cast<const Pack<float, NPL>*>(&s_b[w][t4 + j][q * NPL]);
+            float a[TW][NPL], in_[TW][NPL], hl[NPL] = {}, ds = 0.f;
+            static_for<TW / 4>([&](auto t4) {
+                const f32x4 d4 = *reinterpret_cast<const f32x4*>(&s_d[w][ch][t4 * 4]);
+                const f32x4 u4 = *reinterpret_cast<const f32x4*>(&s_u[w][ch][t4 * 4]);
+                static_for<4>([&](auto j_) {
+                    constexpr int j = j_, tt = t4 * 4 + j;
                     ds += d4[j];
                     #pragma unroll
                     for (int i = 0; i < NPL; ++i) {
-                        a[t4 + j][i] = __builtin_amdgcn_exp2f(d4[j] * A2[i]);
-                        hl[i] = fmaf(a[t4 + j][i], hl[i], u4[j] * Bv.e[i]);
+                        a[tt][i] = __builtin_amdgcn_exp2f(d4[j] * A2[i]);
+                        in_[tt][i] = u4[j] * row_lane<tt>(Bv[i]);
+                        hl[i] = fmaf(a[tt][i], hl[i], in_[tt][i]);
                     }
-                }
-            }
-            Pack<float, NPL> P, H;
+                });
+            });
             #pragma unroll
             for (int i = 0; i < NPL; ++i) {
-                P.e[i] = __builtin_amdgcn_exp2f(ds * A2[i]);
-                H.e[i] = hl[i];
+                s_p[par][w][i][lane] = __builtin_amdgcn_exp2f(ds * A2[i]);
+                s_h[par][w][i][lane] = hl[i];
             }
-            *reinterpret_cast<Pack<float, NPL>*>(&s_p[par][w][lane * NPL]) = P;
-            *reinterpret_cast<Pack<float, NPL>*>(&s_h[par][w][lane * NPL]) = H;
             __syncthreads();
-            float hin[NPL];
+            float hc[NPL];   // the state before this wave's tokens; h goes on to the state after the round
             #pragma unroll
             for (int v = 0; v < WT; ++v) {
                 if (v == w) {
                     #pragma unroll
-                    for (int i = 0; i < NPL; ++i) hin[i] = h[i];
+                    for (int i = 0; i < NPL; ++i) hc[i] = h[i];
                 }
-                const Pack<float, NPL> Pv = *reinterpret_cast<const Pack<float, NPL>*>(&s_p[par][v][lane * NPL]);
-                const Pack<float, NPL> Hv = *reinterpret_cast<const Pack<float, NPL>*>(&s_h[par][v][lane * NPL]);
                 #pragma unroll
-                for (int i = 0; i < NPL; ++i) h[i] = fmaf(Pv.e[i], h[i], Hv.e[i]);
+                for (int i = 0; i < NPL; ++i) h[i] = fmaf(s_p[par][v][i][lane], h[i], s_h[par][v][i][lane]);
             }
-            par ^= 1;
-            // h: the state after the round; hc: this wave's own
-            float hc[NPL];
-            #pragma unroll
-            for (int i = 0; i < NPL; ++i) hc[i] = hin[i];
-            const int tw = t0 + w * TW;
-            if (g.ck && tw % SSM_CHECKPOINT_TOKENS == 0 && tw < g.T) {
-                #pragma unroll
-                for (int i = 0; i < NPL; ++i)
-                    if (ch_in && q * NPL + i < g.N)
-                        g.ck[((b * g.nck + tw / SSM_CHECKPOINT_TOKENS) * g.C + c0 + ch) * g.N + q * NPL + i] = hc[i];
-            }
-            #pragma unroll
-            for (int tg = 0; tg < TW; tg += LPC) {
-                float y[LPC];
-                #pragma unroll
-                for (int j = 0; j < LPC; ++j) {
-                    const float u = s_u[w][ch][tg + j];
-                    const Pack<float, NPL> Bv = *reinterpret_cast<const Pack<float, NPL>*>(&s_b[w][tg + j][q * NPL]);
-                    const Pack<float, NPL> Cv = *reinterpret_cast<const Pack<float, NPL>*>(&s_c[w][tg + j][q * NPL]);
-                    y[j] = 0.f;
-                    #pragma unroll
-                    for (int i = 0; i < NPL; ++i) {
-                        hc[i] = fmaf(a[tg + j][i], hc[i], u * Bv.e[i]);
-                        y[j] = fmaf(Cv.e[i], hc[i], y[j]);
-                    }
-                }
-                s_d[w][ch][tg + q] = sum_transposed<LPC>(y, lane);
-            }
+            if (g.ck && tw % SSM_CHECKPOINT_TOKENS == 0 && tw < g.T) checkpoint(tw, hc);
+            run(hc, [&](int tt, int i, float) { return a[tt][i]; }, [&](auto j, auto t4, int i, float) { return in_[t4 * 4 + j][i]; });
         } else {
-            if (g.ck && t0 % SSM_CHECKPOINT_TOKENS == 0) {
-                #pragma unroll
-                for (int i = 0; i < NPL; ++i)
-                    if (ch_in && q * NPL + i < g.N)
-                        g.ck[((b * g.nck + t0 / SSM_CHECKPOINT_TOKENS) * g.C + c0 + ch) * g.N + q * NPL + i] = h[i];
-            }
-            #pragma unroll
-            for (int tg = 0; tg < TW; tg += LPC) {
-                float y[LPC];
-                #pragma unroll
-                for (int j = 0; j < LPC; ++j) {
-                    const float d = s_d[w][ch][tg + j], u = s_u[w][ch][tg + j];
-                    const Pack<float, NPL> Bv = *reinterpret_cast<const Pack<float, NPL>*>(&s_b[w][tg + j][q * NPL]);
-                    const Pack<float, NPL> Cv = *reinterpret_cast<const Pack<float, NPL>*>(&s_c[w][tg + j][q * NPL]);
-                    y[j] = 0.f;
-                    #pragma unroll
-                    for (int i = 0; i < NPL; ++i) {
-                        h[i] = fmaf(__builtin_amdgcn_exp2f(d * A2[i]), h[i], u * Bv.e[i]);
-                        y[j] = fmaf(Cv.e[i], h[i], y[j]);
-                    }
-                }
-                const float ys = sum_transposed<LPC>(y, lane);
-                wave_sync();   // every lane has read these tokens' d
-                s_d[w][ch][tg + q] = ys;
-            }
+            if (g.ck && t0 % SSM_CHECKPOINT_TOKENS == 0) checkpoint(t0, h);
+            run(h, [&](int, int i, float dd) { return __builtin_amdgcn_exp2f(dd * A2[i]); },
+                [&](auto j, auto t4, int i, float uu) { return uu * row_lane<t4 * 4 + j>(Bv[i]); });
         }
+        par ^= 1;
         wave_sync();
         float out[E];
         #pragma unroll
         for (int i = 0; i < E; ++i) {
-            float y = fmaf(Dv[i], widen(x_c.e[i]), s_d[w][e0 + i][te]);
-            if (g.z) {
-                const float z = widen(z_c.e[i]);
-                y *= z * sigmoidf_(z);
-            }
-            out[i] = in ? y : 0.f;
+            const float y = fmaf(Dv[i], x_c.get(i), (s_y[w][0][e0 + i][te] + s_y[w][1][e0 + i][te]) + (s_y[w][2][e0 + i][te] + s_y[w][3][e0 + i][te]));
+            const float z = z_c.get(i);
+            out[i] = y * fmaf(z, sigmoidf_(z), no_z);
         }
-        if (t < g.T && g.y) st_pack_as<E>(g.y, (b * g.T + t) * g.C + c0 + e0, g.y_bf16, out, whole, ne);
+        store_y(t0, out);
         wave_sync();   // the LDS rows are free again
     }
     // Padding after the last round: y = 0, and the state as it is at the checkpoints there.
-    const int done = (len + TW * WT - 1) / (TW * WT) * (TW * WT);
+    const int done = (len + ROUND - 1) / ROUND * ROUND;
     const float zero[E] = {};
-    for (int t = done + w * TW + te; t < g.T && g.y; t += TW * WT)
-        st_pack_as<E>(g.y, (b * g.T + t) * g.C + c0 + e0, g.y_bf16, zero, whole, ne);
-    #pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-        if (!ch_in || q * NPL + i >= g.N || w != 0) continue;
-        if (g.ck)
-            for (int k = (done + SSM_CHECKPOINT_TOKENS - 1) / SSM_CHECKPOINT_TOKENS; k < g.nck; ++k)
-                g.ck[((b * g.nck + k) * g.C + c0 + ch) * g.N + q * NPL + i] = h[i];
-        if (g.s1) g.s1[srow + i] = h[i];
+    for (int t0 = done; t0 < g.T; t0 += ROUND) store_y(t0, zero);
+    if (w != 0) return;
+    if (g.ck)
+        for (int k = (done + SSM_CHECKPOINT_TOKENS - 1) / SSM_CHECKPOINT_TOKENS; k < g.nck; ++k)
+            checkpoint(k * SSM_CHECKPOINT_TOKENS, h);
+    if (g.s1) {
+        #pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            if (ch_in && n0 + i < g.N) g.s1[srow + i] = h[i];
     }
 }
 
-template <typename Tin, int LPC, int NPL>
+template <typename Tin, int NPL, bool VEC>
 hipError_t launch_scan_wt(const SsmParams& p, hipStream_t stream) {
-    constexpr int CH = 64 / LPC;
     const int Cg = p.C / p.G;
     const int64_t blocks = int64_t(p.B) * p.G * ((Cg + CH - 1) / CH);
     const dim3 grid{unsigned(blocks)};
     // Waves over the tokens while the chip has room for them.
-    const int wt = blocks >= 2048 || p.T <= TW ? 1 : blocks >= 512 || p.T <= 4 * TW ? 4 : 8;
-    if (wt == 1) hipLaunchKernelGGL((ssm_scan_kernel<Tin, LPC, NPL, 1>), grid, dim3(64), 0, stream, p);
-    else if (wt == 4) hipLaunchKernelGGL((ssm_scan_kernel<Tin, LPC, NPL, 4>), grid, dim3(256), 0, stream, p);
-    else hipLaunchKernelGGL((ssm_scan_kernel<Tin, LPC, NPL, 8>), grid, dim3(512), 0, stream, p);
+    const int wt = NPL > 4 || blocks >= 2048 || p.T <= TW ? 1 : blocks >= 512 || p.T <= 4 * TW ? 4 : 8;
+    if (wt == 1) hipLaunchKernelGGL((ssm_scan_kernel<Tin, NPL, 1, VEC>), grid, dim3(64), 0, stream, p);
+    else if constexpr (NPL <= 4) {
+        if (wt == 4) hipLaunchKernelGGL((ssm_scan_kernel<Tin, NPL, 4, VEC>), grid, dim3(256), 0, stream, p);
+        else hipLaunchKernelGGL((ssm_scan_kernel<Tin, NPL, 8, VEC>), grid, dim3(512), 0, stream, p);
+    }
     return hipGetLastError();
+}
+template <typename Tin, int NPL>
+hipError_t launch_scan_n(const SsmParams& p, hipStream_t stream) {
+    const bool vec = p.N % NPL == 0 && (!p.in_bf16 || (p.C % 2 == 0 && p.C / p.G % 2 == 0 && p.N % 2 == 0));
+    return vec ? launch_scan_wt<Tin, NPL, true>(p, stream) : launch_scan_wt<Tin, NPL, false>(p, stream);
 }
 
 template <typename Tin>
-hipError_t launch_scan_in(SsmParams p, hipStream_t stream) {
-    const int lpc = p.N <= 8 ? 2 : p.N <= 16 ? 4 : p.N <= 32 ? 8 : 16;
-    const int E = 16 / lpc;
-    p.vec_c = p.C % E == 0 && (p.C / p.G) % E == 0;
-    p.vec_n = p.N == lpc * 4;
-    switch (lpc) {
-        case 2: return launch_scan_wt<Tin, 2, 4>(p, stream);
-        case 4: return launch_scan_wt<Tin, 4, 4>(p, stream);
-        case 8: return launch_scan_wt<Tin, 8, 4>(p, stream);
-        default: return launch_scan_wt<Tin, 16, 4>(p, stream);
-    }
+hipError_t launch_scan_in(const SsmParams& p, hipStream_t stream) {
+    if (p.N <= 4) return launch_scan_n<Tin, 1>(p, stream);
+    if (p.N <= 8) return launch_scan_n<Tin, 2>(p, stream);
+    if (p.N <= 16) return launch_scan_n<Tin, 4>(p, stream);
+    if (p.N <= 32) return launch_scan_n<Tin, 8>(p, stream);
+    return launch_scan_n<Tin, 16>(p, stream);
 }
 
 // One token per row.  LN lanes to a channel, 4 states each: a wave's loads and
-// stores of the states are 1 KiB runs.  A workgroup has 64 / LN channels of each
-// of its 4 waves, and RB rows one after another (A stays in registers).
+// stores of the states are 1 KiB runs.  A workgroup has 256 / LN channels of R
+// rows, whose states are in flight together; A is loaded once for them.
 constexpr int SB = 256;
 
-template <typename Tin, int LN>
+template <typename Tin, int LN, int R>
 __global__ __launch_bounds__(SB) void ssm_step_kernel(SsmParams g) {
     constexpr int CHB = SB / LN;
-    const int ch = threadIdx.x / LN, q = threadIdx.x % LN;
+    const int q = threadIdx.x % LN;
     const int ncb = (g.C + CHB - 1) / CHB;
-    const int64_t item = blockIdx.x;
-    const int c = int(item % ncb) * CHB + ch;
-    const int b = int(item / ncb);
+    const int c = int(blockIdx.x % ncb) * CHB + threadIdx.x / LN, b0 = int(blockIdx.x / ncb) * R;
     const bool in = c < g.C;
+    const int cc = in ? c : 0, grp = cc / (g.C / g.G);
     const int n0 = q * 4, nn = in ? g.N - n0 : 0;
     const bool whole = g.vec_n && nn >= 4;
-    const int slot = g.index ? g.index[b] : b;
-    bool mine = slot >= 0 && slot < g.S;
-    float hv[4] = {};
-    const int64_t sr = (int64_t(slot) * g.C + c) * g.N + n0;
-    if (mine && nn > 0) ld_pack_as<4>(g.s0, sr, false, hv, whole, nn);
-    if (g.index && mine) mine = first_of_slot(g.index, b, slot, SB);
-    const int64_t e = int64_t(b) * g.C + (in ? c : 0);
-    const int grp = (in ? c : 0) / (g.C / g.G);
-    const int64_t r = (int64_t(b) * g.G + grp) * g.N + n0;
-    float Av[4], Bv[4], Cv[4];
-    ld_pack_as<4>(g.A, int64_t(in ? c : 0) * g.N + n0, false, Av, whole, nn);
-    ld_pack_as<4>(g.Bm, r, sizeof(Tin) == 2, Bv, whole, nn);
-    ld_pack_as<4>(g.Cm, r, sizeof(Tin) == 2, Cv, whole, nn);
-    const float x = widen(static_cast<const Tin*>(g.x)[e]);
-    float d = widen(static_cast<const Tin*>(g.dt)[e]) + (g.dt_bias && in ? g.dt_bias[c] : 0.f);
-    if (g.softplus) d = softplusf_(d);
-    float y = 0.f;
+    int slot[R];
+    bool mine[R];
+    float hv[R][4] = {}, Bv[R][4], Cv[R][4], x[R], d[R], z[R], Av[4];
     #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        hv[i] = fmaf(__builtin_amdgcn_exp2f(d * (Av[i] * kLog2e)), hv[i], d * x * Bv[i]);
-        y = fmaf(Cv[i], hv[i], y);
+    for (int r = 0; r < R; ++r) {
+        const int b = min(b0 + r, g.B - 1);
+        slot[r] = g.index ? g.index[b] : b;
+        mine[r] = b0 + r < g.B && slot[r] >= 0 && slot[r] < g.S;
+        if (mine[r] && nn > 0) ld_pack_as<4>(g.s0, (int64_t(slot[r]) * g.C + c) * g.N + n0, false, hv[r], whole, nn);
+        const int64_t e = int64_t(b) * g.C + cc, v = (int64_t(b) * g.G + grp) * g.N + n0;
+        ld_pack_as<4>(g.Bm, v, sizeof(Tin) == 2, Bv[r], whole, nn);
+        ld_pack_as<4>(g.Cm, v, sizeof(Tin) == 2, Cv[r], whole, nn);
+        x[r] = widen(static_cast<const Tin*>(g.x)[e]);
+        d[r] = widen(static_cast<const Tin*>(g.dt)[e]);
+        z[r] = g.z ? widen(static_cast<const Tin*>(g.z)[e]) : 0.f;
     }
-    if (mine && nn > 0) st_pack<4>(g.s1 + sr, hv, whole, nn);
-    if constexpr (LN >= 2) y += dpp<kDppQuadXor1>(y);
-    if constexpr (LN >= 4) y += dpp<kDppQuadXor2>(y);
-    if constexpr (LN >= 8) y += dpp<kDppRowHalfMirror>(y);
-    if constexpr (LN >= 16) y += dpp<kDppRowMirror>(y);
-    if (!in || q != 0) return;
-    if (g.D) y = fmaf(g.D[c], x, y);
-    if (g.z) {
-        const float z = widen(static_cast<const Tin*>(g.z)[e]);
-        y *= z * sigmoidf_(z);
+    ld_pack_as<4>(g.A, int64_t(cc) * g.N + n0, false, Av, whole, nn);
+    const float bias = g.dt_bias ? g.dt_bias[cc] : 0.f, Dv = g.D ? g.D[cc] : 0.f;
+    if (g.index) first_of_slots<R>(g.index, b0, slot, mine, SB);
+    #pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const float v = d[r] + bias, dd = g.softplus ? softplusf_(v) : v;
+        float y = 0.f;
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            hv[r][i] = fmaf(__builtin_amdgcn_exp2f(dd * (Av[i] * kLog2e)), hv[r][i], dd * x[r] * Bv[r][i]);
+            y = fmaf(Cv[r][i], hv[r][i], y);
+        }
+        if (mine[r] && nn > 0) st_pack<4>(g.s1 + (int64_t(slot[r]) * g.C + c) * g.N + n0, hv[r], whole, nn);
+        if constexpr (LN >= 2) y += dpp<kDppQuadXor1>(y);
+        if constexpr (LN >= 4) y += dpp<kDppQuadXor2>(y);
+        if constexpr (LN >= 8) y += dpp<kDppRowHalfMirror>(y);
+        if constexpr (LN >= 16) y += dpp<kDppRowMirror>(y);
+        y = fmaf(Dv, x[r], y);
+        if (g.z) y *= z[r] * sigmoidf_(z[r]);
+        y = mine[r] ? y : 0.f;
+        if (in && q == 0 && b0 + r < g.B) st_pack_as<1>(g.y, int64_t(b0 + r) * g.C + c, g.y_bf16, &y, true, 1);
     }
-    y = mine ? y : 0.f;
-    st_pack_as<1>(g.y, e, g.y_bf16, &y, true, 1);
+}
+
+template <typename Tin, int LN>
+hipError_t launch_step_ln(const SsmParams& p, hipStream_t stream) {
+    const int64_t ncb = (p.C + SB / LN - 1) / (SB / LN);
+    // four rows to a workgroup where that leaves four workgroups to a compute unit
+    if (ncb * p.B >= 4096) hipLaunchKernelGGL((ssm_step_kernel<Tin, LN, 4>), dim3(unsigned(ncb * ((p.B + 3) / 4))), dim3(SB), 0, stream, p);
+    else hipLaunchKernelGGL((ssm_step_kernel<Tin, LN, 1>), dim3(unsigned(ncb * p.B)), dim3(SB), 0, stream, p);
+    return hipGetLastError();
 }
 
 template <typename Tin>
 hipError_t launch_step_in(SsmParams p, hipStream_t stream) {
-    const int ln = p.N <= 4 ? 1 : p.N <= 8 ? 2 : p.N <= 16 ? 4 : p.N <= 32 ? 8 : 16;
     p.vec_n = p.N % 4 == 0;
-    const int chb = SB / ln;
-    const dim3 grid{unsigned(int64_t(p.B) * ((p.C + chb - 1) / chb))}, block{SB};
-    switch (ln) {
-        case 1: hipLaunchKernelGGL((ssm_step_kernel<Tin, 1>), grid, block, 0, stream, p); break;
-        case 2: hipLaunchKernelGGL((ssm_step_kernel<Tin, 2>), grid, block, 0, stream, p); break;
-        case 4: hipLaunchKernelGGL((ssm_step_kernel<Tin, 4>), grid, block, 0, stream, p); break;
-        case 8: hipLaunchKernelGGL((ssm_step_kernel<Tin, 8>), grid, block, 0, stream, p); break;
-        default: hipLaunchKernelGGL((ssm_step_kernel<Tin, 16>), grid, block, 0, stream, p); break;
-    }
-    return hipGetLastError();
+    if (p.N <= 4) return launch_step_ln<Tin, 1>(p, stream);
+    if (p.N <= 8) return launch_step_ln<Tin, 2>(p, stream);
+    if (p.N <= 16) return launch_step_ln<Tin, 4>(p, stream);
+    if (p.N <= 32) return launch_step_ln<Tin, 8>(p, stream);
+    return launch_step_ln<Tin, 16>(p, stream);
 }
 
 }  // namespace

@@ -75,19 +75,24 @@ def _inputs(x, dt, A, Bm, Cm, D, dt_bias, z, lengths, step):
     if A.dim() != 2 or A.shape[0] != C:
         raise ValueError(f"A must be [C, N] with C = {C}, got {tuple(A.shape)}")
     N = A.shape[1]
-    M.check("A", A, A.shape, f32, dev)
     if Bm.dim() != len(row) + 1:
         raise ValueError(f"Bm must be {'[B, G, N]' if step else '[B, T, G, N]'}, got {tuple(Bm.shape)}")
     G = Bm.shape[-2]
     if G == 0 or C % G:
         raise ValueError(f"{C} channels are not a multiple of G = {G}")
-    M.check("dt", dt, row, x.dtype, dev)
-    M.check("Bm", Bm, row[:-1] + (G, N), x.dtype, dev)
-    M.check("Cm", Cm, Bm.shape, x.dtype, dev)
-    M.check_if("z", z, row, x.dtype, dev)
-    M.check_if("D", D, (C,), f32, dev)
-    M.check_if("dt_bias", dt_bias, (C,), f32, dev)
-    M.check_if("lengths", lengths, (row[0],), torch.int32, dev)
+    dtype, vec, check = x.dtype, row[:-1] + (G, N), M.check
+    check("A", A, (C, N), f32, dev)
+    check("dt", dt, row, dtype, dev)
+    check("Bm", Bm, vec, dtype, dev)
+    check("Cm", Cm, vec, dtype, dev)
+    if z is not None:
+        check("z", z, row, dtype, dev)
+    if D is not None:
+        check("D", D, (C,), f32, dev)
+    if dt_bias is not None:
+        check("dt_bias", dt_bias, (C,), f32, dev)
+    if lengths is not None:
+        check("lengths", lengths, (row[0],), torch.int32, dev)
     return dev, row[0], 1 if step else row[1], C, N, G
 
 
