@@ -55,10 +55,10 @@ typedef struct ssm_desc {
 } ssm_desc;
 
 /* Tokens from one checkpointed state to the next. */
-#define SSM_CHECKPOINT_TOKENS 64
+#define SSM_CHECKPOINT_TOKENS 32
 
-/* Bytes of the states that ssm_forward can leave for ssm_backward: [B][ceil(T / 64)][C][N]
- * fp32, the state before every 64th token.  A negative wkv7_status if the
+/* Bytes of the states that ssm_forward can leave for ssm_backward: [B][ceil(T / 32)][C][N]
+ * fp32, the state before every 32nd token.  A negative wkv7_status if the
  * descriptor is invalid.  Host only. */
 int64_t ssm_checkpoint_bytes(const ssm_desc* desc);
 

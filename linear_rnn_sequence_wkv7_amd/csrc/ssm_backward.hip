@@ -8,70 +8,34 @@
 //   dx_t = du_t d_t + do_t D,   ddt_t = dd_t softplus'(dt_t + dt_bias),
 //   dz_t = dy_t y'_t silu'(z_t)   with y' the output before the gate
 //
-// The lanes are the forward's (ssm_scan.hip): LPC to a channel with NPL states
-// each, the WT waves of a workgroup on consecutive runs of 16 tokens of the same
-// channels.  The workgroup goes from its last 16 WT tokens to its first.  A round
-// computes the decays of its tokens (kept in registers), each wave's state from
-// zero and its gradient from zero, exchanges both and the wave's decay through
-// LDS (one barrier, double buffered), so that every wave has its incoming state,
-// starting from the checkpoint of the round, and its incoming gradient, starting
-// from the later round's; runs the states forward once more, into registers, and
-// then the gradients backward.
+// A wave has 16 channels, 16 tokens and 8 states: lane (q, c) of its 4 rows of 16
+// lanes has states 2 q, 2 q + 1 of channel c, and holds B and C of token c for them,
+// which an operand modifier hands to the whole row when their token comes.  WS waves
+// share the states of a token run and its elements (step sizes, products, gates, which
+// each computes a part of, through LDS); the WT runs of a workgroup follow one another.
+// The workgroup goes from its last 16 WT tokens to its first.  A round computes the
+// decays of its tokens (kept in registers), each run's state from zero and its
+// gradient from zero, and exchanges both with the run's decay through LDS, so that
+// every run has its incoming state, from the checkpoint of the round, and its incoming
+// gradient, from the later round's; it runs the states forward once more, into
+// registers, and then the gradients backward.  Two states a lane keep it within 128
+// registers, which is what lets four waves share a SIMD: with four states a lane and
+// two waves the same work issued a fifth more slowly.
 //
-// Sums over a channel's lanes and over the channels of a wave are transposing
-// butterflies: a step halves the values that a lane holds while it doubles the
-// lanes summed.  dB and dC of a wave's channels go to the workspace, one row for
-// each block of channels, and a second kernel adds the rows; no atomics, so the
-// order is fixed.  dA, dD and ddt_bias are kept in registers over the whole
-// sequence and added over the batch by a third kernel.
+// Sums over the rows and over a row's channels are transposing butterflies: a step
+// halves the values that a lane holds while it doubles the lanes summed.  dB and dC of
+// a wave's channels go to the workspace, one row for each block of channels, and a
+// second kernel adds the rows; no atomics, so the order is fixed.  dA, dD and ddt_bias
+// are kept in registers over the whole sequence and added over the batch by a third.
 #include "seq_device.h"
 #include "seq_internal.h"
 
 namespace wkv7 {
 namespace {
 
-constexpr int TW = 16, TP = 20;
-constexpr int PT = 4, PARTS = TW / PT;   // tokens whose states and decays are in registers at once
+constexpr int TW = 16, CH = 16, TP = 20, NPL = 2;
+constexpr int PT = 8;   // tokens whose states are in registers at once
 constexpr float kLn2 = 0.6931471805599453f;
-
-// The value of lane ^ M.
-template <int M>
-__device__ __forceinline__ float from_xor(float x) {
-    if constexpr (M == 1) return dpp<kDppQuadXor1>(x);
-    if constexpr (M == 2) return dpp<kDppQuadXor2>(x);
-    if constexpr (M == 8) return dpp<0x128>(x);   // row_ror:8
-    // 4: down for the odd banks of four lanes, up for the even ones
-    const int v = __float_as_int(x);
-    const int t = __builtin_amdgcn_update_dpp(v, v, 0x114, 0xF, 0xA, false);   // row_shr:4
-    return __int_as_float(__builtin_amdgcn_update_dpp(t, v, 0x104, 0xF, 0x5, false));   // row_shl:4
-}
-// lo where the lane's bit M is 0, hi where it is 1, each summed over the pair of lanes.
-template <int M>
-__device__ __forceinline__ float halve(float lo, float hi, int lane) {
-    if constexpr (M == 32) {
-        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(lo), __float_as_uint(hi), false, false);
-        return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-    } else if constexpr (M == 16) {
-        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(lo), __float_as_uint(hi), false, false);
-        return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-    } else {
-        const bool b = lane & M;
-        return (b ? hi : lo) + from_xor<M>(b ? lo : hi);
-    }
-}
-// Sum over a channel's lanes of 4 tokens, into LDS (row of the channel, from the first token).
-template <int LPC>
-__device__ __forceinline__ void sum_lanes_to(float* row, float* y, int lane) {
-    #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        if constexpr (LPC >= 16) y[k] += dpp<kDppRowMirror>(y[k]);
-        if constexpr (LPC >= 8) y[k] += dpp<kDppRowHalfMirror>(y[k]);
-    }
-    const float s = halve<1>(halve<2>(y[0], y[2], lane), halve<2>(y[1], y[3], lane), lane);
-    if (lane % LPC < 4) row[lane & 3] = s;
-}
-// Values read from LDS are not to be kept in registers across this point: read them again.
-__device__ __forceinline__ void forget_lds() { wave_sync(); }
 
 struct BwdWs {
     float* bc;    // [ncb][B][T][G][2][N]: dB and dC of each block of channels
@@ -79,159 +43,208 @@ struct BwdWs {
     const float* ck;
 };
 
-template <typename Tin, int LPC, int NPL, int WT>
-__global__ __launch_bounds__(64 * WT, 2) void ssm_backward_kernel(SsmParams g, BwdWs ws) {
-    constexpr int CH = 64 / LPC, E = CH / 4, NP = LPC * NPL, BN = NP / 4, ROUND = TW * WT;
-    constexpr int NV = 4 * 2 * NPL;   // values of dB and dC of 4 tokens in a lane
-    __shared__ float s_d[WT][CH][TP], s_u[WT][CH][TP], s_o[WT][CH][TP];
-    __shared__ float s_b[WT][TW][NP], s_c[WT][TW][NP];
-    __shared__ float s_keep[WT][5][E][64];   // a lane's own x, d, softplus', do and dz factor, while it computes
-    __shared__ float s_p[2][WT][64 * NPL], s_h[2][WT][64 * NPL], s_g[2][WT][64 * NPL];
-    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t item = xcd_order(blockIdx.x, gridDim.x);
-    const int Cg = g.C / g.G, ncb = (Cg + CH - 1) / CH;
+// One token backward, for the two states of a lane.  In: e, the gradient of the state as later
+// tokens left it.  e += C do; y = C . h and us = B . e are the lane's parts of the readout and of
+// the input's gradient.  B and C of lane T of the row, by operand modifiers (the compiler folds
+// them into products only).
+template <int T>
+__device__ __forceinline__ void token_back(float (&e)[2], const float* C, const float* B, float o, const float* h, float& y, float& us) {
+#define WKV7_BC " row_newbcast:%c[t] row_mask:0xf bank_mask:0xf\n"
+    asm("s_nop 1\n"
+        "v_fmac_f32_dpp %0, %4, %8" WKV7_BC "v_fmac_f32_dpp %1, %5, %8" WKV7_BC
+        "v_mul_f32_dpp %2, %4, %9" WKV7_BC "v_mul_f32_dpp %3, %6, %0" WKV7_BC
+        "v_fmac_f32_dpp %2, %5, %10" WKV7_BC "v_fmac_f32_dpp %3, %7, %1" WKV7_BC
+        : "+&v"(e[0]), "+&v"(e[1]), "=&v"(y), "=&v"(us)
+        : "v"(C[0]), "v"(C[1]), "v"(B[0]), "v"(B[1]), "v"(o), "v"(h[0]), "v"(h[1]), [t] "n"(T));
+#undef WKV7_BC
+}
+
+// lo in the lanes whose bit 3 (2) is 0, hi in the others, each summed over the lane and its mirror
+// in 16 (8): the second sum is written to the upper banks of four lanes only.
+template <int M>
+__device__ __forceinline__ void halve_banks(float& a0, float b0, float& a1, float b1) {
+    float r0, r1;
+    if constexpr (M == 8)
+        asm("s_nop 1\nv_add_f32_dpp %0, %2, %2 row_mirror row_mask:0xf bank_mask:0xf\nv_add_f32_dpp %1, %4, %4 row_mirror row_mask:0xf bank_mask:0xf\n"
+            "v_add_f32_dpp %0, %3, %3 row_mirror row_mask:0xf bank_mask:0xc\nv_add_f32_dpp %1, %5, %5 row_mirror row_mask:0xf bank_mask:0xc"
+            : "=&v"(r0), "=&v"(r1) : "v"(a0), "v"(b0), "v"(a1), "v"(b1));
+    else
+        asm("s_nop 1\nv_add_f32_dpp %0, %2, %2 row_half_mirror row_mask:0xf bank_mask:0xf\nv_add_f32_dpp %1, %4, %4 row_half_mirror row_mask:0xf bank_mask:0xf\n"
+            "v_add_f32_dpp %0, %3, %3 row_half_mirror row_mask:0xf bank_mask:0xa\nv_add_f32_dpp %1, %5, %5 row_half_mirror row_mask:0xf bank_mask:0xa"
+            : "=&v"(r0), "=&v"(r1) : "v"(a0), "v"(b0), "v"(a1), "v"(b1));
+    a0 = r0;
+    a1 = r1;
+}
+
+// x, by a way that the compiler does not see through: what is computed from it is computed where it
+// is used, and not kept in registers over the loop.
+__device__ __forceinline__ int opaque(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// Waves to a SIMD that the registers are held to: 4 where they fit, or have to because the
+// workgroup has 16 waves.
+constexpr int waves_of(int WS, int WT, bool vec) { return WS * WT >= 16 || (vec && WT > 1 && WS * WT >= 8) ? 4 : 2; }
+
+// WS waves with 8 states each; WT runs of 16 tokens.  VEC: rows of channels and of states start on
+// 4 bytes, for each group too, and no lane has only one of its two states.
+template <typename Tin, typename Ty, int WS, int WT, bool VEC>
+__global__ __launch_bounds__(64 * WS * WT, waves_of(WS, WT, VEC)) void ssm_backward_kernel(SsmParams g, BwdWs ws) {
+    constexpr int ROUND = TW * WT, NP = 8 * WS, E = WS <= 2 ? 4 / WS : 1, ES = int(sizeof(Tin)), YS = int(sizeof(Ty));
+    __shared__ float s_d[WT][CH][TP], s_u[WT][CH][TP], s_o[WT][CH][TP], s_k[2][WT][CH][TP];   // d, d x, do; softplus', dz's factor
+    __shared__ float s_r[WT][WS][3][CH][TP];
+    __shared__ float s_x[3][WT][WS][NPL][64];      // decay, state and gradient of each run
+    __shared__ float s_bc[WT][TW][2][NP];
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int s = wv % WS, w = wv / WS;            // part of the states, run
+    const unsigned item = unsigned(xcd_order(blockIdx.x, gridDim.x));
+    const int Cg = g.C / g.G;
+    const unsigned ncb = (Cg + CH - 1) / CH;
     const int cb = int(item % ncb), grp = int(item / ncb % g.G);
     const int64_t b = item / ncb / g.G;
     const int c0 = grp * Cg + cb * CH, nc = min(CH, Cg - cb * CH);
-    const int len = seq_length(g.lengths, b, g.T);
+    const int len = __builtin_amdgcn_readfirstlane(seq_length(g.lengths, b, g.T));
 
-    const int ch = lane / LPC, q = lane % LPC;
-    const bool ch_in = ch < nc;
-    const int64_t srow = (b * g.C + c0 + ch) * g.N + q * NPL;
+    const int ch = lane & 15, q = lane >> 4, n0 = s * 8 + q * NPL;
+    const int64_t srow = (b * g.C + c0 + ch) * g.N + n0;
     float A2[NPL], gc[NPL], dA[NPL] = {};
     bool n_in[NPL];
     #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-        n_in[i] = ch_in && q * NPL + i < g.N;
-        A2[i] = n_in[i] ? g.A[int64_t(c0 + ch) * g.N + q * NPL + i] * kLog2e : 0.f;
+        n_in[i] = ch < nc && n0 + i < g.N;
+        A2[i] = n_in[i] ? g.A[int64_t(c0 + ch) * g.N + n0 + i] * kLog2e : 0.f;
         gc[i] = n_in[i] && g.ds1 ? g.ds1[srow + i] : 0.f;   // gradient of the state after the round
     }
-    const int te = lane >> 2, e0 = (lane & 3) * E, ne = nc - e0;
-    const bool whole = g.vec_c && ne >= E;
-    const int bn0 = (lane & 3) * BN, nb = g.N - bn0;
-    float bias[E], Dv[E], dD[E] = {}, dbias[E] = {};
-    #pragma unroll
-    for (int i = 0; i < E; ++i) {
-        bias[i] = g.dt_bias && i < ne ? g.dt_bias[c0 + e0 + i] : 0.f;
-        Dv[i] = g.D && i < ne ? g.D[c0 + e0 + i] : 0.f;
+    // A thread's elements: token te, channels e0 .. e0 + E of its run (WS = 8: the first half's threads).
+    const int idx = (s * 64 + lane) * E, te = idx >> 4 & 15, e0 = idx & 15, ne = idx < 256 ? nc - e0 : 0;
+    const bool el_in = ne > 0;
+    float dD[E] = {}, dbias[E] = {};
+    __shared__ float s_par[2][CH];   // dt_bias and D of the channels
+    if (threadIdx.x < 2 * CH) {
+        const float* p = threadIdx.x < CH ? g.dt_bias : g.D;
+        s_par[threadIdx.x >> 4][ch] = p && ch < nc ? p[c0 + ch] : 0.f;
     }
-    const Tin *xp = static_cast<const Tin*>(g.x), *dtp = static_cast<const Tin*>(g.dt), *zp = static_cast<const Tin*>(g.z);
-    const Tin *bp = static_cast<const Tin*>(g.Bm), *cp = static_cast<const Tin*>(g.Cm);
-    auto store = [&](void* p, int64_t e, const float* v) { st_pack<E>(static_cast<Tin*>(p) + e, v, whole, ne); };
+    __syncthreads();
+    const uint32_t soft = g.softplus ? ~0u : 0u;
+    const float no_z = g.z ? 0.f : 1.f;
+
+    // Rows of a round through descriptors that end with the sequence: a padded token's values are 0.
+    const int64_t erow = int64_t(g.C) * ES, vrow = int64_t(g.G) * g.N * ES, yrow = int64_t(g.C) * YS;
+    const uint32_t eoff = el_in ? uint32_t((w * TW + te) * g.C + c0 + e0) : 0u;
+    const uint32_t voff = n0 < g.N ? uint32_t((w * TW + ch) * g.G * g.N + grp * g.N + n0) * ES : 0xfffffff0u;
+    struct Inputs {
+        Raw<Tin, E, VEC> x, dt, z;
+        Raw<Ty, E, VEC> dy;
+        Raw<Tin, NPL, VEC> b, c;
+        Raw<float, NPL, VEC> h;
+    } nx;
+    auto load = [&](int t0) {
+        const int n = max(0, min(len - t0, ROUND));
+        const int64_t row = b * g.T + t0;
+        auto rows = [&](const void* p, int64_t width) { return buf_rsrc(static_cast<const char*>(p) + row * width, p ? n * width : 0); };
+        nx.dt.load(rows(g.dt, erow), eoff * ES, ne);
+        nx.x.load(rows(g.x, erow), eoff * ES, ne);
+        nx.z.load(rows(g.z, erow), eoff * ES, ne);
+        nx.dy.load(rows(g.dy, yrow), eoff * YS, ne);
+        nx.b.load(rows(g.Bm, vrow), voff, g.N - n0);
+        nx.c.load(rows(g.Cm, vrow), voff, g.N - n0);
+        const rsrc_t ck = buf_rsrc(ws.ck + ((b * g.nck + t0 / SSM_CHECKPOINT_TOKENS) * g.C + c0) * g.N, int64_t(nc) * g.N * 4);
+        nx.h.load(ck, n0 < g.N ? uint32_t(ch * g.N + n0) * 4 : 0xfffffff0u, g.N - n0);
+    };
+    auto store = [&](void* p, int t0, const float* v, uint32_t eoff, int ne) {
+        const int n = min(g.T - t0, ROUND);
+        buf_store<Tin, E, VEC>(buf_rsrc(static_cast<char*>(p) + (b * g.T + t0) * erow, n * erow), eoff * ES, v, ne);
+    };
 
     const int rounds = (len + ROUND - 1) / ROUND;
-    {   // padding after the last round
+    for (int t0 = rounds * ROUND; t0 < g.T; t0 += ROUND) {   // padding after the last round
         const float zero[E] = {};
-        for (int t = rounds * ROUND + w * TW + te; t < g.T; t += ROUND) {
-            const int64_t e = (b * g.T + t) * g.C + c0 + e0;
-            store(g.dx, e, zero);
-            store(g.ddt, e, zero);
-            if (g.z) store(g.dz, e, zero);
-        }
+        store(g.dx, t0, zero, eoff, ne);
+        store(g.ddt, t0, zero, eoff, ne);
+        if (g.z) store(g.dz, t0, zero, eoff, ne);
     }
-    int par = 0;
+    if (rounds > 0) load((rounds - 1) * ROUND);
     for (int rd = rounds - 1; rd >= 0; --rd) {
-        const int tw = rd * ROUND + w * TW, t = tw + te;
-        const bool in = t < len;
-        const int64_t row = b * g.T + min(t, g.T - 1), e = row * g.C + c0 + e0;
-        float hin[NPL];
-        {   // elements, and the round's checkpoint
-            const Pack<Tin, E> xr = ld_pack<E>(xp + e, whole, ne), dr = ld_pack<E>(dtp + e, whole, ne);
-            Pack<Tin, E> zr;
-            if (g.z) zr = ld_pack<E>(zp + e, whole, ne);
-            const int64_t r = (row * g.G + grp) * g.N + bn0;
-            const Pack<Tin, BN> br = ld_pack<BN>(bp + r, g.vec_n, nb), cr = ld_pack<BN>(cp + r, g.vec_n, nb);
-            float dyv[E];
-            ld_pack_as<E>(g.dy, e, g.y_bf16, dyv, whole, ne);
-            const float* ck = ws.ck + ((b * g.nck + rd * (ROUND < SSM_CHECKPOINT_TOKENS ? 1 : ROUND / SSM_CHECKPOINT_TOKENS)) * g.C + c0 + ch) * g.N + q * NPL;
-            #pragma unroll
-            for (int i = 0; i < NPL; ++i) hin[i] = n_in[i] ? ck[i] : 0.f;
+        const int t0 = rd * ROUND, tw = t0 + w * TW;
+        float Bv[NPL], Cv[NPL], hin[NPL];
+        const auto x_c = nx.x;
+        {   // elements; a padded token, and a channel that is not there, have x = d = do = 0
+            const uint32_t keep = tw + te < len && el_in ? ~0u : 0u;
             #pragma unroll
             for (int i = 0; i < E; ++i) {
-                const float v = widen(dr.e[i]) + bias[i], x = in ? widen(xr.e[i]) : 0.f, dy = in ? dyv[i] : 0.f;
-                const float d = in ? (g.softplus ? softplusf_(v) : v) : 0.f;
-                float o = dy, dzf = 0.f;
-                if (g.z) {
-                    const float z = in ? widen(zr.e[i]) : 0.f, s = sigmoidf_(z);
-                    o = dy * (z * s);
-                    dzf = dy * s * fmaf(z, 1.f - s, 1.f);
+                const uint32_t k = i < ne ? keep : 0u;
+                // softplus and its derivative from one exponential: e = exp(-|v|), 1 / (1 + e) or e / (1 + e)
+                const float v = nx.dt.get(i) + s_par[0][e0 + i], ex = __builtin_amdgcn_exp2f(-kLog2e * fabsf(v));
+                const float r = __builtin_amdgcn_rcpf(1.f + ex), sp = fmaxf(v, 0.f) + log1p_unit(ex), sg = v > 0.f ? r : ex * r;
+                const float z = nx.z.get(i), sz = sigmoidf_(z), dy = nx.dy.get(i);
+                auto kept = [&](float f) { return __uint_as_float(__float_as_uint(f) & k); };
+                const float d = kept(bit_select(soft, sp, v));
+                if (idx < 256) {
+                    s_k[0][w][e0 + i][te] = kept(bit_select(soft, sg, 1.f));
+                    s_k[1][w][e0 + i][te] = kept(dy * sz * fmaf(z, 1.f - sz, 1.f));
+                    s_d[w][e0 + i][te] = d;
+                    s_u[w][e0 + i][te] = kept(d * nx.x.get(i));
+                    s_o[w][e0 + i][te] = kept(dy * fmaf(z, sz, no_z));
                 }
-                s_d[w][e0 + i][te] = d;
-                s_u[w][e0 + i][te] = d * x;
-                s_o[w][e0 + i][te] = o;
-                s_keep[w][0][i][lane] = x;
-                s_keep[w][1][i][lane] = d;
-                s_keep[w][2][i][lane] = in ? (g.softplus ? sigmoidf_(v) : 1.f) : 0.f;
-                s_keep[w][3][i][lane] = o;
-                s_keep[w][4][i][lane] = dzf;
             }
             #pragma unroll
-            for (int i = 0; i < BN; ++i) {
-                s_b[w][te][bn0 + i] = in ? widen(br.e[i]) : 0.f;
-                s_c[w][te][bn0 + i] = in ? widen(cr.e[i]) : 0.f;
+            for (int i = 0; i < NPL; ++i) {
+                Bv[i] = nx.b.get(i);
+                Cv[i] = nx.c.get(i);
+                hin[i] = nx.h.get(i);
             }
         }
-        wave_sync();
-        auto Bv = [&](int tt) { return *reinterpret_cast<const Pack<float, NPL>*>(&s_b[w][tt][q * NPL]); };
-        auto Cv = [&](int tt) { return *reinterpret_cast<const Pack<float, NPL>*>(&s_c[w][tt][q * NPL]); };
+        __syncthreads();
 
-        // The state and the gradient that the wave's tokens give from zero, and their decay;
-        // the state from zero and the decay up to each part of PT tokens.
-        float Pm[PARTS - 1][NPL], Hm[PARTS - 1][NPL];
+        // Decays; the state and the gradient that the run gives from zero, and its decay.
+        float a[TW][NPL], Hm[NPL], dm = 0.f;   // after the first PT tokens: the state from zero, the sum of d
         {
-            float hl[NPL] = {}, gl[NPL] = {}, pr[NPL];
-            #pragma unroll
-            for (int i = 0; i < NPL; ++i) pr[i] = 1.f;
-            #pragma unroll
-            for (int tt = 0; tt < (WT > 1 ? TW : TW - PT); ++tt) {
-                if (tt % 4 == 0) forget_lds();
-                if (tt % PT == 0 && tt > 0) {
+            float hl[NPL] = {}, el[NPL] = {}, ds = 0.f;
+            static_for<TW / 4>([&](auto t4) {
+                if constexpr (t4 * 4 == PT) {
+                    dm = ds;
+                    #pragma unroll
+                    for (int i = 0; i < NPL; ++i) Hm[i] = hl[i];
+                }
+                const f32x4 d4 = *reinterpret_cast<const f32x4*>(&s_d[w][ch][t4 * 4]);
+                const f32x4 u4 = *reinterpret_cast<const f32x4*>(&s_u[w][ch][t4 * 4]);
+                static_for<4>([&](auto j_) {
+                    constexpr int j = j_, tt = t4 * 4 + j;
+                    ds += d4[j];
                     #pragma unroll
                     for (int i = 0; i < NPL; ++i) {
-                        Pm[tt / PT - 1][i] = pr[i];
-                        Hm[tt / PT - 1][i] = hl[i];
+                        a[tt][i] = __builtin_amdgcn_exp2f(d4[j] * A2[i]);
+                        hl[i] = fmaf(a[tt][i], hl[i], u4[j] * row_lane<tt>(Bv[i]));
                     }
-                }
-                const float dd = s_d[w][ch][tt], u = s_u[w][ch][tt], od = s_o[w][ch][tt];
-                const Pack<float, NPL> B = Bv(tt), C = Cv(tt);
-                #pragma unroll
-                for (int i = 0; i < NPL; ++i) {
-                    const float at = __builtin_amdgcn_exp2f(dd * A2[i]);
-                    hl[i] = fmaf(at, hl[i], u * B.e[i]);
-                    pr[i] *= at;
-                    if constexpr (WT > 1) gl[i] = fmaf(pr[i], C.e[i] * od, gl[i]);
-                }
-            }
-            if constexpr (WT == 1) {
-                #pragma unroll
-                for (int i = 0; i < NPL; ++i) {
-                    Pm[PARTS - 2][i] = pr[i];
-                    Hm[PARTS - 2][i] = hl[i];
-                }
-            }
+                });
+            });
             if constexpr (WT > 1) {
-                Pack<float, NPL> P, H, Gl;
+                static_for<TW / 4>([&](auto r4) {
+                    constexpr int t4 = TW / 4 - 1 - r4;
+                    const f32x4 o4 = *reinterpret_cast<const f32x4*>(&s_o[w][ch][t4 * 4]);
+                    static_for<4>([&](auto j_) {
+                        constexpr int j = 3 - j_, tt = t4 * 4 + j;
+                        #pragma unroll
+                        for (int i = 0; i < NPL; ++i) el[i] = a[tt][i] * (o4[j] * row_lane<tt>(Cv[i]) + el[i]);
+                    });
+                });
                 #pragma unroll
                 for (int i = 0; i < NPL; ++i) {
-                    P.e[i] = pr[i];
-                    H.e[i] = hl[i];
-                    Gl.e[i] = gl[i];
+                    s_x[0][w][s][i][lane] = __builtin_amdgcn_exp2f(ds * A2[i]);
+                    s_x[1][w][s][i][lane] = hl[i];
+                    s_x[2][w][s][i][lane] = el[i];
                 }
-                *reinterpret_cast<Pack<float, NPL>*>(&s_p[par][w][lane * NPL]) = P;
-                *reinterpret_cast<Pack<float, NPL>*>(&s_h[par][w][lane * NPL]) = H;
-                *reinterpret_cast<Pack<float, NPL>*>(&s_g[par][w][lane * NPL]) = Gl;
             }
         }
-        float gi[NPL];   // gradient of the state after the wave's tokens
+        float gi[NPL];   // gradient of the state after the run
         if constexpr (WT > 1) {
             __syncthreads();
             #pragma unroll
             for (int v = 0; v < WT - 1; ++v) {
                 if (v >= w) break;
-                const Pack<float, NPL> P = *reinterpret_cast<const Pack<float, NPL>*>(&s_p[par][v][lane * NPL]);
-                const Pack<float, NPL> H = *reinterpret_cast<const Pack<float, NPL>*>(&s_h[par][v][lane * NPL]);
                 #pragma unroll
-                for (int i = 0; i < NPL; ++i) hin[i] = fmaf(P.e[i], hin[i], H.e[i]);
+                for (int i = 0; i < NPL; ++i) hin[i] = fmaf(s_x[0][v][s][i][lane], hin[i], s_x[1][v][s][i][lane]);
             }
             #pragma unroll
             for (int v = WT - 1; v >= 0; --v) {
@@ -239,165 +252,194 @@ __global__ __launch_bounds__(64 * WT, 2) void ssm_backward_kernel(SsmParams g, B
                     #pragma unroll
                     for (int i = 0; i < NPL; ++i) gi[i] = gc[i];
                 }
-                const Pack<float, NPL> P = *reinterpret_cast<const Pack<float, NPL>*>(&s_p[par][v][lane * NPL]);
-                const Pack<float, NPL> Gl = *reinterpret_cast<const Pack<float, NPL>*>(&s_g[par][v][lane * NPL]);
                 #pragma unroll
-                for (int i = 0; i < NPL; ++i) gc[i] = fmaf(P.e[i], gc[i], Gl.e[i]);
+                for (int i = 0; i < NPL; ++i) gc[i] = fmaf(s_x[0][v][s][i][lane], gc[i], s_x[2][v][s][i][lane]);
             }
-            par ^= 1;
         } else {
             #pragma unroll
             for (int i = 0; i < NPL; ++i) gi[i] = gc[i];
         }
-        // Part by part from the last: the part's states, then its gradients.
+        // The run's states and gradients, the later PT tokens first.
         float dAr[NPL] = {};
+        static_for<TW / PT>([&](auto rp) {
+        constexpr int tp = TW - PT - rp * PT;
+        float h[PT][NPL], hb[NPL];   // hb: the state before the part
         #pragma unroll
-        for (int t8 = TW - PT; t8 >= 0; t8 -= PT) {
-        float a[PT][NPL], h[PT][NPL], hb[NPL];   // hb: the state before the part
-        #pragma unroll
-        for (int i = 0; i < NPL; ++i)
-            hb[i] = t8 ? fmaf(Pm[t8 ? t8 / PT - 1 : 0][i], hin[i], Hm[t8 ? t8 / PT - 1 : 0][i]) : hin[i];
-        #pragma unroll
-        for (int tt = 0; tt < PT; ++tt) {
-            if (tt % 4 == 0) forget_lds();
-            const float dd = s_d[w][ch][t8 + tt], u = s_u[w][ch][t8 + tt];
-            const Pack<float, NPL> B = Bv(t8 + tt);
-            #pragma unroll
-            for (int i = 0; i < NPL; ++i) {
-                a[tt][i] = __builtin_amdgcn_exp2f(dd * A2[i]);
-                h[tt][i] = fmaf(a[tt][i], tt ? h[tt ? tt - 1 : 0][i] : hb[i], u * B.e[i]);
-            }
-        }
-        // Backward, in groups of 4 tokens.
-        #pragma unroll
-        for (int tg = t8 + PT - 4; tg >= t8; tg -= 4) {
-            forget_lds();
-            float ys[4], us[4], ds[4], bc[NV];
-            #pragma unroll
-            for (int k = 3; k >= 0; --k) {
-                const int tt = tg + k;
-                const float dd = s_d[w][ch][tt], u = s_u[w][ch][tt], od = s_o[w][ch][tt];
-                const Pack<float, NPL> B = Bv(tt), C = Cv(tt);
-                ys[k] = us[k] = ds[k] = 0.f;
+        for (int i = 0; i < NPL; ++i) hb[i] = tp ? fmaf(__builtin_amdgcn_exp2f(dm * A2[i]), hin[i], Hm[i]) : hin[i];
+        static_for<PT / 4>([&](auto p4) {
+            const f32x4 u4 = *reinterpret_cast<const f32x4*>(&s_u[w][ch][tp + p4 * 4]);
+            static_for<4>([&](auto j_) {
+                constexpr int j = j_, tt = p4 * 4 + j;
+                #pragma unroll
+                for (int i = 0; i < NPL; ++i)
+                    h[tt][i] = fmaf(a[tp + tt][i], tt ? h[tt ? tt - 1 : 0][i] : hb[i], u4[j] * row_lane<tp + tt>(Bv[i]));
+            });
+        });
+        // four tokens at a time
+        static_for<PT / 4>([&](auto r4) {
+            constexpr int t4 = (tp + PT) / 4 - 1 - r4;
+            __builtin_amdgcn_sched_barrier(0);
+            const f32x4 d4 = *reinterpret_cast<const f32x4*>(&s_d[w][ch][t4 * 4]);
+            const f32x4 u4 = *reinterpret_cast<const f32x4*>(&s_u[w][ch][t4 * 4]);
+            const f32x4 o4 = *reinterpret_cast<const f32x4*>(&s_o[w][ch][t4 * 4]);
+            float y[4], us[4], ds[4], bc[16];
+            static_for<4>([&](auto j_) {
+                constexpr int j = 3 - j_, tt = t4 * 4 + j;
+                token_back<tt>(gi, Cv, Bv, o4[j], h[tt - tp], y[j], us[j]);
+                ds[j] = 0.f;
                 #pragma unroll
                 for (int i = 0; i < NPL; ++i) {
-                    const float et = fmaf(C.e[i], od, gi[i]);
-                    gi[i] = a[tt - t8][i] * et;
-                    const float qt = gi[i] * (tt > t8 ? h[tt > t8 ? tt - t8 - 1 : 0][i] : hb[i]);
-                    ys[k] = fmaf(C.e[i], h[tt - t8][i], ys[k]);
-                    us[k] = fmaf(et, B.e[i], us[k]);
-                    ds[k] = fmaf(qt, A2[i], ds[k]);
-                    dAr[i] = fmaf(qt, dd, dAr[i]);
-                    bc[k * 2 * NPL + i] = et * u;
-                    bc[k * 2 * NPL + NPL + i] = h[tt - t8][i] * od;
+                    bc[j * 4 + i] = gi[i] * u4[j];
+                    bc[j * 4 + 2 + i] = h[tt - tp][i] * o4[j];
+                    gi[i] *= a[tt][i];
+                    const float qt = gi[i] * (tt > tp ? h[tt > tp ? tt - tp - 1 : 0][i] : hb[i]);
+                    ds[j] = fmaf(qt, A2[i], ds[j]);
+                    dAr[i] = fmaf(qt, d4[j], dAr[i]);
                 }
-            }
-            // over the channels: the values are (token, dB or dC, state), the highest index bit first
-            #pragma unroll
-            for (int v = 0; v < NV / 2; ++v) bc[v] = halve<32>(bc[v], bc[v + NV / 2], lane);
-            #pragma unroll
-            for (int v = 0; v < NV / 4; ++v) bc[v] = halve<16>(bc[v], bc[v + NV / 4], lane);
-            if constexpr (LPC <= 8) {
-                #pragma unroll
-                for (int v = 0; v < NV / 8; ++v) bc[v] = halve<8>(bc[v], bc[v + NV / 8], lane);
-            }
-            if constexpr (LPC <= 4) {
-                #pragma unroll
-                for (int v = 0; v < NV / 16; ++v) bc[v] = halve<4>(bc[v], bc[v + NV / 16], lane);
-            }
-            constexpr int LEFT = NV / CH;   // values that stay with a lane
-            const int tt = tw + tg + (lane >> 4), v0 = (lane & 15) / LPC * LEFT;
-            if (tt < len) {
-                float* p = ws.bc + (((int64_t(cb) * g.B + b) * g.T + tt) * g.G + grp) * 2 * g.N;
-                #pragma unroll
-                for (int v = 0; v < LEFT; ++v) {
-                    const int n = q * NPL + (v0 + v) % NPL;
-                    if (n < g.N) p[(v0 + v) / NPL * g.N + n] = bc[v];
+                // over the rows, and the channels: as soon as the pair of tokens is there
+                if constexpr (j < 2) {
+                    y[j] = halve<32>(y[j], y[j + 2], lane);
+                    us[j] = halve<32>(us[j], us[j + 2], lane);
+                    ds[j] = halve<32>(ds[j], ds[j + 2], lane);
+                    halve_banks<8>(bc[j * 4], bc[j * 4 + 8], bc[j * 4 + 1], bc[j * 4 + 9]);
+                    halve_banks<8>(bc[j * 4 + 2], bc[j * 4 + 10], bc[j * 4 + 3], bc[j * 4 + 11]);
                 }
-            }
-            // over the channel's lanes; these tokens' d, u and o have been read
-            sum_lanes_to<LPC>(&s_d[w][ch][tg], ys, lane);
-            sum_lanes_to<LPC>(&s_u[w][ch][tg], us, lane);
-            sum_lanes_to<LPC>(&s_o[w][ch][tg], ds, lane);
-        }
-        }
+            });
+            // dB and dC: values (token, which, state); a lane keeps the one that its bits 3 .. 0 name
+            #pragma unroll
+            for (int v = 0; v < 4; v += 2) halve_banks<4>(bc[v], bc[v + 4], bc[v + 1], bc[v + 5]);
+            #pragma unroll
+            for (int v = 0; v < 2; ++v) bc[v] = halve<2>(bc[v], bc[v + 2], lane);
+            s_bc[w][t4 * 4 + (ch >> 2)][ch >> 1 & 1][n0 + (ch & 1)] = halve<1>(bc[0], bc[1], lane);
+            // row q keeps token q
+            s_r[w][s][0][ch][t4 * 4 + q] = halve<16>(y[0], y[1], lane);
+            s_r[w][s][1][ch][t4 * 4 + q] = halve<16>(us[0], us[1], lane);
+            s_r[w][s][2][ch][t4 * 4 + q] = halve<16>(ds[0], ds[1], lane);
+            // (without this the compiler puts off the sum and keeps all its terms)
+            #pragma unroll
+            for (int i = 0; i < NPL; ++i) settle(dAr[i]);
+        });
+        });
+        if (rd > 0) load(t0 - ROUND);   // here, where the registers of the decays and states are free
         #pragma unroll
         for (int i = 0; i < NPL; ++i) {
             dA[i] += dAr[i];
             if constexpr (WT == 1) gc[i] = gi[i];
         }
-        wave_sync();
-        float dx[E], ddt[E], dz[E];
+        __syncthreads();
+        const int thr = opaque(s * 64 + lane);
+        if (thr * E < 256) {
+            const int te = thr * E >> 4, e0 = thr * E & 15, ne = nc - e0;
+            const uint32_t eoff = uint32_t((w * TW + te) * g.C + c0 + e0);
+            float dx[E], ddt[E], dz[E];
+            #pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const float x = x_c.get(i), d = s_d[w][e0 + i][te], o = s_o[w][e0 + i][te], Dv = s_par[1][e0 + i];
+                float y = Dv * x, du = 0.f, dd = 0.f;
+                #pragma unroll
+                for (int v = 0; v < WS; ++v) {
+                    y += s_r[w][v][0][e0 + i][te];
+                    du += s_r[w][v][1][e0 + i][te];
+                    dd += s_r[w][v][2][e0 + i][te];
+                }
+                dd = fmaf(du, x, dd * kLn2);
+                dx[i] = fmaf(du, d, o * Dv);
+                ddt[i] = dd * s_k[0][w][e0 + i][te];
+                dz[i] = s_k[1][w][e0 + i][te] * y;
+                dD[i] = fmaf(o, x, dD[i]);
+                dbias[i] += ddt[i];
+            }
+            store(g.dx, t0, dx, eoff, ne);
+            store(g.ddt, t0, ddt, eoff, ne);
+            if (g.z) store(g.dz, t0, dz, eoff, ne);
+        }
+        // dB and dC of the run, 4 tokens at once.
+        {
+            const int r = thr & (2 * NP - 1), kind = r / NP, n = r % NP, width = g.G * 2 * g.N;
+            const rsrc_t bc = buf_rsrc(ws.bc + (((int64_t(cb) * g.B + b) * g.T + tw) * g.G + grp) * 2 * g.N,
+                                       int64_t(max(0, min(len - tw, TW))) * width * 4);
+            if (n < g.N) {
+                #pragma unroll
+                for (int k = 0; k < TW; k += 4) {
+                    const int tt = k + thr / (2 * NP);
+                    if (tw + tt < len)
+                        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(s_bc[w][tt][kind][n]), bc, uint32_t(tt * width + kind * g.N + n) * 4, 0, 0);
+                }
+            }
+        }
+        __syncthreads();   // the LDS rows are free again
+    }
+    // Places once more, from scratch.
+    const int lane_ = opaque(lane), ch_ = lane_ & 15, n0_ = s * 8 + (lane_ >> 4) * NPL;
+    auto there = [&](int i) { return ch_ < nc && n0_ + i < g.N; };
+    if (g.ds0 && w == 0) {
+        #pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            if (there(i)) g.ds0[(b * g.C + c0 + ch_) * g.N + n0_ + i] = gc[i];
+    }
+    // The parameters' gradients of this sequence, summed over the runs, and over the tokens of a channel.
+    __syncthreads();
+    #pragma unroll
+    for (int i = 0; i < NPL; ++i) s_x[0][w][s][i][lane_] = dA[i];
+    const int idx_ = (s * 64 + lane_) * E;
+    if (idx_ < 256) {
         #pragma unroll
         for (int i = 0; i < E; ++i) {
-            const float x = s_keep[w][0][i][lane], d = s_keep[w][1][i][lane], o = s_keep[w][3][i][lane];
-            const float y = fmaf(Dv[i], x, s_d[w][e0 + i][te]), du = s_u[w][e0 + i][te];
-            const float dd = fmaf(du, x, s_o[w][e0 + i][te] * kLn2);
-            dx[i] = fmaf(du, d, o * Dv[i]);
-            ddt[i] = in ? dd * s_keep[w][2][i][lane] : 0.f;
-            dz[i] = s_keep[w][4][i][lane] * y;
-            dD[i] = fmaf(o, x, dD[i]);
-            dbias[i] += ddt[i];
-        }
-        if (t < g.T) {
-            store(g.dx, e, dx);
-            store(g.ddt, e, ddt);
-            if (g.z) store(g.dz, e, dz);
-        }
-        wave_sync();   // the LDS rows are free again
-    }
-    #pragma unroll
-    for (int i = 0; i < NPL; ++i)
-        if (g.ds0 && n_in[i] && w == 0) g.ds0[srow + i] = gc[i];
-
-    // The parameters' gradients of this sequence: over the lanes of the same channels, then over the waves.
-    #pragma unroll
-    for (int i = 0; i < E; ++i) {
-        #pragma unroll
-        for (int m = 4; m < 64; m *= 2) {
-            dD[i] += __shfl_xor(dD[i], m);
-            dbias[i] += __shfl_xor(dbias[i], m);
+            s_d[w][(idx_ & 15) + i][idx_ >> 4] = dD[i];
+            s_u[w][(idx_ & 15) + i][idx_ >> 4] = dbias[i];
         }
     }
     __syncthreads();
-    #pragma unroll
-    for (int i = 0; i < NPL; ++i) s_p[0][w][lane * NPL + i] = dA[i];
-    if (te == 0) {
-        #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            s_d[w][e0 + i][0] = dD[i];
-            s_d[w][e0 + i][1] = dbias[i];
-        }
-    }
-    __syncthreads();
-    if (w != 0) return;
     float* out = ws.par + b * (int64_t(g.C) * g.N + 2 * g.C);
-    #pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-        float s = 0.f;
+    if (w == 0) {
         #pragma unroll
-        for (int v = 0; v < WT; ++v) s += s_p[0][v][lane * NPL + i];
-        if (n_in[i]) out[int64_t(c0 + ch) * g.N + q * NPL + i] = s;
+        for (int i = 0; i < NPL; ++i) {
+            float sum = 0.f;
+            #pragma unroll
+            for (int v = 0; v < WT; ++v) sum += s_x[0][v][s][i][lane_];
+            if (there(i)) out[int64_t(c0 + ch_) * g.N + n0_ + i] = sum;
+        }
     }
-    if (lane < 2 * CH && lane / 2 < nc) {
-        float s = 0.f;
-        #pragma unroll
-        for (int v = 0; v < WT; ++v) s += s_d[v][lane / 2][lane & 1];
-        out[int64_t(g.C) * g.N + (lane & 1) * g.C + c0 + lane / 2] = s;
+    if (wv == 0 && lane_ < 2 * CH && ch_ < nc) {
+        const bool second = lane_ >= CH;
+        float sum = 0.f;
+        for (int v = 0; v < WT; ++v)
+            #pragma unroll
+            for (int t = 0; t < TW; ++t) sum += second ? s_u[v][ch_][t] : s_d[v][ch_][t];
+        out[int64_t(g.C) * g.N + (second ? g.C : 0) + c0 + ch_] = sum;
     }
 }
 
-// dBm and dCm: the sums over the blocks of channels.
+// dBm and dCm: the sums over the blocks of channels.  A workgroup has 64 runs of V values and 4
+// threads to each, which take every fourth block.
+template <int V>
 __global__ __launch_bounds__(256) void ssm_sum_bc_kernel(SsmParams g, const float* bc, int ncb) {
     const int64_t M = int64_t(g.B) * g.T * g.G * 2 * g.N;
-    const int64_t m = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    if (m >= M) return;
-    const int n = int(m % g.N), kind = int(m / g.N % 2);
-    const int64_t bt = m / (2 * g.N), row = bt / g.G, b = row / g.T;
-    float s = 0.f;
-    if (row - b * g.T < seq_length(g.lengths, b, g.T))
-        for (int i = 0; i < ncb; ++i) s += bc[i * M + m];
-    st_pack_as<1>(kind ? g.dCm : g.dBm, bt * g.N + n, g.in_bf16, &s, true, 1);
+    const int64_t m = (int64_t(blockIdx.x) * 64 + (threadIdx.x & 63)) * V;
+    const int y = threadIdx.x >> 6;
+    const bool in = m < M;
+    const int64_t bt = m / (2 * g.N), row = bt / g.G, b = in ? row / g.T : 0;
+    float s[V] = {};
+    if (in && row - b * g.T < seq_length(g.lengths, b, g.T)) {
+        #pragma unroll 4
+        for (int i = y; i < ncb; i += 4) {
+            const Pack<float, V> p = ld_pack<V>(bc + i * M + m, true, V);
+            #pragma unroll
+            for (int v = 0; v < V; ++v) s[v] += p.e[v];
+        }
+    }
+    __shared__ float sm[3][64][V];
+    if (y > 0) {
+        #pragma unroll
+        for (int v = 0; v < V; ++v) sm[y - 1][threadIdx.x & 63][v] = s[v];
+    }
+    __syncthreads();
+    if (y > 0 || !in) return;
+    #pragma unroll
+    for (int v = 0; v < V; ++v)
+        for (int o = 0; o < 3; ++o) s[v] += sm[o][threadIdx.x][v];
+    const int n = int(m % g.N);
+    st_pack_as<V>(m / g.N % 2 ? g.dCm : g.dBm, bt * g.N + n, g.in_bf16, s, true, V);
 }
 
 // dA, dD and ddt_bias: the sums over the batch.
@@ -413,39 +455,30 @@ __global__ __launch_bounds__(256) void ssm_sum_batch_kernel(SsmParams g, const f
     } else if (g.dbias) g.dbias[m - CN - g.C] = s;
 }
 
-int lanes_of(int N) { return N <= 16 ? 4 : N <= 32 ? 8 : 16; }
-int blocks_of(const SsmParams& p) {
-    const int CH = 64 / lanes_of(p.N);
-    return (p.C / p.G + CH - 1) / CH;
-}
+int blocks_of(const SsmParams& p) { return (p.C / p.G + CH - 1) / CH; }
 int64_t up(int64_t x) { return (x + 255) & ~int64_t(255); }
 int64_t bc_bytes(const SsmParams& p) { return up(int64_t(blocks_of(p)) * p.B * p.T * p.G * 2 * p.N * 4); }
 int64_t par_bytes(const SsmParams& p) { return up(int64_t(p.B) * (int64_t(p.C) * p.N + 2 * p.C) * 4); }
 
-template <typename Tin, int LPC, int NPL>
-hipError_t launch_lpc(SsmParams p, const BwdWs& ws, hipStream_t stream) {
-    constexpr int E = 16 / LPC;
-    p.vec_c = p.C % E == 0 && (p.C / p.G) % E == 0;
-    p.vec_n = p.N == LPC * NPL;
-    const int ncb = blocks_of(p);
-    const dim3 grid{unsigned(int64_t(p.B) * p.G * ncb)};
-    if (grid.x == 0) {   // no channels or no sequences: only zeros to write
-    } else if (p.T <= TW) hipLaunchKernelGGL((ssm_backward_kernel<Tin, LPC, NPL, 1>), grid, dim3(64), 0, stream, p, ws);
-    else hipLaunchKernelGGL((ssm_backward_kernel<Tin, LPC, NPL, 4>), grid, dim3(256), 0, stream, p, ws);
-    const int64_t M = int64_t(p.B) * p.T * p.G * 2 * p.N, Mp = int64_t(p.C) * p.N + 2 * p.C;
-    if (M > 0)
-        hipLaunchKernelGGL(ssm_sum_bc_kernel, dim3(unsigned((M + 255) / 256)), dim3(256), 0, stream, p, ws.bc, ncb);
-    if (Mp > 0) hipLaunchKernelGGL(ssm_sum_batch_kernel, dim3(unsigned((Mp + 255) / 256)), dim3(256), 0, stream, p, ws.par);
+template <typename Tin, typename Ty, int WS, bool VEC>
+hipError_t launch_ws(const SsmParams& p, const BwdWs& ws, hipStream_t stream) {
+    const dim3 grid{unsigned(int64_t(p.B) * p.G * blocks_of(p))};
+    constexpr int WT = WS <= 4 ? 4 : 2;
+    if (p.T <= TW) hipLaunchKernelGGL((ssm_backward_kernel<Tin, Ty, WS, 1, VEC>), grid, dim3(64 * WS), 0, stream, p, ws);
+    else hipLaunchKernelGGL((ssm_backward_kernel<Tin, Ty, WS, WT, VEC>), grid, dim3(64 * WS * WT), 0, stream, p, ws);
     return hipGetLastError();
 }
-template <typename Tin>
-hipError_t launch_in(const SsmParams& p, const BwdWs& ws, hipStream_t stream) {
-    if (p.N <= 8) return launch_lpc<Tin, 4, 2>(p, ws, stream);
-    switch (lanes_of(p.N)) {
-        case 4: return launch_lpc<Tin, 4, 4>(p, ws, stream);
-        case 8: return launch_lpc<Tin, 8, 4>(p, ws, stream);
-        default: return launch_lpc<Tin, 16, 4>(p, ws, stream);
-    }
+template <typename Tin, typename Ty, bool VEC>
+hipError_t launch_vec(const SsmParams& p, const BwdWs& ws, hipStream_t stream) {
+    if (p.N <= 8) return launch_ws<Tin, Ty, 1, VEC>(p, ws, stream);
+    if (p.N <= 16) return launch_ws<Tin, Ty, 2, VEC>(p, ws, stream);
+    if (p.N <= 32) return launch_ws<Tin, Ty, 4, VEC>(p, ws, stream);
+    return launch_ws<Tin, Ty, 8, VEC>(p, ws, stream);
+}
+template <typename Tin, typename Ty>
+hipError_t launch_types(const SsmParams& p, const BwdWs& ws, hipStream_t stream) {
+    const bool vec = p.N % 2 == 0 && ((!p.in_bf16 && !p.y_bf16) || (p.C % 2 == 0 && p.C / p.G % 2 == 0));
+    return vec ? launch_vec<Tin, Ty, true>(p, ws, stream) : launch_vec<Tin, Ty, false>(p, ws, stream);
 }
 
 }  // namespace
@@ -467,7 +500,20 @@ hipError_t launch_ssm_backward(const SsmParams& p, hipStream_t stream) {
         if (e != hipSuccess) return e;
         ws.ck = f.ck;
     }
-    return p.in_bf16 ? launch_in<bf16_t>(p, ws, stream) : launch_in<float>(p, ws, stream);
+    if (int64_t(p.B) * p.C > 0) {
+        const hipError_t e = p.in_bf16 ? p.y_bf16 ? launch_types<bf16_t, bf16_t>(p, ws, stream) : launch_types<bf16_t, float>(p, ws, stream)
+                                       : p.y_bf16 ? launch_types<float, bf16_t>(p, ws, stream) : launch_types<float, float>(p, ws, stream);
+        if (e != hipSuccess) return e;
+    }
+    // The sums; without channels or sequences, the zeros.
+    const int ncb = blocks_of(p);
+    const int64_t M = int64_t(p.B) * p.T * p.G * 2 * p.N, Mp = int64_t(p.C) * p.N + 2 * p.C;
+    if (M > 0) {
+        if (p.N % 4 == 0) hipLaunchKernelGGL((ssm_sum_bc_kernel<4>), dim3(unsigned((M / 4 + 63) / 64)), dim3(256), 0, stream, p, ws.bc, ncb);
+        else hipLaunchKernelGGL((ssm_sum_bc_kernel<1>), dim3(unsigned((M + 63) / 64)), dim3(256), 0, stream, p, ws.bc, ncb);
+    }
+    if (Mp > 0) hipLaunchKernelGGL(ssm_sum_batch_kernel, dim3(unsigned((Mp + 255) / 256)), dim3(256), 0, stream, p, ws.par);
+    return hipGetLastError();
 }
 
 }  // namespace wkv7

@@ -24,7 +24,7 @@ __all__ = ["ssm_forward", "ssm_step", "ssm_backward", "ssm_checkpoint_bytes", "s
            "CHECKPOINT_TOKENS", "SsmDesc", "EXPORTED_SYMBOLS"]
 
 EXPORTED_SYMBOLS = ("ssm_checkpoint_bytes", "ssm_forward", "ssm_step", "ssm_backward_workspace_bytes", "ssm_backward")
-CHECKPOINT_TOKENS = 64
+CHECKPOINT_TOKENS = 32
 
 
 class SsmDesc(ctypes.Structure):

@@ -192,7 +192,7 @@ def test_descriptors(fn):
 
 
 def test_size_queries():
-    assert S.ssm_checkpoint_bytes(2, 65, 64, 16) == 2 * 2 * 64 * 16 * 4
+    assert S.ssm_checkpoint_bytes(2, 65, 64, 16) == 2 * 3 * 64 * 16 * 4
     assert S.ssm_checkpoint_bytes(2, 0, 64, 16) == 0
     assert S.ssm_backward_workspace_bytes(0, 10, 64, 16) == 0
     assert K.shortconv_backward_workspace_bytes(2, 0, 64, 4) == 0
