@@ -105,10 +105,9 @@ __global__ __launch_bounds__(64 * WT) void ssm_scan_kernel(SsmParams g) {
         left -= ROUND;
     };
     auto store_y = [&](int t0, const float* v) {
-        const rsrc_t r = buf_rsrc(yp, (max(0, min(g.T - t0, ROUND)) * int(yrow)) & ykeep);
+        const rsrc_t r = buf_rsrc(yp + t0 * yrow, (t0 < 0 ? 0 : max(0, min(g.T - t0, ROUND)) * int(yrow)) & ykeep);
         if (g.y_bf16) buf_store<bf16_t, E, VEC>(r, eoff * 2, v, ne);
         else buf_store<float, E, true>(r, eoff * 4, v, ne);
-        yp += ROUND * yrow;
     };
     auto checkpoint = [&](int t, const float* v) {
         #pragma unroll
@@ -129,6 +128,18 @@ __global__ __launch_bounds__(64 * WT) void ssm_scan_kernel(SsmParams g) {
             s_u[w][e0 + i][te] = d * nx.x.get(i);
         }
     };
+    // y of a round, from the rows' parts in LDS.
+    auto x_p = nx.x, z_p = nx.z;
+    auto output = [&](int t0) {
+        float out[E];
+        #pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const float y = fmaf(Dv[i], x_p.get(i), (s_y[w][0][e0 + i][te] + s_y[w][1][e0 + i][te]) + (s_y[w][2][e0 + i][te] + s_y[w][3][e0 + i][te]));
+            const float z = z_p.get(i);
+            out[i] = y * fmaf(z, sigmoidf_(z), no_z);
+        }
+        store_y(t0, out);
+    };
     load();
     int par = 0;
     for (int t0 = 0; t0 < len; t0 += ROUND) {
@@ -142,6 +153,9 @@ __global__ __launch_bounds__(64 * WT) void ssm_scan_kernel(SsmParams g) {
             Cv[i] = nx.c.get(i);
         }
         load();
+        // With a wave to itself the round before is finished here, while LDS turns this one's elements
+        // round (8 x 4096 x 4096 bf16: 700 -> 664 us; with more waves it is no faster).
+        if constexpr (WT == 1) output(t0 - ROUND);
         wave_sync();
 
         // The wave's tokens from a state: decay(token, state, d) and input(token, state, u).
@@ -205,17 +219,15 @@ __global__ __launch_bounds__(64 * WT) void ssm_scan_kernel(SsmParams g) {
                 [&](auto j, auto t4, int i, float uu) { return uu * row_lane<t4 * 4 + j>(Bv[i]); });
         }
         par ^= 1;
+        x_p = x_c;
+        z_p = z_c;
         wave_sync();
-        float out[E];
-        #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const float y = fmaf(Dv[i], x_c.get(i), (s_y[w][0][e0 + i][te] + s_y[w][1][e0 + i][te]) + (s_y[w][2][e0 + i][te] + s_y[w][3][e0 + i][te]));
-            const float z = z_c.get(i);
-            out[i] = y * fmaf(z, sigmoidf_(z), no_z);
+        if constexpr (WT > 1) {
+            output(t0);
+            wave_sync();
         }
-        store_y(t0, out);
-        wave_sync();   // the LDS rows are free again
     }
+    if (WT == 1 && len > 0) output((len + ROUND - 1) / ROUND * ROUND - ROUND);
     // Padding after the last round: y = 0, and the state as it is at the checkpoints there.
     const int done = (len + ROUND - 1) / ROUND * ROUND;
     const float zero[E] = {};
