@@ -523,6 +523,159 @@ __global__ __launch_bounds__(NTG) void norm_means_kernel(NormParams g, int runs,
     m12[2 * blockIdx.x + 1] = n > 0.f ? sm[1][0] / n : 0.f;
 }
 
+// A group's values over all positions in the registers of one workgroup: x is read once and the
+// statistics, or in the backward the two means, need no other pass.  A thread has V neighbouring channels
+// of up to R positions, `apart` positions from one to the next.
+constexpr int NTS = 1024;
+
+// Sum over the workgroup; every thread gets it.  Wave sums, then their sum in a fixed order.
+__device__ __forceinline__ float sum_group(float x, float* s_wave) {
+    x = sum_lanes<64>(x);
+    if ((threadIdx.x & 63) == 0) s_wave[threadIdx.x >> 6] = x;
+    __syncthreads();
+    float s = 0.f;
+    #pragma unroll
+    for (int i = 0; i < NTS / 64; ++i) s += s_wave[i];
+    return s;
+}
+
+template <typename Tin, typename Ty, int V, int R, bool BWD>
+__global__ __launch_bounds__(NTS) void norm_slab_kernel(NormParams g, float* part) {
+    __shared__ float s_wave[2][NTS / 64];
+    const int64_t b = blockIdx.x / g.G;
+    const int grp = int(blockIdx.x % g.G), Cg = g.C / g.G, slots = Cg / V, apart = NTS / slots;
+    const int ry = threadIdx.x / slots, c = grp * Cg + int(threadIdx.x % slots) * V;
+    const int len = seq_length(g.lengths, b, g.T);
+    const bool in = ry < apart;
+    const float count = float(len) * float(Cg), inv = count > 0.f ? 1.f / count : 0.f;
+    Pack<Tin, V> xr[R];
+    #pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int t = r * apart + ry;
+        if (in && t < len) xr[r] = ld_pack<V>(static_cast<const Tin*>(g.x) + (b * g.T + t) * g.C + c, true, V);
+    }
+    float mean, rstd;
+    if constexpr (!BWD) {
+        float s = 0.f, q = 0.f;
+        #pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (in && r * apart + ry < len) {
+                float sr = 0.f;
+                #pragma unroll
+                for (int j = 0; j < V; ++j) sr += widen(xr[r].e[j]);
+                s += sr;
+            }
+        mean = sum_group(s, s_wave[0]) * inv;
+        #pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (in && r * apart + ry < len) {
+                float qr = 0.f;
+                #pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float d = widen(xr[r].e[j]) - mean;
+                    qr = fmaf(d, d, qr);
+                }
+                q += qr;
+            }
+        rstd = 1.f / __builtin_sqrtf(fmaf(sum_group(q, s_wave[1]), inv, g.eps));
+        if (g.mean && threadIdx.x == 0) {
+            g.mean[blockIdx.x] = mean;
+            g.rstd[blockIdx.x] = rstd;
+        }
+    } else {
+        mean = g.mean[blockIdx.x];
+        rstd = g.rstd[blockIdx.x];
+    }
+    float wt[V], bs[V];
+    channel_params<V>(g, in ? c : 0, wt, bs);
+    if constexpr (!BWD) {
+        #pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int t = r * apart + ry;
+            if (!in || t >= g.T) break;
+            const int64_t e = (b * g.T + t) * g.C + c;
+            float out[V] = {};
+            if (t < len) {
+                Pack<Tin, V> gt;
+                if (g.gate) gt = ld_pack<V>(static_cast<const Tin*>(g.gate) + e, true, V);
+                #pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float pre = fmaf((widen(xr[r].e[j]) - mean) * rstd, wt[j], bs[j]);
+                    out[j] = g.silu ? pre * sigmoidf_(pre) : pre;
+                    if (g.gate) out[j] *= widen(gt.e[j]);
+                }
+            }
+            st_pack_as<V>(g.y, e, g.y_bf16, out, true, V);
+        }
+    } else {
+        Pack<Ty, V> dyr[R];
+        #pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int t = r * apart + ry;
+            if (in && t < len) dyr[r] = ld_pack<V>(static_cast<const Ty*>(g.dy) + (b * g.T + t) * g.C + c, true, V);
+        }
+        float dxh[R][V], dw[V] = {}, db[V] = {}, s1 = 0.f, s2 = 0.f;
+        #pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int t = r * apart + ry;
+            if (!in || t >= g.T) break;
+            const int64_t e = (b * g.T + t) * g.C + c;
+            Pack<Tin, V> gt;
+            float dg[V] = {}, s1r = 0.f, s2r = 0.f;
+            if (t < len && g.gate) gt = ld_pack<V>(static_cast<const Tin*>(g.gate) + e, true, V);
+            #pragma unroll
+            for (int j = 0; j < V; ++j) {
+                dxh[r][j] = 0.f;
+                if (t >= len) continue;
+                const float xh = (widen(xr[r].e[j]) - mean) * rstd, pre = fmaf(xh, wt[j], bs[j]);
+                float act = pre, da = 1.f, d = widen(dyr[r].e[j]);
+                if (g.silu) {
+                    const float sg = sigmoidf_(pre);
+                    act = pre * sg;
+                    da = sg * fmaf(pre, 1.f - sg, 1.f);
+                }
+                dg[j] = d * act;
+                if (g.gate) d *= widen(gt.e[j]);
+                d *= da;
+                db[j] += d;
+                dw[j] = fmaf(d, xh, dw[j]);
+                dxh[r][j] = d * wt[j];
+                s1r += dxh[r][j];
+                s2r = fmaf(dxh[r][j], xh, s2r);
+            }
+            s1 += s1r;
+            s2 += s2r;
+            if (g.gate) st_pack<V>(static_cast<Tin*>(g.dgate) + e, dg, true, V);
+        }
+        s1 = sum_group(s1, s_wave[0]) * inv;
+        s2 = sum_group(s2, s_wave[1]) * inv;
+        #pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int t = r * apart + ry;
+            if (!in || t >= g.T) break;
+            float out[V];
+            #pragma unroll
+            for (int j = 0; j < V; ++j)
+                out[j] = t < len ? (dxh[r][j] - s1 - (widen(xr[r].e[j]) - mean) * rstd * s2) * rstd : 0.f;
+            st_pack<V>(static_cast<Tin*>(g.dx) + (b * g.T + t) * g.C + c, out, true, V);
+        }
+        // The channels' sums of this sequence, [B][2][C]: over the threads of a channel, through LDS.
+        __shared__ float s_par[2][NTS * V];
+        #pragma unroll
+        for (int j = 0; j < V; ++j) {
+            s_par[0][threadIdx.x * V + j] = dw[j];
+            s_par[1][threadIdx.x * V + j] = db[j];
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < 2 * Cg; i += NTS) {
+            const int which = i >= Cg, cc = i - which * Cg;
+            float s = 0.f;
+            for (int r = 0; r < apart; ++r) s += s_par[which][(r * slots) * V + cc];
+            part[(b * 2 + which) * g.C + grp * Cg + cc] = s;
+        }
+    }
+}
+
 // Lanes of a group in the row form (0: the general form).
 int row_lanes(const NormParams& p) {
     const int Cg = p.C / p.G;
@@ -553,6 +706,19 @@ int64_t wave_rows(const NormParams& p, bool bwd) {
 int channels_per_thread(const NormParams& p) {
     const int Cg = p.C / p.G;
     return Cg % 8 == 0 ? 8 : Cg % 2 == 0 ? 2 : 1;
+}
+// Channels (up to 16 bytes of them) and positions of a thread in the slab form (0 positions: the group
+// does not fit the registers of a workgroup).  1 x 1531 x 1024 in 32 groups: 11 us, with three passes 12;
+// 8 x 1531 x 1024: 19 and 30; 8 x 500 x 1024: 8 and 16, with gradients 15 and 30 (fp32).
+int slab_channels(const NormParams& p, bool bwd) {
+    const int Cg = p.C / p.G;
+    return p.in_bf16 && !bwd && Cg % 8 == 0 ? 8 : Cg % 4 == 0 ? 4 : Cg % 2 == 0 ? 2 : 1;
+}
+int slab_positions(const NormParams& p, bool bwd) {
+    const int Cg = p.C / p.G, V = slab_channels(p, bwd), slots = Cg / V;
+    if (p.T <= 1 || slots > NTS) return 0;
+    const int apart = NTS / slots, r = (p.T + apart - 1) / apart;
+    return r <= 4 ? 4 : r <= 8 ? 8 : r <= 16 && V < 8 && !bwd ? 16 : 0;   // (the backward has three arrays)
 }
 // Positions of one partial sum: 64, fewer where that leaves less than a wave for every SIMD.
 int run_of(const NormParams& p) {
@@ -591,6 +757,31 @@ hipError_t launch_wave(const NormParams& p, bool bwd, hipStream_t stream) {
     else hipLaunchKernelGGL((norm_wave_kernel<Tin, float, K, V, true>), grid, dim3(NTG), 0, stream, p, nrow, part);
     hipLaunchKernelGGL(norm_sum_kernel, dim3(unsigned((2 * int64_t(p.C) + 31) / 32)), dim3(1024), 0, stream, p, part, nrow);
     return hipGetLastError();
+}
+
+template <typename Tin, int V, int R>
+hipError_t launch_slab(const NormParams& p, bool bwd, hipStream_t stream) {
+    float* part = static_cast<float*>(p.ws);
+    const dim3 grid{unsigned(int64_t(p.B) * p.G)};
+    constexpr bool kBwd = R <= 8 && V <= 4;
+    if (!bwd || !kBwd) {
+        hipLaunchKernelGGL((norm_slab_kernel<Tin, Tin, V, R, false>), grid, dim3(NTS), 0, stream, p, part);
+        return hipGetLastError();
+    }
+    if constexpr (kBwd) {
+        if (p.y_bf16) hipLaunchKernelGGL((norm_slab_kernel<Tin, bf16_t, V, R, true>), grid, dim3(NTS), 0, stream, p, part);
+        else hipLaunchKernelGGL((norm_slab_kernel<Tin, float, V, R, true>), grid, dim3(NTS), 0, stream, p, part);
+        hipLaunchKernelGGL(norm_sum_kernel, dim3(unsigned((2 * int64_t(p.C) + 31) / 32)), dim3(1024), 0, stream, p, part, int64_t(p.B));
+    }
+    return hipGetLastError();
+}
+template <typename Tin, int V>
+hipError_t launch_slab_r(const NormParams& p, bool bwd, hipStream_t stream) {
+    switch (slab_positions(p, bwd)) {
+        case 4: return launch_slab<Tin, V, 4>(p, bwd, stream);
+        case 8: return launch_slab<Tin, V, 8>(p, bwd, stream);
+        default: return launch_slab<Tin, V, 16>(p, bwd, stream);
+    }
 }
 
 template <typename Tin, int V>
@@ -646,6 +837,15 @@ hipError_t launch_in(const NormParams& p, bool bwd, hipStream_t stream) {
         case 16: return even ? launch_wave<Tin, 16, 2>(p, bwd, stream) : launch_wave<Tin, 16, 1>(p, bwd, stream);
         default: break;
     }
+    if (slab_positions(p, bwd)) {
+        switch (slab_channels(p, bwd)) {
+            case 8:
+                if constexpr (sizeof(Tin) == 2) return slab_positions(p, bwd) == 4 ? launch_slab<Tin, 8, 4>(p, bwd, stream) : launch_slab<Tin, 8, 8>(p, bwd, stream);
+            case 4: return launch_slab_r<Tin, 4>(p, bwd, stream);
+            case 2: return launch_slab_r<Tin, 2>(p, bwd, stream);
+            default: return launch_slab_r<Tin, 1>(p, bwd, stream);
+        }
+    }
     switch (channels_per_thread(p)) {
         case 8: return launch_general<Tin, 8>(p, bwd, stream);
         case 2: return launch_general<Tin, 2>(p, bwd, stream);
@@ -656,7 +856,7 @@ hipError_t launch_in(const NormParams& p, bool bwd, hipStream_t stream) {
 }  // namespace
 
 int64_t groupnorm_workspace(const NormParams& p) {
-    if (int64_t(p.B) * p.T * p.C == 0 || row_lanes(p) || wave_runs(p)) return 0;
+    if (int64_t(p.B) * p.T * p.C == 0 || row_lanes(p) || wave_runs(p) || slab_positions(p, false)) return 0;
     const int64_t slots = p.C / channels_per_thread(p);
     return up(4 * (up(2 * int64_t(p.B) * p.G) + 2 * int64_t(p.B) * runs_of(p) * slots));
 }
@@ -664,6 +864,7 @@ int64_t groupnorm_backward_workspace(const NormParams& p) {
     if (int64_t(p.B) * p.T * p.C == 0) return 0;
     if (row_lanes(p)) return up(4 * rows_of(p, true).nrow * 2 * p.C);
     if (wave_runs(p)) return up(4 * wave_rows(p, true) * 2 * p.C);
+    if (slab_positions(p, true)) return up(4 * int64_t(p.B) * 2 * p.C);
     return up(4 * (up(2 * int64_t(p.B) * p.G) + 2 * int64_t(p.B) * runs_of(p) * p.C));
 }
 

@@ -57,6 +57,12 @@ CASES = [
     (1, 300, 33, 11, "f32", None, True, True, "none"),
     (2, 64, 1024, 8, "bf16", None, False, False, "none"),
     (2, 65, 10, 2, "bf16", None, True, True, "silu"),
+    (2, 1531, 96, 3, "f32", [1531, 700], True, True, "silu"),      # a group of a sequence in a workgroup's registers
+    (2, 1100, 28, 2, "bf16", None, True, True, "none"),
+    (2, 3000, 96, 2, "f32", [2999, 3000], True, True, "silu"),     # and past them
+    (1, 700, 1044, 1, "bf16", None, True, False, "silu"),
+    (1, 1000, 514, 1, "f32", None, True, True, "none"),
+    (1, 130, 1999, 1, "bf16", [77], False, True, "silu"),
 ]
 IDS = ["B{}_T{}_C{}_G{}_{}_{}".format(*c[:5], c[8]) for c in CASES]
 
