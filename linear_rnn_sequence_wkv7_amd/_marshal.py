@@ -56,6 +56,39 @@ def ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def ptrs(*tensors):
+    """The addresses of tensors, None for None."""
+    return [None if t is None else t.data_ptr() for t in tensors]
+
+
+def output(name, t, like, y_dtype, dev):
+    """The output t, checked, or a new one of like's shape and the named dtype (None: like's)."""
+    if t is not None:
+        check(name, t, like.shape, dtype_named(y_dtype, t.dtype), dev)
+        return t
+    if y_dtype is None:
+        return torch.empty_like(like)
+    return torch.empty(like.shape, dtype=dtype_named(y_dtype, None), device=dev)
+
+
+def gradients(grads, wanted, dev):
+    """The output tensors of a backward: for each (key, like, shape, dtype) None where like is, else the
+    caller's, checked, or a new one (of like itself where shape is None)."""
+    out = {}
+    for key, like, shape, dtype in wanted:
+        given = grads.get(key) if grads else None
+        if like is None:
+            out[key] = None
+        elif given is not None:
+            check(f"grads[{key!r}]", given, like.shape if shape is None else shape, like.dtype if dtype is None else dtype, dev)
+            out[key] = given
+        elif shape is None:
+            out[key] = torch.empty_like(like)
+        else:
+            out[key] = torch.empty(shape, dtype=dtype, device=dev)
+    return out
+
+
 def size(fn, *args) -> int:
     """A size query of the library."""
     n = fn(*args)
@@ -77,13 +110,13 @@ def scratch(workspace, need, dev):
 
 # The current stream's handle and the current device's index, without the wrapper objects
 # that torch.cuda's own functions make (2 of the 13 microseconds of a small call).
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 def call(fn, dev, *args):
     """fn(*args, stream) on dev's current stream, with dev the current device."""
     index = dev.index
-    if torch.cuda.current_device() == index:
+    if _device() == index:
         rc = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):

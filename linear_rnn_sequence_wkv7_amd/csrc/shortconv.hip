@@ -77,14 +77,20 @@ __global__ __launch_bounds__(NTC) void conv_forward_kernel(ConvParams g, Runs r)
         #pragma unroll
         for (int k = 0; k < K - 1; ++k) input_row<Tin, V>(g, b, t0 - K + 1 + k, c, win[k + 1]);
     }
-    constexpr int U = 8;   // rows in flight
+    // Rows are loaded a group ahead.
+    constexpr int U = 4;
+    Pack<Tin, V> next[U];
+    auto load = [&](int tb) {
+        #pragma unroll
+        for (int i = 0; i < U; ++i)
+            next[i] = ld_pack<V>(static_cast<const Tin*>(g.x) + (b * g.T + min(tb + i, t1 - 1)) * g.C + c, true, V);
+    };
+    load(t0);
     for (int tb = t0; tb < t1; tb += U) {
         Pack<Tin, V> rows[U];
         #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int t = min(tb + i, t1 - 1);
-            rows[i] = ld_pack<V>(static_cast<const Tin*>(g.x) + (b * g.T + t) * g.C + c, true, V);
-        }
+        for (int i = 0; i < U; ++i) rows[i] = next[i];
+        load(tb + U);
         #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int t = tb + i;
@@ -313,10 +319,11 @@ hipError_t copy_state(const void* from, void* to, int64_t n, hipStream_t stream)
     return hipGetLastError();
 }
 
-// Run lengths: 32 tokens where that leaves a wave for every SIMD, shorter for small calls.
-Runs runs_of(const ConvParams& p, int V) {
+// Run lengths: 32 tokens where that leaves two waves (in the backward four) for every SIMD, shorter
+// for small calls.
+Runs runs_of(const ConvParams& p, int V, bool bwd) {
     Runs r{p.C / V, 0, 32};
-    while (r.len > 8 && int64_t(p.B) * ((p.T + r.len - 1) / r.len) * r.slots < 4 * 65536) r.len /= 2;
+    while (r.len > 8 && int64_t(p.B) * ((p.T + r.len - 1) / r.len) * r.slots < (bwd ? 4 : 2) * 65536) r.len /= 2;
     r.runs = (p.T + r.len - 1) / r.len;
     return r;
 }
@@ -328,7 +335,7 @@ int channels_per_thread(const ConvParams& p, bool bwd) {
 
 template <typename Tin, int K, int V>
 hipError_t launch_k(const ConvParams& p, int what, hipStream_t stream) {
-    const Runs r = runs_of(p, V);
+    const Runs r = runs_of(p, V, what == 2);
     if constexpr (V == 8) {
         if (what == 2) return hipErrorInvalidValue;   // channels_per_thread gives 4 at most
     }
@@ -383,7 +390,7 @@ hipError_t launch(const ConvParams& p, int what, hipStream_t stream) {
 
 int64_t shortconv_backward_workspace(const ConvParams& p) {
     if (int64_t(p.B) * p.T * p.C == 0) return 0;
-    const Runs r = runs_of(p, channels_per_thread(p, true));
+    const Runs r = runs_of(p, channels_per_thread(p, true), true);
     return (int64_t(p.B) * ((r.runs + 3) / 4) * (p.K + 1) * p.C * 4 + 255) & ~int64_t(255);
 }
 

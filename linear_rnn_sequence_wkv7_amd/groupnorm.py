@@ -87,10 +87,7 @@ def groupnorm_forward(x, G: int, *, weight=None, bias=None, gate=None, act: str 
     """Returns (y, mean, rstd); mean and rstd, which groupnorm_backward takes, are None when
     return_stats is False and they are not given."""
     dev, B, T, C = _inputs(x, G, weight, bias, gate, lengths)
-    if y is None:
-        y = torch.empty(x.shape, dtype=M.dtype_named(y_dtype, x.dtype), device=dev)
-    else:
-        M.check("y", y, x.shape, M.dtype_named(y_dtype, y.dtype), dev)
+    y = M.output("y", y, x, y_dtype, dev)
     if return_stats:
         mean = torch.empty((B, G), dtype=torch.float32, device=dev) if mean is None else mean
         rstd = torch.empty((B, G), dtype=torch.float32, device=dev) if rstd is None else rstd
@@ -99,9 +96,7 @@ def groupnorm_forward(x, G: int, *, weight=None, bias=None, gate=None, act: str 
     desc = GroupnormDesc(B, T, C, G, M.dtype_code(x), M.dtype_code(y), _act(act), eps, M.ptr(lengths))
     lib = _lib()
     ws, ws_bytes, keep = M.scratch(workspace, M.size(lib.groupnorm_workspace_bytes, ctypes.byref(desc)), dev)
-    p = M.ptr
-    M.call(lib.groupnorm_forward, dev, ctypes.byref(desc), p(x), p(weight), p(bias), p(gate), p(y), p(mean), p(rstd), ws,
-           ws_bytes)
+    M.call(lib.groupnorm_forward, dev, ctypes.byref(desc), *M.ptrs(x, weight, bias, gate, y, mean, rstd), ws, ws_bytes)
     return y, mean, rstd
 
 
@@ -115,21 +110,11 @@ def groupnorm_backward(x, G: int, dy, mean, rstd, *, weight=None, bias=None, gat
     M.check("dy", dy, x.shape, dy.dtype, dev)
     M.check("mean", mean, (B, G), f32, dev)
     M.check("rstd", rstd, (B, G), f32, dev)
-    out = {}
-    for key, like, shape, dtype in (("x", x, x.shape, x.dtype), ("weight", weight, (C,), f32), ("bias", bias, (C,), f32),
-                                    ("gate", gate, x.shape, x.dtype)):
-        given = grads.get(key) if grads else None
-        if like is None:
-            out[key] = None
-        elif given is None:
-            out[key] = torch.empty(shape, dtype=dtype, device=dev)
-        else:
-            M.check(f"grads[{key!r}]", given, shape, dtype, dev)
-            out[key] = given
+    out = M.gradients(grads, (("x", x, None, None), ("weight", weight, None, None), ("bias", bias, None, None),
+                              ("gate", gate, None, None)), dev)
     desc = GroupnormDesc(B, T, C, G, M.dtype_code(x), M.dtype_code(dy), _act(act), 1.0, M.ptr(lengths))
     lib = _lib()
     ws, ws_bytes, keep = M.scratch(workspace, M.size(lib.groupnorm_backward_workspace_bytes, ctypes.byref(desc)), dev)
-    p = M.ptr
-    M.call(lib.groupnorm_backward, dev, ctypes.byref(desc), p(x), p(weight), p(bias), p(gate), p(dy), p(mean), p(rstd),
-           p(out["x"]), p(out["weight"]), p(out["bias"]), p(out["gate"]), ws, ws_bytes)
+    M.call(lib.groupnorm_backward, dev, ctypes.byref(desc),
+           *M.ptrs(x, weight, bias, gate, dy, mean, rstd, out["x"], out["weight"], out["bias"], out["gate"]), ws, ws_bytes)
     return out

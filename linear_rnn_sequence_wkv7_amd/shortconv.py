@@ -77,17 +77,13 @@ def shortconv_forward(x, w, *, bias=None, state=None, lengths=None, act: str = "
     state_out); state_out is None when return_state is False and may be state (in place)."""
     dev, B, T, C, K = _inputs(x, w, bias, lengths, False)
     M.check_if("state", state, (B, K - 1, C), x.dtype, dev)
-    if y is None:
-        y = torch.empty(x.shape, dtype=M.dtype_named(y_dtype, x.dtype), device=dev)
-    else:
-        M.check("y", y, x.shape, M.dtype_named(y_dtype, y.dtype), dev)
+    y = M.output("y", y, x, y_dtype, dev)
     if state_out is not None:
         M.check("state_out", state_out, (B, K - 1, C), x.dtype, dev)
     elif return_state:
         state_out = torch.empty((B, max(K - 1, 0), C), dtype=x.dtype, device=dev)
     desc = ShortconvDesc(B, T, C, K, M.dtype_code(x), M.dtype_code(y), _act(act), 0, M.ptr(lengths))
-    p = M.ptr
-    M.call(_lib().shortconv_forward, dev, ctypes.byref(desc), p(x), p(w), p(bias), p(state), p(y), p(state_out))
+    M.call(_lib().shortconv_forward, dev, ctypes.byref(desc), *M.ptrs(x, w, bias, state, y, state_out))
     return y, state_out
 
 
@@ -99,13 +95,9 @@ def shortconv_step(x, w, state, *, bias=None, state_index=None, act: str = "silu
     S = state.shape[0] if state.dim() else 0
     M.check("state", state, (S, K - 1, C), x.dtype, dev)
     M.check_if("state_index", state_index, (B,), torch.int32, dev)
-    if y is None:
-        y = torch.empty((B, C), dtype=M.dtype_named(y_dtype, x.dtype), device=dev)
-    else:
-        M.check("y", y, x.shape, M.dtype_named(y_dtype, y.dtype), dev)
+    y = M.output("y", y, x, y_dtype, dev)
     desc = ShortconvDesc(B, 1, C, K, M.dtype_code(x), M.dtype_code(y), _act(act), S, None)
-    p = M.ptr
-    M.call(_lib().shortconv_step, dev, ctypes.byref(desc), p(x), p(w), p(bias), p(state), p(state_index), p(y))
+    M.call(_lib().shortconv_step, dev, ctypes.byref(desc), *M.ptrs(x, w, bias, state, state_index, y))
     return y
 
 
@@ -120,22 +112,12 @@ def shortconv_backward(x, w, dy, *, bias=None, state=None, dstate=None, lengths=
     M.check_if("state", state, (B, K - 1, C), x.dtype, dev)
     M.check("dy", dy, x.shape, dy.dtype, dev)
     M.check_if("dstate", dstate, (B, K - 1, C), f32, dev)
-    out = {}
-    for key, like, shape, dtype in (("x", x, x.shape, x.dtype), ("w", w, (C, K), f32), ("bias", bias, (C,), f32),
-                                    ("state", True if return_dstate else None, (B, max(K - 1, 0), C), f32)):
-        given = grads.get(key) if grads else None
-        if like is None:
-            out[key] = None
-        elif given is None:
-            out[key] = torch.empty(shape, dtype=dtype, device=dev)
-        else:
-            M.check(f"grads[{key!r}]", given, shape, dtype, dev)
-            out[key] = given
+    out = M.gradients(grads, (("x", x, None, None), ("w", w, None, None), ("bias", bias, None, None),
+                              ("state", x if return_dstate else None, (B, max(K - 1, 0), C), f32)), dev)
     desc = ShortconvDesc(B, T, C, K, M.dtype_code(x), M.dtype_code(dy), _act(act), 0, M.ptr(lengths))
     lib = _lib()
     need = M.size(lib.shortconv_backward_workspace_bytes, ctypes.byref(desc))
     ws, ws_bytes, keep = M.scratch(workspace, need, dev)
-    p = M.ptr
-    M.call(lib.shortconv_backward, dev, ctypes.byref(desc), p(x), p(w), p(bias), p(state), p(dy), p(dstate), p(out["x"]),
-           p(out["w"]), p(out["bias"]), p(out["state"]), ws, ws_bytes)
+    M.call(lib.shortconv_backward, dev, ctypes.byref(desc),
+           *M.ptrs(x, w, bias, state, dy, dstate, out["x"], out["w"], out["bias"], out["state"]), ws, ws_bytes)
     return out

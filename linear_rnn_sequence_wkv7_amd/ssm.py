@@ -118,19 +118,15 @@ def ssm_forward(x, dt, A, Bm, Cm, *, D=None, dt_bias=None, z=None, state=None, l
     the call fills for ssm_backward."""
     dev, B, T, C, N, G = _inputs(x, dt, A, Bm, Cm, D, dt_bias, z, lengths, False)
     M.check_if("state", state, (B, C, N), torch.float32, dev)
-    if y is None:
-        y = torch.empty(x.shape, dtype=M.dtype_named(y_dtype, x.dtype), device=dev)
-    else:
-        M.check("y", y, x.shape, M.dtype_named(y_dtype, y.dtype), dev)
+    y = M.output("y", y, x, y_dtype, dev)
     if state_out is not None:
         M.check("state_out", state_out, (B, C, N), torch.float32, dev)
     elif return_state:
         state_out = torch.empty((B, C, N), dtype=torch.float32, device=dev)
     _check_checkpoints(checkpoints, B, T, C, N, dev)
     desc = _desc(x, y, B, T, C, N, G, softplus, lengths)
-    p = M.ptr
-    M.call(_lib().ssm_forward, dev, ctypes.byref(desc), p(x), p(dt), p(A), p(Bm), p(Cm), p(D), p(dt_bias), p(z),
-           p(state), p(y), p(state_out), p(checkpoints))
+    M.call(_lib().ssm_forward, dev, ctypes.byref(desc),
+           *M.ptrs(x, dt, A, Bm, Cm, D, dt_bias, z, state, y, state_out, checkpoints))
     return y, state_out
 
 
@@ -144,14 +140,9 @@ def ssm_step(x, dt, A, Bm, Cm, state, *, D=None, dt_bias=None, z=None, state_ind
     S = state.shape[0] if state.dim() else 0
     M.check("state", state, (S, C, N), torch.float32, dev)
     M.check_if("state_index", state_index, (B,), torch.int32, dev)
-    if y is None:
-        y = torch.empty((B, C), dtype=M.dtype_named(y_dtype, x.dtype), device=dev)
-    else:
-        M.check("y", y, x.shape, M.dtype_named(y_dtype, y.dtype), dev)
+    y = M.output("y", y, x, y_dtype, dev)
     desc = _desc(x, y, B, 1, C, N, G, softplus, None, S)
-    p = M.ptr
-    M.call(_lib().ssm_step, dev, ctypes.byref(desc), p(x), p(dt), p(A), p(Bm), p(Cm), p(D), p(dt_bias), p(z), p(state),
-           p(state_index), p(y))
+    M.call(_lib().ssm_step, dev, ctypes.byref(desc), *M.ptrs(x, dt, A, Bm, Cm, D, dt_bias, z, state, state_index, y))
     return y
 
 
@@ -170,25 +161,14 @@ def ssm_backward(x, dt, A, Bm, Cm, dy, *, D=None, dt_bias=None, z=None, state=No
     M.check("dy", dy, x.shape, dy.dtype, dev)
     M.check_if("dstate", dstate, (B, C, N), f32, dev)
     _check_checkpoints(checkpoints, B, T, C, N, dev)
-    out = {}
-    for key, like, shape, dtype in (("x", x, x.shape, x.dtype), ("dt", dt, x.shape, x.dtype), ("z", z, x.shape, x.dtype),
-                                    ("B", Bm, Bm.shape, x.dtype), ("C", Cm, Bm.shape, x.dtype), ("A", A, (C, N), f32),
-                                    ("D", D, (C,), f32), ("dt_bias", dt_bias, (C,), f32),
-                                    ("state", True if return_dstate else None, (B, C, N), f32)):
-        given = grads.get(key) if grads else None
-        if like is None:
-            out[key] = None
-        elif given is None:
-            out[key] = torch.empty(shape, dtype=dtype, device=dev)
-        else:
-            M.check(f"grads[{key!r}]", given, shape, dtype, dev)
-            out[key] = given
+    out = M.gradients(grads, (("x", x, None, None), ("dt", dt, None, None), ("z", z, None, None), ("B", Bm, None, None),
+                              ("C", Cm, None, None), ("A", A, None, None), ("D", D, None, None), ("dt_bias", dt_bias, None, None),
+                              ("state", x if return_dstate else None, (B, C, N), f32)), dev)
     desc = _desc(x, dy, B, T, C, N, G, softplus, lengths)
     lib = _lib()
     need = M.size(lib.ssm_backward_workspace_bytes, ctypes.byref(desc), 1 if checkpoints is None else 0)
     ws, ws_bytes, keep = M.scratch(workspace, need, dev)
-    p = M.ptr
-    M.call(lib.ssm_backward, dev, ctypes.byref(desc), p(x), p(dt), p(A), p(Bm), p(Cm), p(D), p(dt_bias), p(z), p(state),
-           p(dy), p(dstate), p(checkpoints), p(out["x"]), p(out["dt"]), p(out["A"]), p(out["B"]), p(out["C"]), p(out["D"]),
-           p(out["dt_bias"]), p(out["z"]), p(out["state"]), ws, ws_bytes)
+    M.call(lib.ssm_backward, dev, ctypes.byref(desc),
+           *M.ptrs(x, dt, A, Bm, Cm, D, dt_bias, z, state, dy, dstate, checkpoints, out["x"], out["dt"], out["A"], out["B"], out["C"],
+                   out["D"], out["dt_bias"], out["z"], out["state"]), ws, ws_bytes)
     return out

@@ -87,7 +87,8 @@ def desc(kind, step=False, **kw):
     if kind == "conv":
         d = dict(B=2, T=T, C=64, K=4, in_dtype=1, y_dtype=1, act=1, S=5)
         return K.ShortconvDesc(**{**d, **kw})
-    d = dict(B=2, T=T, C=64, G=4, in_dtype=1, y_dtype=1, act=1, eps=1e-5)
+    # positions past what one workgroup holds: the form with a workspace
+    d = dict(B=2, T=9000, C=64, G=4, in_dtype=1, y_dtype=1, act=1, eps=1e-5)
     return N.GroupnormDesc(**{**d, **kw})
 
 
