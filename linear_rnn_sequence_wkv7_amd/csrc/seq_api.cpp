@@ -33,6 +33,10 @@ struct Arrays {
         it[n++] = {{p, bytes, name}, written};
         return WKV7_OK;
     }
+    // An optional array of int32 (its own alignment is checked with the descriptor).
+    void index(const int32_t* p, int64_t count, const char* name) {
+        if (p) it[n++] = {{p, count * 4, name}, false};
+    }
     // Every written array shares no byte with another; `a` may be `b` itself (in place).
     int disjoint(const void* a = nullptr, const void* b = nullptr) const {
         for (int i = 0; i < n; ++i)
@@ -98,6 +102,7 @@ int ssm_desc_check(const ssm_desc* d, bool step, SsmParams* p) {
         return fail(WKV7_EUNSUPPORTED, "B=%d, T=%d, C=%d or S=%d too large", d->B, d->T, d->C, d->S);
     // Offsets within 128 rows are 32-bit.
     if (d->C >= (1 << 22) || int64_t(G) * d->N >= (1 << 22)) return fail(WKV7_EUNSUPPORTED, "C=%d or G*N=%lld too large", d->C, (long long)(int64_t(G) * d->N));
+    if (bt > (int64_t(1) << 38) / (int64_t(G) * d->N)) return fail(WKV7_EUNSUPPORTED, "B*T*G*N too large");
     *p = SsmParams{};
     p->B = d->B; p->T = d->T; p->C = d->C; p->N = d->N; p->G = G; p->S = d->S;
     p->in_bf16 = d->in_dtype == WKV7_BF16; p->y_bf16 = d->y_dtype == WKV7_BF16; p->softplus = d->dt_softplus;
@@ -111,13 +116,14 @@ int ssm_inputs(const SsmParams& p, Arrays& a) {
     const bool some = row > 0;
     WKV7_TRY(a.add(p.x, row * e, "x", true, false));
     WKV7_TRY(a.add(p.dt, row * e, "dt", true, false));
-    WKV7_TRY(a.add(p.A, int64_t(p.C) * p.N * 4, "A", some, false));
+    WKV7_TRY(a.add(p.A, int64_t(p.C) * p.N * 4, "A", true, false));
     WKV7_TRY(a.add(p.Bm, some ? vec * e : 0, "Bm", true, false));
     WKV7_TRY(a.add(p.Cm, some ? vec * e : 0, "Cm", true, false));
     WKV7_TRY(a.add(p.D, int64_t(p.C) * 4, "D", false, false));
     WKV7_TRY(a.add(p.dt_bias, int64_t(p.C) * 4, "dt_bias", false, false));
     WKV7_TRY(a.add(p.z, row * e, "z", false, false));
-    return a.add(p.lengths, p.lengths ? int64_t(p.B) * 4 : 0, "lengths", false, false);
+    a.index(p.lengths, p.B, "lengths");
+    return WKV7_OK;
 }
 int64_t ssm_ck_bytes(const SsmParams& p) { return int64_t(p.B) * p.nck * p.C * p.N * 4; }
 
@@ -148,7 +154,8 @@ int conv_inputs(const ConvParams& p, Arrays& a) {
     WKV7_TRY(a.add(p.x, row * esize(p.in_bf16), "x", true, false));
     WKV7_TRY(a.add(p.w, int64_t(p.C) * p.K * 4, "w", row > 0, false));
     WKV7_TRY(a.add(p.bias, int64_t(p.C) * 4, "bias", false, false));
-    return a.add(p.lengths, p.lengths ? int64_t(p.B) * 4 : 0, "lengths", false, false);
+    a.index(p.lengths, p.B, "lengths");
+    return WKV7_OK;
 }
 
 // ---------------------------------------------------------------- norm
@@ -178,7 +185,8 @@ int norm_inputs(const NormParams& p, Arrays& a) {
     WKV7_TRY(a.add(p.weight, int64_t(p.C) * 4, "weight", false, false));
     WKV7_TRY(a.add(p.bias, int64_t(p.C) * 4, "bias", false, false));
     WKV7_TRY(a.add(p.gate, row * esize(p.in_bf16), "gate", false, false));
-    return a.add(p.lengths, p.lengths ? int64_t(p.B) * 4 : 0, "lengths", false, false);
+    a.index(p.lengths, p.B, "lengths");
+    return WKV7_OK;
 }
 
 hipStream_t stream_of(void* s) { return reinterpret_cast<hipStream_t>(s); }
@@ -211,7 +219,6 @@ int ssm_forward(const ssm_desc* desc, const void* x, const void* dt, const float
     WKV7_TRY(a.add(checkpoints, ssm_ck_bytes(p), "checkpoints", false, true));
     WKV7_TRY(a.disjoint(state_in, state_out));
     if (int64_t(p.B) * p.C == 0 || (p.T == 0 && !state_out)) return WKV7_OK;
-    if (p.T == 0 && !A) p.A = nullptr;
     WKV7_TRY(check_device());
     return finish_launch(launch_ssm_forward(p, stream_of(stream)), "ssm");
 }
@@ -227,7 +234,7 @@ int ssm_step(const ssm_desc* desc, const void* x, const void* dt, const float* A
     p.s0 = state; p.s1 = state; p.index = state_index; p.y = y;
     Arrays a;
     WKV7_TRY(ssm_inputs(p, a));
-    if (state_index) a.it[a.n++] = {{state_index, int64_t(p.B) * 4, "state_index"}, false};
+    a.index(state_index, p.B, "state_index");
     WKV7_TRY(a.add(state, int64_t(p.B) * p.C == 0 ? 0 : int64_t(p.S) * p.C * p.N * 4, "state", true, true));
     WKV7_TRY(a.add(y, int64_t(p.B) * p.C * esize(p.y_bf16), "y", true, true));
     WKV7_TRY(a.disjoint());
@@ -310,7 +317,7 @@ int shortconv_step(const shortconv_desc* desc, const void* x, const float* w, co
     p.x = x; p.w = w; p.bias = bias; p.s0 = state; p.s1 = state; p.index = state_index; p.y = y;
     Arrays a;
     WKV7_TRY(conv_inputs(p, a));
-    if (state_index) a.it[a.n++] = {{state_index, int64_t(p.B) * 4, "state_index"}, false};
+    a.index(state_index, p.B, "state_index");
     WKV7_TRY(a.add(state, int64_t(p.B) * p.C == 0 ? 0 : int64_t(p.S) * (p.K - 1) * p.C * esize(p.in_bf16), "state", true, true));
     WKV7_TRY(a.add(y, int64_t(p.B) * p.C * esize(p.y_bf16), "y", true, true));
     WKV7_TRY(a.disjoint());

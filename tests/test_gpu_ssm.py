@@ -149,6 +149,32 @@ def test_padding_values_do_not_matter():
     np.testing.assert_array_equal(out[0]["s"][1], x["state"][1])
 
 
+def test_no_tokens():
+    """T = 0: the state goes over, its gradient back, and the parameters have none."""
+    t = torch()
+    B, C, N = 2, 20, 16
+    x = S.scan_inputs(1, B, 0, C, N, dtype="bf16", state=True)
+    a, kw = dev_args(x)
+    st = to_dev(x["state"])
+    y, s = M().ssm_forward(*a, state=st, **kw)
+    assert y.shape == (B, 0, C) and t.equal(s, st)
+    _, s = M().ssm_forward(*a, **kw)
+    assert bool((s == 0).all())
+    ds = t.randn(B, C, N, device="cuda")
+    g = M().ssm_backward(*a, y, dstate=ds, state=st, **kw)
+    assert t.equal(g["state"], ds)
+    assert all(bool((g[k] == 0).all()) for k in ("A", "D", "dt_bias"))
+
+
+def test_lengths_from_the_middle_of_a_tensor():
+    t = torch()
+    x = S.scan_inputs(3, 2, 20, 8, 16, dtype="f32")
+    a, kw = dev_args(x)
+    y1, s1 = M().ssm_forward(*a, **kw, lengths=t.tensor([99, 7, 20], dtype=t.int32, device="cuda")[1:])
+    y2, s2 = M().ssm_forward(*a, **kw, lengths=lens([7, 20]))
+    assert t.equal(y1, y2) and t.equal(s1, s2)
+
+
 def test_lengths_out_of_range_are_held():
     x = S.scan_inputs(3, 2, 20, 8, 16, dtype="f32")
     a, kw = dev_args(x)
@@ -235,6 +261,33 @@ def test_in_place_state_and_repeatability():
     g2 = M().ssm_backward(*a, dy, **kw)
     for k in g1:
         assert torch().equal(g1[k], g2[k]), k
+
+
+@pytest.mark.parametrize("T,C,lens_", [(500, 48, None), (1000, 32, [1000, 777])])
+def test_long_sequences_in_rounds(T, C, lens_):
+    """Several rounds of the kernels, each taking up where the other left (also the checkpoints), for
+    every number of runs: few channels here, many sequences below."""
+    x = S.scan_inputs(T, 2, T, C, 16, dtype="f32", state=True)
+    dy = np.random.default_rng(T).standard_normal((2, T, C)).astype(np.float32)
+    a, kw = dev_args(x)
+    kw.update(state=to_dev(x["state"]), lengths=lens(lens_))
+    (y_ref, s_ref), (y_tol, s_tol) = S.scan_bounds(x, T, lens_, True, B=2, Cg=C)
+    saved = torch().empty(M().ssm_checkpoint_bytes(2, T, C, 16), dtype=torch().uint8, device="cuda")
+    y, s = M().ssm_forward(*a, **kw, checkpoints=saved)
+    S.check("y", to_host(y), y_ref, y_tol)
+    S.check("state", to_host(s), s_ref, s_tol)
+    ref, tol = S.scan_bounds(x, T, lens_, True, dy=dy, B=2, Cg=C)
+    g = M().ssm_backward(*a, to_dev(dy), checkpoints=saved, **kw)
+    for k in ref:
+        S.check("d" + k, to_host(g[k]), ref[k], tol[k])
+    # the same two sequences among many: other numbers of runs
+    for copies in (100, 600):
+        rep = lambda v: v.repeat(copies, *([1] * (v.dim() - 1)))
+        am = tuple(rep(v) if v.dim() >= 3 else v for v in a)
+        km = {k: rep(v) if v is not None and (v.dim() == 3 or k == "lengths") else v for k, v in kw.items()}
+        ym, sm = M().ssm_forward(*am, **km)
+        S.check("y", to_host(ym[-2:]), y_ref, y_tol)
+        S.check("state", to_host(sm[-2:]), s_ref, s_tol)
 
 
 def test_step_sizes_at_the_ends():

@@ -166,7 +166,8 @@ def test_workspace_sizes(fn):
 BAD = {
     "ssm": [(dict(B=-1), 1), (dict(T=-1), 1), (dict(C=-1), 1), (dict(G=-1), 1), (dict(N=0), 1), (dict(N=65), 2), (dict(G=3), 1),
             (dict(in_dtype=2), 1), (dict(y_dtype=-1), 1), (dict(dt_softplus=2), 1), (dict(reserved=1), 1), (dict(lengths=BASE + 2), 1),
-            (dict(B=1 << 30, C=1 << 20), 2), (dict(T=2147483647), 2)],
+            (dict(B=1 << 30, C=1 << 20), 2), (dict(T=2147483647), 2), (dict(C=1 << 22), 2), (dict(C=1 << 18, G=1 << 18, N=16), 2),
+            (dict(B=1 << 15, T=1 << 12, C=1 << 10, G=1 << 10, N=64), 2)],
     "conv": [(dict(B=-1), 1), (dict(T=-1), 1), (dict(C=-1), 1), (dict(K=0), 1), (dict(K=1), 2), (dict(K=5), 2), (dict(in_dtype=2), 1),
              (dict(y_dtype=5), 1), (dict(act=2), 1), (dict(lengths=BASE + 1), 1), (dict(B=1 << 30, C=1 << 20), 2)],
     "norm": [(dict(B=-1), 1), (dict(T=-1), 1), (dict(C=-1), 1), (dict(G=0), 1), (dict(G=5), 1), (dict(in_dtype=2), 1), (dict(y_dtype=5), 1),
@@ -190,6 +191,22 @@ def test_descriptors(fn):
         assert call(fn, desc(kind, True, S=-1)) == W.WKV7_EINVAL
         assert call(fn, desc(kind, True, S=1), state_index=None) == W.WKV7_EINVAL
         assert "state_index" in message()
+
+
+def test_lengths_need_the_alignment_of_an_int32():
+    """A slice of a tensor of lengths is taken (nothing to do here: no device call)."""
+    for off in (4, 8, 12):
+        assert call("ssm_forward", desc("ssm", B=0, lengths=BASE + off)) == W.WKV7_OK
+        assert call("shortconv_forward", desc("conv", B=0, lengths=BASE + off)) == W.WKV7_OK
+        assert call("groupnorm_forward", desc("norm", B=0, lengths=BASE + off)) == W.WKV7_OK
+        assert call("ssm_step", desc("ssm", True, B=0), state_index=BASE + off) == W.WKV7_OK
+
+
+def test_scan_without_tokens_still_needs_its_rates():
+    """The kernel reads A whatever T is."""
+    assert call("ssm_forward", desc("ssm", T=0), A=None) == W.WKV7_EINVAL
+    assert call("ssm_backward", desc("ssm", T=0), A=None) == W.WKV7_EINVAL
+    assert "A is NULL" in message()
 
 
 def test_size_queries():
