@@ -22,7 +22,7 @@ struct SsmParams {
     void* y;
     float *s1, *ck;
     int nck;                          // checkpoints of a sequence
-    bool vec_c, vec_n;                // set by the launchers: aligned runs of channels / states
+    bool vec_n;                       // set by the step's launcher: runs of 4 states are aligned
     // backward
     const void* dy;
     const float* ds1;

@@ -298,6 +298,7 @@ __global__ __launch_bounds__(64 * WS * WT, waves_of(WS, WT, VEC)) void ssm_backw
                 }
                 // over the rows, and the channels: as soon as the pair of tokens is there
                 if constexpr (j < 2) {
+                    asm("s_nop 1" : "+v"(y[j]), "+v"(us[j]));   // from their write, which the compiler does not see, to the swap
                     y[j] = halve<32>(y[j], y[j + 2], lane);
                     us[j] = halve<32>(us[j], us[j + 2], lane);
                     ds[j] = halve<32>(ds[j], ds[j + 2], lane);

@@ -8,23 +8,38 @@
 // for every channel and state, so the readout is no matrix product: the work is
 // elementwise, a product, an exponential, the update and the readout per state.
 //
-// Lanes: LPC neighbouring lanes share a channel, each with NPL of its states in
-// registers (LPC NPL >= N, unused states have A = B = C = 0), so a wave has
-// 64 / LPC channels.  The WT waves of a workgroup have the same channels and
-// consecutive runs of 16 tokens, which is how few channels still fill the chip:
-// each wave first runs its tokens from a zero state, which gives its state H and,
-// from the sum of its d_t, the factor P that an incoming state is multiplied by;
-// the pairs (P, H) go through LDS, every wave composes those before it to its
-// incoming state and all of them to the next round's, and runs its tokens again
-// with the decays kept in registers.  One barrier a round; the pairs are double
-// buffered.
+// Lanes: a wave has 16 channels; lane (q, c) of its 4 rows of 16 lanes has NPL
+// states of channel c in registers, q NPL and on (4 NPL >= N, unused states have
+// A = B = C = 0).  B and C of 16 tokens lie across a row, token t in lane t, and an
+// operand modifier hands lane t's to the whole row when token t comes: no LDS
+// traffic and no extra instruction, which is why a row has 16 channels and not
+// some states of fewer.  The readout is left in four parts, one a row, that are
+// added where y is written.
 //
-// x, dt and z are loaded for the next round while this one computes, 4 lanes to a
-// token's channels; step sizes and products d x are formed there, once per
-// element, and change to the lanes' layout through LDS private to the wave, as
-// do B and C and, on the way back, y (summed over the LPC lanes by a transposing
-// butterfly that leaves each lane one token).  Everything is fp32 between the
+// Tokens: the WT waves of a workgroup have the same channels and consecutive runs
+// of 16 tokens, which is how few channels still fill the chip: each wave first runs
+// its tokens from a zero state, which gives its state H and, from the sum of its
+// d_t, the factor P that an incoming state is multiplied by; the pairs (P, H) go
+// through LDS, every wave composes those before it to its incoming state and all of
+// them to the next round's, and runs its tokens again with the decays kept in
+// registers.  One barrier a round; the pairs are double buffered.  That is one more
+// update per state and token than WT = 1 does, which is taken as soon as its waves
+// fill the chip.
+//
+// x, dt, z, B and C are loaded a round ahead as raw words (a conversion would wait
+// for them), 4 lanes to a token's channels, through descriptors that end with the
+// sequence, so that padding reads as zeros without a branch; step sizes and products
+// d x are formed there, once per element, and change to the lanes' layout through LDS
+// private to the wave, as y does on the way back.  Everything is fp32 between the
 // loads and the stores of y.
+//
+// Bound: the vector units.  A state and token needs a multiplication and an
+// exponential for its decay, a product, an update and a readout (two updates where
+// WT > 1); an exponential takes the time of two of the others and a half.  Measured at
+// N = 16, G = 1, bf16: 8 x 4096 tokens x 4096 channels 634 us (1.6 TB/s; 3.4e12
+// updates of a state a second), 1 x 2048 x 4096 59 us.  Tried and left: 2 states a
+// lane and twice the waves (786 and 72 us: the elements and barriers count twice), the
+// next round's elements formed between this one's updates (no faster).
 #include "seq_device.h"
 #include "seq_internal.h"
 
