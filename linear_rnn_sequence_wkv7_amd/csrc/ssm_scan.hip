@@ -56,8 +56,11 @@ constexpr int TP = 20;   // LDS row of 16 tokens, padded
 template <typename Tin, int NPL, int WT, bool VEC>
 __global__ __launch_bounds__(64 * WT) void ssm_scan_kernel(SsmParams g) {
     constexpr int ROUND = TW * WT, ES = int(sizeof(Tin));
-    __shared__ float s_d[WT][CH][TP], s_u[WT][CH][TP], s_y[WT][4][CH][TP];
-    __shared__ float s_p[WT > 1 ? 2 : 1][WT][NPL][64], s_h[WT > 1 ? 2 : 1][WT][NPL][64];
+    // Step sizes, products and the rows' parts of y; where a wave's decays stay in its registers y takes
+    // the place of the others.
+    constexpr int Y0 = WT > 1 ? 0 : 2;
+    __shared__ float s_e[WT][Y0 + 4][CH][TP];
+    __shared__ Pack<float, NPL> s_p[WT > 1 ? 2 : 1][WT][64], s_h[WT > 1 ? 2 : 1][WT][64];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
     // The workgroup's sequence, group and channels.
@@ -139,8 +142,8 @@ __global__ __launch_bounds__(64 * WT) void ssm_scan_kernel(SsmParams g) {
         for (int i = 0; i < E; ++i) {
             const float v = nx.dt.get(i) + bias[i];
             const float d = __uint_as_float(__float_as_uint(bit_select(soft, softplusf_(v), v)) & keep);
-            s_d[w][e0 + i][te] = d;
-            s_u[w][e0 + i][te] = d * nx.x.get(i);
+            s_e[w][0][e0 + i][te] = d;
+            s_e[w][1][e0 + i][te] = d * nx.x.get(i);
         }
     };
     // y of a round, from the rows' parts in LDS.
@@ -149,7 +152,7 @@ __global__ __launch_bounds__(64 * WT) void ssm_scan_kernel(SsmParams g) {
         float out[E];
         #pragma unroll
         for (int i = 0; i < E; ++i) {
-            const float y = fmaf(Dv[i], x_p.get(i), (s_y[w][0][e0 + i][te] + s_y[w][1][e0 + i][te]) + (s_y[w][2][e0 + i][te] + s_y[w][3][e0 + i][te]));
+            const float y = fmaf(Dv[i], x_p.get(i), (s_e[w][Y0][e0 + i][te] + s_e[w][Y0 + 1][e0 + i][te]) + (s_e[w][Y0 + 2][e0 + i][te] + s_e[w][Y0 + 3][e0 + i][te]));
             const float z = z_p.get(i);
             out[i] = y * fmaf(z, sigmoidf_(z), no_z);
         }
@@ -179,8 +182,8 @@ __global__ __launch_bounds__(64 * WT) void ssm_scan_kernel(SsmParams g) {
                 f32x4 d4, u4, y;
                 float hh[4][NPL];
                 if constexpr (WT == 1) {
-                    d4 = *reinterpret_cast<const f32x4*>(&s_d[w][ch][t4 * 4]);
-                    u4 = *reinterpret_cast<const f32x4*>(&s_u[w][ch][t4 * 4]);
+                    d4 = *reinterpret_cast<const f32x4*>(&s_e[w][0][ch][t4 * 4]);
+                    u4 = *reinterpret_cast<const f32x4*>(&s_e[w][1][ch][t4 * 4]);
                 }
                 static_for<4>([&](auto j_) {
                     constexpr int j = j_, tt = t4 * 4 + j;
@@ -191,14 +194,14 @@ __global__ __launch_bounds__(64 * WT) void ssm_scan_kernel(SsmParams g) {
                     }
                 });
                 row_dot4<t4 * 4, NPL>(Cv, hh, y);
-                *reinterpret_cast<f32x4*>(&s_y[w][q][ch][t4 * 4]) = y;
+                *reinterpret_cast<f32x4*>(&s_e[w][Y0 + q][ch][t4 * 4]) = y;
             });
         };
         if constexpr (WT > 1) {
             float a[TW][NPL], in_[TW][NPL], hl[NPL] = {}, ds = 0.f;
             static_for<TW / 4>([&](auto t4) {
-                const f32x4 d4 = *reinterpret_cast<const f32x4*>(&s_d[w][ch][t4 * 4]);
-                const f32x4 u4 = *reinterpret_cast<const f32x4*>(&s_u[w][ch][t4 * 4]);
+                const f32x4 d4 = *reinterpret_cast<const f32x4*>(&s_e[w][0][ch][t4 * 4]);
+                const f32x4 u4 = *reinterpret_cast<const f32x4*>(&s_e[w][1][ch][t4 * 4]);
                 static_for<4>([&](auto j_) {
                     constexpr int j = j_, tt = t4 * 4 + j;
                     ds += d4[j];
@@ -210,11 +213,14 @@ __global__ __launch_bounds__(64 * WT) void ssm_scan_kernel(SsmParams g) {
                     }
                 });
             });
+            Pack<float, NPL> P, H;
             #pragma unroll
             for (int i = 0; i < NPL; ++i) {
-                s_p[par][w][i][lane] = __builtin_amdgcn_exp2f(ds * A2[i]);
-                s_h[par][w][i][lane] = hl[i];
+                P.e[i] = __builtin_amdgcn_exp2f(ds * A2[i]);
+                H.e[i] = hl[i];
             }
+            s_p[par][w][lane] = P;
+            s_h[par][w][lane] = H;
             __syncthreads();
             float hc[NPL];   // the state before this wave's tokens; h goes on to the state after the round
             #pragma unroll
@@ -223,8 +229,9 @@ __global__ __launch_bounds__(64 * WT) void ssm_scan_kernel(SsmParams g) {
                     #pragma unroll
                     for (int i = 0; i < NPL; ++i) hc[i] = h[i];
                 }
+                const Pack<float, NPL> P = s_p[par][v][lane], H = s_h[par][v][lane];
                 #pragma unroll
-                for (int i = 0; i < NPL; ++i) h[i] = fmaf(s_p[par][v][i][lane], h[i], s_h[par][v][i][lane]);
+                for (int i = 0; i < NPL; ++i) h[i] = fmaf(P.e[i], h[i], H.e[i]);
             }
             if (g.ck && tw % SSM_CHECKPOINT_TOKENS == 0 && tw < g.T) checkpoint(tw, hc);
             run(hc, [&](int tt, int i, float) { return a[tt][i]; }, [&](auto j, auto t4, int i, float) { return in_[t4 * 4 + j][i]; });
