@@ -684,6 +684,8 @@ __global__ __launch_bounds__(NTS) void norm_slab_kernel(NormParams g, float* par
     }
 }
 
+constexpr int64_t kMaxThreads = int64_t(1) << 32;
+
 // Lanes of a group in the row form (0: the general form).
 int row_lanes(const NormParams& p) {
     const int Cg = p.C / p.G;
@@ -724,7 +726,7 @@ int slab_channels(const NormParams& p, bool bwd) {
 }
 int slab_positions(const NormParams& p, bool bwd) {
     const int Cg = p.C / p.G, V = slab_channels(p, bwd), slots = Cg / V;
-    if (p.T <= 1 || slots > NTS) return 0;
+    if (p.T <= 1 || slots > NTS || int64_t(p.B) * p.G * NTS >= kMaxThreads) return 0;
     const int apart = NTS / slots, r = (p.T + apart - 1) / apart;
     return r <= 4 ? 4 : r <= 8 ? 8 : r <= 16 && V < 8 && !bwd ? 16 : 0;   // (the backward has three arrays)
 }
@@ -736,6 +738,20 @@ int run_of(const NormParams& p) {
 }
 int runs_of(const NormParams& p) { return (p.T + run_of(p) - 1) / run_of(p); }
 int64_t up(int64_t x) { return (x + 255) & ~int64_t(255); }
+
+// The elementwise pass: slots of a workgroup, workgroups side by side, positions of a thread, workgroups.
+struct Apply {
+    int cols, ncol, per;
+    int64_t blocks;
+};
+Apply apply_of(const NormParams& p, int slots) {
+    const int cols = slots < NTG ? slots : NTG, ncol = (slots + cols - 1) / cols, at_once = NTG / cols;
+    // Positions of a thread: 8, fewer where that leaves less than 16 workgroups to a compute unit
+    // (3 x 1531 x 960 fp32: 18.6 us with 8, 8 with 1).
+    int per = 8;
+    while (per > 1 && int64_t(p.B) * p.T * ncol / (at_once * per) < 4096) per /= 2;
+    return {cols, ncol, per, (p.T + int64_t(per) * at_once - 1) / (int64_t(per) * at_once) * p.B * ncol};
+}
 
 template <typename Tin, int LG>
 hipError_t launch_rows(const NormParams& p, bool bwd, hipStream_t stream) {
@@ -797,13 +813,8 @@ hipError_t launch_general(const NormParams& p, bool bwd, hipStream_t stream) {
     const int slots = p.C / V, runs = runs_of(p), run_len = run_of(p);
     const int64_t threads = int64_t(p.B) * runs * slots;
     const dim3 g1{unsigned((threads + NTG - 1) / NTG)}, g2{unsigned(int64_t(p.B) * p.G)};
-    const int cols = slots < NTG ? slots : NTG, ncol = (slots + cols - 1) / cols, at_once = NTG / cols;
-    // Positions of a thread: 8, fewer where that leaves less than 16 workgroups to a compute unit
-    // (3 x 1531 x 960 fp32: 18.6 us with 8, 8 with 1).
-    int per = 8;
-    while (per > 1 && int64_t(p.B) * p.T * ncol / (at_once * per) < 4096) per /= 2;
-    const int64_t chunks = (p.T + int64_t(per) * at_once - 1) / (int64_t(per) * at_once);
-    const dim3 g3{unsigned(chunks * p.B * ncol)};
+    const auto [cols, ncol, per, blocks] = apply_of(p, slots);
+    const dim3 g3{unsigned(blocks)};
     float* ws = static_cast<float*>(p.ws);
     if (!bwd) {
         float *mean = p.mean, *rstd = p.rstd;
@@ -863,6 +874,25 @@ hipError_t launch_in(const NormParams& p, bool bwd, hipStream_t stream) {
 
 }  // namespace
 
+int64_t groupnorm_threads(const NormParams& p, bool bwd) {
+    if (int64_t(p.B) * p.T * p.C == 0) return 0;
+    int64_t n;
+    if (row_lanes(p)) {
+        const Rows r = rows_of(p, bwd);
+        n = r.nrow * r.ncol * NTG;
+    } else if (wave_runs(p)) {
+        n = wave_rows(p, bwd) * p.G * 64 + NTG;
+    } else if (slab_positions(p, bwd)) {
+        n = int64_t(p.B) * p.G * NTS;
+    } else {
+        const int slots = p.C / channels_per_thread(p);
+        const int64_t stats = int64_t(p.B) * runs_of(p) * slots + NTG, join = int64_t(p.B) * p.G * NTG, apply = apply_of(p, slots).blocks * NTG;
+        n = stats > join ? stats : join;
+        n = n > apply ? n : apply;
+    }
+    const int64_t sums = bwd ? int64_t(p.C) * 64 + 1024 : 0;
+    return n > sums ? n : sums;
+}
 int64_t groupnorm_workspace(const NormParams& p) {
     if (int64_t(p.B) * p.T * p.C == 0 || row_lanes(p) || wave_runs(p) || slab_positions(p, false)) return 0;
     const int64_t slots = p.C / channels_per_thread(p);

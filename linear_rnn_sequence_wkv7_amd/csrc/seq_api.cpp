@@ -81,6 +81,11 @@ int check_index(const int32_t* index, int B, int S) {
 }
 int64_t esize(bool bf16) { return bf16 ? 2 : 4; }
 
+int check_threads(int64_t threads) {
+    if (threads >> 32) return fail(WKV7_EUNSUPPORTED, "the call needs %lld threads in one launch; less than 2^32 are supported", (long long)threads);
+    return WKV7_OK;
+}
+
 // ---------------------------------------------------------------- scan
 
 int ssm_desc_check(const ssm_desc* d, bool step, SsmParams* p) {
@@ -219,6 +224,7 @@ int ssm_forward(const ssm_desc* desc, const void* x, const void* dt, const float
     WKV7_TRY(a.add(checkpoints, ssm_ck_bytes(p), "checkpoints", false, true));
     WKV7_TRY(a.disjoint(state_in, state_out));
     if (int64_t(p.B) * p.C == 0 || (p.T == 0 && !state_out)) return WKV7_OK;
+    WKV7_TRY(check_threads(ssm_forward_threads(p)));
     WKV7_TRY(check_device());
     return finish_launch(launch_ssm_forward(p, stream_of(stream)), "ssm");
 }
@@ -239,6 +245,7 @@ int ssm_step(const ssm_desc* desc, const void* x, const void* dt, const float* A
     WKV7_TRY(a.add(y, int64_t(p.B) * p.C * esize(p.y_bf16), "y", true, true));
     WKV7_TRY(a.disjoint());
     if (int64_t(p.B) * p.C == 0) return WKV7_OK;
+    WKV7_TRY(check_threads(ssm_step_threads(p)));
     WKV7_TRY(check_device());
     return finish_launch(launch_ssm_step(p, stream_of(stream)), "ssm step");
 }
@@ -286,6 +293,7 @@ int ssm_backward(const ssm_desc* desc, const void* x, const void* dt, const floa
     WKV7_TRY(a.workspace(workspace, workspace_bytes, ssm_backward_workspace(p, !checkpoints)));
     WKV7_TRY(a.disjoint());
     if (p.C == 0 && vec == 0) return WKV7_OK;
+    WKV7_TRY(check_threads(ssm_backward_threads(p)));
     WKV7_TRY(check_device());
     return finish_launch(launch_ssm_backward(p, stream_of(stream)), "ssm backward");
 }
@@ -304,6 +312,7 @@ int shortconv_forward(const shortconv_desc* desc, const void* x, const float* w,
     WKV7_TRY(a.add(state_out, st, "state_out", false, true));
     WKV7_TRY(a.disjoint(state_in, state_out));
     if (int64_t(p.B) * p.C == 0) return WKV7_OK;
+    WKV7_TRY(check_threads(shortconv_forward_threads(p)));
     WKV7_TRY(check_device());
     return finish_launch(launch_shortconv_forward(p, stream_of(stream)), "shortconv");
 }
@@ -322,6 +331,7 @@ int shortconv_step(const shortconv_desc* desc, const void* x, const float* w, co
     WKV7_TRY(a.add(y, int64_t(p.B) * p.C * esize(p.y_bf16), "y", true, true));
     WKV7_TRY(a.disjoint());
     if (int64_t(p.B) * p.C == 0) return WKV7_OK;
+    WKV7_TRY(check_threads(shortconv_step_threads(p)));
     WKV7_TRY(check_device());
     return finish_launch(launch_shortconv_step(p, stream_of(stream)), "shortconv step");
 }
@@ -355,6 +365,7 @@ int shortconv_backward(const shortconv_desc* desc, const void* x, const float* w
     WKV7_TRY(a.workspace(workspace, workspace_bytes, shortconv_backward_workspace(p)));
     WKV7_TRY(a.disjoint());
     if (p.C == 0) return WKV7_OK;
+    WKV7_TRY(check_threads(shortconv_backward_threads(p)));
     WKV7_TRY(check_device());
     return finish_launch(launch_shortconv_backward(p, stream_of(stream)), "shortconv backward");
 }
@@ -382,6 +393,7 @@ int groupnorm_forward(const groupnorm_desc* desc, const void* x, const float* we
     WKV7_TRY(a.workspace(workspace, workspace_bytes, groupnorm_workspace(p)));
     WKV7_TRY(a.disjoint());
     if (p.B == 0 || (int64_t(p.T) * p.C == 0 && !mean)) return WKV7_OK;
+    WKV7_TRY(check_threads(groupnorm_threads(p, false)));
     WKV7_TRY(check_device());
     return finish_launch(launch_groupnorm_forward(p, stream_of(stream)), "groupnorm");
 }
@@ -418,6 +430,7 @@ int groupnorm_backward(const groupnorm_desc* desc, const void* x, const float* w
     WKV7_TRY(a.workspace(workspace, workspace_bytes, groupnorm_backward_workspace(p)));
     WKV7_TRY(a.disjoint());
     if (p.C == 0) return WKV7_OK;
+    WKV7_TRY(check_threads(groupnorm_threads(p, true)));
     WKV7_TRY(check_device());
     return finish_launch(launch_groupnorm_backward(p, stream_of(stream)), "groupnorm backward");
 }

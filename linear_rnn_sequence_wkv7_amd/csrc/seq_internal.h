@@ -31,6 +31,10 @@ struct SsmParams {
     void* ws;
 };
 int64_t ssm_backward_workspace(const SsmParams& p, bool own_checkpoints);
+// The threads of a call's largest launch: HIP takes less than 2^32.
+int64_t ssm_forward_threads(const SsmParams& p);
+int64_t ssm_step_threads(const SsmParams& p);
+int64_t ssm_backward_threads(const SsmParams& p);
 hipError_t launch_ssm_forward(const SsmParams& p, hipStream_t stream);
 hipError_t launch_ssm_step(const SsmParams& p, hipStream_t stream);
 hipError_t launch_ssm_backward(const SsmParams& p, hipStream_t stream);
@@ -51,6 +55,9 @@ struct ConvParams {
     void* ws;
 };
 int64_t shortconv_backward_workspace(const ConvParams& p);
+int64_t shortconv_forward_threads(const ConvParams& p);
+int64_t shortconv_step_threads(const ConvParams& p);
+int64_t shortconv_backward_threads(const ConvParams& p);
 hipError_t launch_shortconv_forward(const ConvParams& p, hipStream_t stream);
 hipError_t launch_shortconv_step(const ConvParams& p, hipStream_t stream);
 hipError_t launch_shortconv_backward(const ConvParams& p, hipStream_t stream);
@@ -72,6 +79,7 @@ struct NormParams {
 };
 int64_t groupnorm_workspace(const NormParams& p);
 int64_t groupnorm_backward_workspace(const NormParams& p);
+int64_t groupnorm_threads(const NormParams& p, bool bwd);
 hipError_t launch_groupnorm_forward(const NormParams& p, hipStream_t stream);
 hipError_t launch_groupnorm_backward(const NormParams& p, hipStream_t stream);
 

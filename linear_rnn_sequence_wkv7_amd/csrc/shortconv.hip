@@ -391,6 +391,18 @@ hipError_t launch(const ConvParams& p, int what, hipStream_t stream) {
 
 }  // namespace
 
+int64_t shortconv_forward_threads(const ConvParams& p) {
+    if (int64_t(p.T) * p.C == 0) return 0;
+    const Runs r = runs_of(p, channels_per_thread(p, false), false);
+    return int64_t(p.B) * r.runs * r.slots + NTC;
+}
+int64_t shortconv_step_threads(const ConvParams& p) { return (p.C / channels_per_thread(p, false) / NTC + 1) * ((int64_t(p.B) + 1) / 2 + 512) * NTC; }
+int64_t shortconv_backward_threads(const ConvParams& p) {
+    if (int64_t(p.T) * p.C == 0) return 0;
+    const Runs r = runs_of(p, channels_per_thread(p, true), true);
+    const int64_t own = int64_t(p.B) * ((r.slots + 63) / 64) * ((r.runs + 3) / 4) * NTC, sums = int64_t(p.K + 1) * p.C * 32 + 1024;
+    return own > sums ? own : sums;
+}
 int64_t shortconv_backward_workspace(const ConvParams& p) {
     if (int64_t(p.B) * p.T * p.C == 0) return 0;
     const Runs r = runs_of(p, channels_per_thread(p, true), true);

@@ -461,20 +461,26 @@ int64_t up(int64_t x) { return (x + 255) & ~int64_t(255); }
 int64_t bc_bytes(const SsmParams& p) { return up(int64_t(blocks_of(p)) * p.B * p.T * p.G * 2 * p.N * 4); }
 int64_t par_bytes(const SsmParams& p) { return up(int64_t(p.B) * (int64_t(p.C) * p.N + 2 * p.C) * 4); }
 
+// Waves over the states and, where there are more tokens than one has, over them.
+constexpr int runs_for(int WS) { return WS <= 4 ? 4 : 2; }
+int states_waves(const SsmParams& p) { return p.N <= 8 ? 1 : p.N <= 16 ? 2 : p.N <= 32 ? 4 : 8; }
+
 template <typename Tin, typename Ty, int WS, bool VEC>
 hipError_t launch_ws(const SsmParams& p, const BwdWs& ws, hipStream_t stream) {
     const dim3 grid{unsigned(int64_t(p.B) * p.G * blocks_of(p))};
-    constexpr int WT = WS <= 4 ? 4 : 2;
+    constexpr int WT = runs_for(WS);
     if (p.T <= TW) hipLaunchKernelGGL((ssm_backward_kernel<Tin, Ty, WS, 1, VEC>), grid, dim3(64 * WS), 0, stream, p, ws);
     else hipLaunchKernelGGL((ssm_backward_kernel<Tin, Ty, WS, WT, VEC>), grid, dim3(64 * WS * WT), 0, stream, p, ws);
     return hipGetLastError();
 }
 template <typename Tin, typename Ty, bool VEC>
 hipError_t launch_vec(const SsmParams& p, const BwdWs& ws, hipStream_t stream) {
-    if (p.N <= 8) return launch_ws<Tin, Ty, 1, VEC>(p, ws, stream);
-    if (p.N <= 16) return launch_ws<Tin, Ty, 2, VEC>(p, ws, stream);
-    if (p.N <= 32) return launch_ws<Tin, Ty, 4, VEC>(p, ws, stream);
-    return launch_ws<Tin, Ty, 8, VEC>(p, ws, stream);
+    switch (states_waves(p)) {
+        case 1: return launch_ws<Tin, Ty, 1, VEC>(p, ws, stream);
+        case 2: return launch_ws<Tin, Ty, 2, VEC>(p, ws, stream);
+        case 4: return launch_ws<Tin, Ty, 4, VEC>(p, ws, stream);
+        default: return launch_ws<Tin, Ty, 8, VEC>(p, ws, stream);
+    }
 }
 template <typename Tin, typename Ty>
 hipError_t launch_types(const SsmParams& p, const BwdWs& ws, hipStream_t stream) {
@@ -487,6 +493,14 @@ hipError_t launch_types(const SsmParams& p, const BwdWs& ws, hipStream_t stream)
 int64_t ssm_backward_workspace(const SsmParams& p, bool own_checkpoints) {
     if (int64_t(p.B) * p.C == 0) return 0;
     return bc_bytes(p) + par_bytes(p) + (own_checkpoints ? up(int64_t(p.B) * p.nck * p.C * p.N * 4) : 0);
+}
+
+int64_t ssm_backward_threads(const SsmParams& p) {
+    if (p.C == 0) return 0;
+    const int ws = states_waves(p), wt = p.T <= TW ? 1 : runs_for(ws);
+    const int64_t own = int64_t(p.B) * p.G * blocks_of(p) * ws * wt * 64, sums = int64_t(p.B) * p.T * p.G * 2 * p.N * (p.N % 4 ? 4 : 1);
+    const int64_t first = ssm_forward_threads(p), most = own > sums ? own : sums;
+    return (most > first ? most : first) + 1024;
 }
 
 hipError_t launch_ssm_backward(const SsmParams& p, hipStream_t stream) {

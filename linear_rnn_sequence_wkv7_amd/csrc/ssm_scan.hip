@@ -265,13 +265,17 @@ __global__ __launch_bounds__(64 * WT) void ssm_scan_kernel(SsmParams g) {
     }
 }
 
+int64_t scan_blocks(const SsmParams& p) { return int64_t(p.B) * p.G * ((p.C / p.G + CH - 1) / CH); }
+// Waves over the tokens while the chip has room for them.
+int scan_waves(const SsmParams& p) {
+    const int64_t blocks = scan_blocks(p);
+    return p.N > 16 || blocks >= 2048 || p.T <= TW ? 1 : blocks >= 512 || p.T <= 4 * TW ? 4 : 8;
+}
+
 template <typename Tin, int NPL, bool VEC>
 hipError_t launch_scan_wt(const SsmParams& p, hipStream_t stream) {
-    const int Cg = p.C / p.G;
-    const int64_t blocks = int64_t(p.B) * p.G * ((Cg + CH - 1) / CH);
-    const dim3 grid{unsigned(blocks)};
-    // Waves over the tokens while the chip has room for them.
-    const int wt = NPL > 4 || blocks >= 2048 || p.T <= TW ? 1 : blocks >= 512 || p.T <= 4 * TW ? 4 : 8;
+    const dim3 grid{unsigned(scan_blocks(p))};
+    const int wt = scan_waves(p);
     if (wt == 1) hipLaunchKernelGGL((ssm_scan_kernel<Tin, NPL, 1, VEC>), grid, dim3(64), 0, stream, p);
     else if constexpr (NPL <= 4) {
         if (wt == 4) hipLaunchKernelGGL((ssm_scan_kernel<Tin, NPL, 4, VEC>), grid, dim3(256), 0, stream, p);
@@ -349,26 +353,44 @@ __global__ __launch_bounds__(SB) void ssm_step_kernel(SsmParams g) {
     }
 }
 
+// Lanes to a channel, rows to a workgroup (four where that leaves four workgroups to a compute unit),
+// workgroups.
+struct StepPlan {
+    int lanes, rows;
+    int64_t blocks;
+};
+StepPlan step_plan(const SsmParams& p) {
+    const int lanes = p.N <= 4 ? 1 : p.N <= 8 ? 2 : p.N <= 16 ? 4 : p.N <= 32 ? 8 : 16;
+    const int64_t ncb = (int64_t(p.C) * lanes + SB - 1) / SB;
+    const int rows = ncb * p.B >= 4096 ? 4 : 1;
+    return {lanes, rows, ncb * ((int64_t(p.B) + rows - 1) / rows)};
+}
+
 template <typename Tin, int LN>
-hipError_t launch_step_ln(const SsmParams& p, hipStream_t stream) {
-    const int64_t ncb = (p.C + SB / LN - 1) / (SB / LN);
-    // four rows to a workgroup where that leaves four workgroups to a compute unit
-    if (ncb * p.B >= 4096) hipLaunchKernelGGL((ssm_step_kernel<Tin, LN, 4>), dim3(unsigned(ncb * ((p.B + 3) / 4))), dim3(SB), 0, stream, p);
-    else hipLaunchKernelGGL((ssm_step_kernel<Tin, LN, 1>), dim3(unsigned(ncb * p.B)), dim3(SB), 0, stream, p);
+hipError_t launch_step_ln(const SsmParams& p, const StepPlan& s, hipStream_t stream) {
+    const dim3 grid{unsigned(s.blocks)};
+    if (s.rows == 4) hipLaunchKernelGGL((ssm_step_kernel<Tin, LN, 4>), grid, dim3(SB), 0, stream, p);
+    else hipLaunchKernelGGL((ssm_step_kernel<Tin, LN, 1>), grid, dim3(SB), 0, stream, p);
     return hipGetLastError();
 }
 
 template <typename Tin>
 hipError_t launch_step_in(SsmParams p, hipStream_t stream) {
     p.vec_n = p.N % 4 == 0;
-    if (p.N <= 4) return launch_step_ln<Tin, 1>(p, stream);
-    if (p.N <= 8) return launch_step_ln<Tin, 2>(p, stream);
-    if (p.N <= 16) return launch_step_ln<Tin, 4>(p, stream);
-    if (p.N <= 32) return launch_step_ln<Tin, 8>(p, stream);
-    return launch_step_ln<Tin, 16>(p, stream);
+    const StepPlan s = step_plan(p);
+    switch (s.lanes) {
+        case 1: return launch_step_ln<Tin, 1>(p, s, stream);
+        case 2: return launch_step_ln<Tin, 2>(p, s, stream);
+        case 4: return launch_step_ln<Tin, 4>(p, s, stream);
+        case 8: return launch_step_ln<Tin, 8>(p, s, stream);
+        default: return launch_step_ln<Tin, 16>(p, s, stream);
+    }
 }
 
 }  // namespace
+
+int64_t ssm_forward_threads(const SsmParams& p) { return p.C ? scan_blocks(p) * scan_waves(p) * 64 : 0; }
+int64_t ssm_step_threads(const SsmParams& p) { return step_plan(p).blocks * SB; }
 
 hipError_t launch_ssm_forward(const SsmParams& p, hipStream_t stream) {
     return p.in_bf16 ? launch_scan_in<bf16_t>(p, stream) : launch_scan_in<float>(p, stream);

@@ -54,13 +54,13 @@ def _lib():
 
 
 def groupnorm_workspace_bytes(B: int, T: int, C: int, G: int) -> int:
-    """Workspace bytes of groupnorm_forward for these sizes."""
-    return M.size(_lib().groupnorm_workspace_bytes, ctypes.byref(GroupnormDesc(B, T, C, G, eps=1.0)))
+    """Workspace bytes of groupnorm_forward for these sizes, of either dtype."""
+    return max(M.size(_lib().groupnorm_workspace_bytes, ctypes.byref(GroupnormDesc(B, T, C, G, d, d, eps=1.0))) for d in (0, 1))
 
 
 def groupnorm_backward_workspace_bytes(B: int, T: int, C: int, G: int) -> int:
-    """Workspace bytes of groupnorm_backward for these sizes."""
-    return M.size(_lib().groupnorm_backward_workspace_bytes, ctypes.byref(GroupnormDesc(B, T, C, G, eps=1.0)))
+    """Workspace bytes of groupnorm_backward for these sizes, of either dtype."""
+    return max(M.size(_lib().groupnorm_backward_workspace_bytes, ctypes.byref(GroupnormDesc(B, T, C, G, d, d, eps=1.0))) for d in (0, 1))
 
 
 def _inputs(x, G, weight, bias, gate, lengths):

@@ -149,3 +149,16 @@ def test_empty():
     g = M().groupnorm_backward(t.empty(0, 3, 16, device="cuda"), 4, t.empty(0, 3, 16, device="cuda"), t.empty(0, 4, device="cuda"),
                                t.empty(0, 4, device="cuda"), weight=w, bias=w)
     assert bool((g["weight"] == 0).all()) and bool((g["bias"] == 0).all())
+
+
+def test_more_groups_than_a_launch_of_whole_workgroups_takes():
+    """2^22 groups of two values.  With u = 2^-24 and M the larger value: the mean is off by 2 u M, a difference by 3 u M,
+    their square's mean by 6 u M |d| + 4 u d^2; so y = d rstd by 6 u M rstd + 4 u; 16 u (M rstd + 1) covers it."""
+    t = torch()
+    x = t.randn(1 << 21, 2, 2, device="cuda")
+    y, mean, rstd = M().groupnorm_forward(x, 2, eps=EPS)
+    xd = x.double()
+    d = xd - xd.mean(1, keepdim=True)
+    r = 1 / t.sqrt((d * d).mean(1, keepdim=True) + EPS)
+    tol = 16 * 2.0 ** -24 * (xd.abs().amax(1, keepdim=True) * r + 1)
+    assert bool(((y.double() - d * r).abs() <= tol).all())

@@ -202,11 +202,42 @@ def test_lengths_need_the_alignment_of_an_int32():
         assert call("ssm_step", desc("ssm", True, B=0), state_index=BASE + off) == W.WKV7_OK
 
 
+WIDE = {
+    # more threads than a launch takes, in arrays that fit a GPU's memory
+    "ssm_forward": dict(B=1 << 14, T=16, C=1 << 12, G=1 << 12, N=1),
+    "ssm_step": dict(B=1 << 27, C=1, N=1, S=1 << 27),
+    "ssm_backward": dict(B=1 << 15, T=17, C=1 << 12, N=16, G=1),
+    "shortconv_step": dict(B=1 << 26, C=1, K=2, S=1 << 26),
+    "shortconv_backward": dict(B=1 << 25, T=2, C=1),
+    "groupnorm_forward": dict(B=1 << 23, T=2, C=2, G=2),
+    "groupnorm_backward": dict(B=1 << 23, T=2, C=2, G=2),
+}
+
+
+@pytest.mark.parametrize("fn", WIDE)
+def test_refuses_more_threads_than_a_launch_takes(fn):
+    kind, names, optional, _ = CALLS[fn]
+    ptrs = {n: BASE + (i << 45) if n not in optional.split() else None for i, n in enumerate(names.split())}
+    d = desc(kind, fn.endswith("_step"), **WIDE[fn])
+    assert call(fn, d, **ptrs, ws_bytes=1 << 50) == W.WKV7_EUNSUPPORTED
+    assert "2^32" in message()
+
+
 def test_scan_without_tokens_still_needs_its_rates():
     """The kernel reads A whatever T is."""
     assert call("ssm_forward", desc("ssm", T=0), A=None) == W.WKV7_EINVAL
     assert call("ssm_backward", desc("ssm", T=0), A=None) == W.WKV7_EINVAL
     assert "A is NULL" in message()
+
+
+def test_norm_size_queries_hold_for_both_dtypes():
+    """The forms differ between the dtypes; the binding's query covers either."""
+    for T in (1, 2, 600, 1100, 1700, 2100, 3000, 9000):
+        for C, G in ((64, 4), (64, 1), (63, 1), (96, 2), (1024, 32)):
+            for dt in (0, 1):
+                d = ctypes.byref(desc("norm", T=T, C=C, G=G, in_dtype=dt, y_dtype=dt))
+                assert N._lib().groupnorm_workspace_bytes(d) <= N.groupnorm_workspace_bytes(2, T, C, G)
+                assert N._lib().groupnorm_backward_workspace_bytes(d) <= N.groupnorm_backward_workspace_bytes(2, T, C, G)
 
 
 def test_size_queries():
