@@ -10,6 +10,8 @@
  *     y_t = (sum_n Cm_t[g][n] h_t[n] + D x_t) * silu(z_t)    (D, z optional)
  *
  * Channels come in G groups of C / G consecutive ones; a group shares Bm and Cm.
+ * Runs of 16 tokens are composed from what they do to any incoming state, so a
+ * growing state (d_t A > 0) has to grow by a finite fp32 factor over 16 tokens.
  *
  * Layouts (row-major, contiguous):
  *     x, dt, z, y : [B, T, C]            Bm, Cm : [B, T, G, N]

@@ -8,7 +8,8 @@ raises.
 
 Shapes: x, dt, z, y [B, T, C]; Bm, Cm [B, T, G, N]; A [C, N] float32; D, dt_bias [C]
 float32; states [B, C, N] float32; lengths [B] int32.  x, dt, z, Bm, Cm are all
-float32 or all bfloat16; everything is contiguous.
+float32 or all bfloat16; everything is contiguous and starts on 16 bytes (lengths and
+state_index on 4).
 """
 from __future__ import annotations
 
