@@ -118,7 +118,6 @@ __global__ __launch_bounds__(64 * WS * WT, waves_of(WS, WT, VEC)) void ssm_backw
     }
     // A thread's elements: token te, channels e0 .. e0 + E of its run (WS = 8: the first half's threads).
     const int idx = (s * 64 + lane) * E, te = idx >> 4 & 15, e0 = idx & 15, ne = idx < 256 ? nc - e0 : 0;
-    const bool el_in = ne > 0;
     float dD[E] = {}, dbias[E] = {};
     __shared__ float s_par[2][CH];   // dt_bias and D of the channels
     if (threadIdx.x < 2 * CH) {
@@ -131,7 +130,6 @@ __global__ __launch_bounds__(64 * WS * WT, waves_of(WS, WT, VEC)) void ssm_backw
 
     // Rows of a round through descriptors that end with the sequence: a padded token's values are 0.
     const int64_t erow = int64_t(g.C) * ES, vrow = int64_t(g.G) * g.N * ES, yrow = int64_t(g.C) * YS;
-    const uint32_t eoff = el_in ? uint32_t((w * TW + te) * g.C + c0 + e0) : 0u;
     const uint32_t voff = n0 < g.N ? uint32_t((w * TW + ch) * g.G * g.N + grp * g.N + n0) * ES : 0xfffffff0u;
     struct Inputs {
         Raw<Tin, E, VEC> x, dt, z;
@@ -143,6 +141,8 @@ __global__ __launch_bounds__(64 * WS * WT, waves_of(WS, WT, VEC)) void ssm_backw
         const int n = max(0, min(len - t0, ROUND));
         const int64_t row = b * g.T + t0;
         auto rows = [&](const void* p, int64_t width) { return buf_rsrc(static_cast<const char*>(p) + row * width, p ? n * width : 0); };
+        const int idx = opaque(s * 64 + lane) * E, te = idx >> 4 & 15, e0 = idx & 15, ne = idx < 256 ? nc - e0 : 0;
+        const uint32_t eoff = ne > 0 ? uint32_t((w * TW + te) * g.C + c0 + e0) : 0u;
         nx.dt.load(rows(g.dt, erow), eoff * ES, ne);
         nx.x.load(rows(g.x, erow), eoff * ES, ne);
         nx.z.load(rows(g.z, erow), eoff * ES, ne);
@@ -160,6 +160,7 @@ __global__ __launch_bounds__(64 * WS * WT, waves_of(WS, WT, VEC)) void ssm_backw
     const int rounds = (len + ROUND - 1) / ROUND;
     for (int t0 = rounds * ROUND; t0 < g.T; t0 += ROUND) {   // padding after the last round
         const float zero[E] = {};
+        const uint32_t eoff = uint32_t((w * TW + te) * g.C + c0 + e0);
         store(g.dx, t0, zero, eoff, ne);
         store(g.ddt, t0, zero, eoff, ne);
         if (g.z) store(g.dz, t0, zero, eoff, ne);
@@ -170,6 +171,8 @@ __global__ __launch_bounds__(64 * WS * WT, waves_of(WS, WT, VEC)) void ssm_backw
         float Bv[NPL], Cv[NPL], hin[NPL];
         const auto x_c = nx.x;
         {   // elements; a padded token, and a channel that is not there, have x = d = do = 0
+            const int idx = opaque(s * 64 + lane) * E, te = idx >> 4 & 15, e0 = idx & 15, ne = idx < 256 ? nc - e0 : 0;
+            const bool el_in = ne > 0;
             const uint32_t keep = tw + te < len && el_in ? ~0u : 0u;
             #pragma unroll
             for (int i = 0; i < E; ++i) {
@@ -461,16 +464,36 @@ int64_t up(int64_t x) { return (x + 255) & ~int64_t(255); }
 int64_t bc_bytes(const SsmParams& p) { return up(int64_t(blocks_of(p)) * p.B * p.T * p.G * 2 * p.N * 4); }
 int64_t par_bytes(const SsmParams& p) { return up(int64_t(p.B) * (int64_t(p.C) * p.N + 2 * p.C) * 4); }
 
-// Waves over the states and, where there are more tokens than one has, over them.
-constexpr int runs_for(int WS) { return WS <= 4 ? 4 : 2; }
+// Waves over the states, 8 to each.
 int states_waves(const SsmParams& p) { return p.N <= 8 ? 1 : p.N <= 16 ? 2 : p.N <= 32 ? 4 : 8; }
+bool vec_of(const SsmParams& p) { return p.N % 2 == 0 && ((!p.in_bf16 && !p.y_bf16) || (p.C % 2 == 0 && p.C / p.G % 2 == 0)); }
+// Token runs of a workgroup, as many as the chip has room for: 16 waves while it has a compute unit to
+// itself, then fewer, which saves the waits of many.  A round starts at a checkpoint, so more than 16
+// tokens take two runs or more.  1024 tokens, N = 16, us with 2, 4, 8 runs: 256 workgroups 145, 109, 99;
+// 512: 196, 173, 185; 1536: 454, 458, 528; 4096: 1105, 1183, 1403.  N = 8 with 4, 8: 256: 85, 70; 1024: 203,
+// 248.  512 tokens, N = 32, with 2, 4: 256: 103, 92; 512: 155, 168; 4096: 1123, 1357.
+int runs_of(const SsmParams& p) {
+    static_assert(SSM_CHECKPOINT_TOKENS == 2 * TW);
+    const int ws = states_waves(p);
+    const int64_t blocks = int64_t(p.B) * p.G * blocks_of(p);
+    if (p.T <= TW) return 1;
+    if (ws == 8) return 2;
+    if (ws == 4) return blocks <= 256 ? 4 : 2;
+    if (blocks <= 256 && p.T > 16 * TW && vec_of(p)) return 8;
+    return ws == 1 || blocks <= 1024 ? 4 : 2;
+}
 
 template <typename Tin, typename Ty, int WS, bool VEC>
 hipError_t launch_ws(const SsmParams& p, const BwdWs& ws, hipStream_t stream) {
     const dim3 grid{unsigned(int64_t(p.B) * p.G * blocks_of(p))};
-    constexpr int WT = runs_for(WS);
-    if (p.T <= TW) hipLaunchKernelGGL((ssm_backward_kernel<Tin, Ty, WS, 1, VEC>), grid, dim3(64 * WS), 0, stream, p, ws);
-    else hipLaunchKernelGGL((ssm_backward_kernel<Tin, Ty, WS, WT, VEC>), grid, dim3(64 * WS * WT), 0, stream, p, ws);
+    const int runs = runs_of(p);
+    if (runs == 1) hipLaunchKernelGGL((ssm_backward_kernel<Tin, Ty, WS, 1, VEC>), grid, dim3(64 * WS), 0, stream, p, ws);
+    if constexpr (WS >= 2)
+        if (runs == 2) hipLaunchKernelGGL((ssm_backward_kernel<Tin, Ty, WS, 2, VEC>), grid, dim3(128 * WS), 0, stream, p, ws);
+    if constexpr (WS <= 4)
+        if (runs == 4) hipLaunchKernelGGL((ssm_backward_kernel<Tin, Ty, WS, 4, VEC>), grid, dim3(256 * WS), 0, stream, p, ws);
+    if constexpr (WS <= 2 && VEC)
+        if (runs == 8) hipLaunchKernelGGL((ssm_backward_kernel<Tin, Ty, WS, 8, VEC>), grid, dim3(512 * WS), 0, stream, p, ws);
     return hipGetLastError();
 }
 template <typename Tin, typename Ty, bool VEC>
@@ -484,8 +507,7 @@ hipError_t launch_vec(const SsmParams& p, const BwdWs& ws, hipStream_t stream) {
 }
 template <typename Tin, typename Ty>
 hipError_t launch_types(const SsmParams& p, const BwdWs& ws, hipStream_t stream) {
-    const bool vec = p.N % 2 == 0 && ((!p.in_bf16 && !p.y_bf16) || (p.C % 2 == 0 && p.C / p.G % 2 == 0));
-    return vec ? launch_vec<Tin, Ty, true>(p, ws, stream) : launch_vec<Tin, Ty, false>(p, ws, stream);
+    return vec_of(p) ? launch_vec<Tin, Ty, true>(p, ws, stream) : launch_vec<Tin, Ty, false>(p, ws, stream);
 }
 
 }  // namespace
@@ -497,8 +519,7 @@ int64_t ssm_backward_workspace(const SsmParams& p, bool own_checkpoints) {
 
 int64_t ssm_backward_threads(const SsmParams& p) {
     if (p.C == 0) return 0;
-    const int ws = states_waves(p), wt = p.T <= TW ? 1 : runs_for(ws);
-    const int64_t own = int64_t(p.B) * p.G * blocks_of(p) * ws * wt * 64, sums = int64_t(p.B) * p.T * p.G * 2 * p.N * (p.N % 4 ? 4 : 1);
+    const int64_t own = int64_t(p.B) * p.G * blocks_of(p) * states_waves(p) * runs_of(p) * 64, sums = int64_t(p.B) * p.T * p.G * 2 * p.N * (p.N % 4 ? 4 : 1);
     const int64_t first = ssm_forward_threads(p), most = own > sums ? own : sums;
     return (most > first ? most : first) + 1024;
 }

@@ -290,6 +290,29 @@ def test_long_sequences_in_rounds(T, C, lens_):
         S.check("state", to_host(sm[-2:]), s_ref, s_tol)
 
 
+@pytest.mark.parametrize("N,T,copies", [(16, 300, 1), (16, 40, 200), (16, 40, 600), (16, 40, 1100), (8, 300, 1), (8, 40, 200), (32, 40, 1),
+                                        (32, 40, 150), (32, 40, 300), (64, 40, 1), (64, 40, 150), (15, 300, 1)])
+def test_gradients_of_many_sequences(N, T, copies):
+    """Two sequences, many times: every number of runs that the backward takes.  The parameters' gradients are the
+    copies' sums, within the bound for so large a batch."""
+    x = S.scan_inputs(N + copies, 2, T, 16, N, dtype="f32", state=True)
+    rng = np.random.default_rng(copies)
+    dy, ds = rng.standard_normal((2, T, 16)).astype(np.float32), rng.standard_normal((2, 16, N)).astype(np.float32)
+    ref, tol = S.scan_bounds(x, T, None, True, dy=dy, dstate=ds, B=2, Cg=16)
+    tol_all = S.scan_bounds(x, T, None, True, dy=dy, dstate=ds, B=2 * copies, Cg=16)[1]
+    rep = lambda v: v.repeat(copies, *([1] * (v.dim() - 1)))
+    a, kw = dev_args(x)
+    a = tuple(rep(v) if v.dim() >= 3 else v for v in a)
+    kw = {k: rep(v) if v is not None and v.dim() == 3 else v for k, v in kw.items()}
+    g = M().ssm_backward(*a, rep(to_dev(dy)), dstate=rep(to_dev(ds)), state=rep(to_dev(x["state"])), **kw)
+    for k in ref:
+        if k in ("A", "D", "dt_bias"):
+            S.check("d" + k, to_host(g[k]), copies * ref[k], copies * tol_all[k])
+        else:
+            S.check("d" + k, to_host(g[k][-2:]), ref[k], tol[k])
+            assert torch().equal(g[k][:2], g[k][-2:])
+
+
 def test_step_sizes_at_the_ends():
     """softplus far below zero keeps its relative accuracy, far above it is the identity; steps
     so long that a decay is 0 leave the newest token only."""
