@@ -118,6 +118,7 @@ __global__ __launch_bounds__(64 * WS * WT, waves_of(WS, WT, VEC)) void ssm_backw
     }
     // A thread's elements: token te, channels e0 .. e0 + E of its run (WS = 8: the first half's threads).
     const int idx = (s * 64 + lane) * E, te = idx >> 4 & 15, e0 = idx & 15, ne = idx < 256 ? nc - e0 : 0;
+    const bool el_in = ne > 0;
     float dD[E] = {}, dbias[E] = {};
     __shared__ float s_par[2][CH];   // dt_bias and D of the channels
     if (threadIdx.x < 2 * CH) {
@@ -130,6 +131,7 @@ __global__ __launch_bounds__(64 * WS * WT, waves_of(WS, WT, VEC)) void ssm_backw
 
     // Rows of a round through descriptors that end with the sequence: a padded token's values are 0.
     const int64_t erow = int64_t(g.C) * ES, vrow = int64_t(g.G) * g.N * ES, yrow = int64_t(g.C) * YS;
+    const uint32_t eoff = el_in ? uint32_t((w * TW + te) * g.C + c0 + e0) : 0u;
     const uint32_t voff = n0 < g.N ? uint32_t((w * TW + ch) * g.G * g.N + grp * g.N + n0) * ES : 0xfffffff0u;
     struct Inputs {
         Raw<Tin, E, VEC> x, dt, z;
@@ -141,8 +143,6 @@ __global__ __launch_bounds__(64 * WS * WT, waves_of(WS, WT, VEC)) void ssm_backw
         const int n = max(0, min(len - t0, ROUND));
         const int64_t row = b * g.T + t0;
         auto rows = [&](const void* p, int64_t width) { return buf_rsrc(static_cast<const char*>(p) + row * width, p ? n * width : 0); };
-        const int idx = opaque(s * 64 + lane) * E, te = idx >> 4 & 15, e0 = idx & 15, ne = idx < 256 ? nc - e0 : 0;
-        const uint32_t eoff = ne > 0 ? uint32_t((w * TW + te) * g.C + c0 + e0) : 0u;
         nx.dt.load(rows(g.dt, erow), eoff * ES, ne);
         nx.x.load(rows(g.x, erow), eoff * ES, ne);
         nx.z.load(rows(g.z, erow), eoff * ES, ne);
@@ -160,7 +160,6 @@ __global__ __launch_bounds__(64 * WS * WT, waves_of(WS, WT, VEC)) void ssm_backw
     const int rounds = (len + ROUND - 1) / ROUND;
     for (int t0 = rounds * ROUND; t0 < g.T; t0 += ROUND) {   // padding after the last round
         const float zero[E] = {};
-        const uint32_t eoff = uint32_t((w * TW + te) * g.C + c0 + e0);
         store(g.dx, t0, zero, eoff, ne);
         store(g.ddt, t0, zero, eoff, ne);
         if (g.z) store(g.dz, t0, zero, eoff, ne);
@@ -171,8 +170,6 @@ __global__ __launch_bounds__(64 * WS * WT, waves_of(WS, WT, VEC)) void ssm_backw
         float Bv[NPL], Cv[NPL], hin[NPL];
         const auto x_c = nx.x;
         {   // elements; a padded token, and a channel that is not there, have x = d = do = 0
-            const int idx = opaque(s * 64 + lane) * E, te = idx >> 4 & 15, e0 = idx & 15, ne = idx < 256 ? nc - e0 : 0;
-            const bool el_in = ne > 0;
             const uint32_t keep = tw + te < len && el_in ? ~0u : 0u;
             #pragma unroll
             for (int i = 0; i < E; ++i) {
