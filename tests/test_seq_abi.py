@@ -206,7 +206,7 @@ WIDE = {
     # more threads than a launch takes, in arrays that fit a GPU's memory
     "ssm_forward": dict(B=1 << 14, T=16, C=1 << 12, G=1 << 12, N=1),
     "ssm_step": dict(B=1 << 27, C=1, N=1, S=1 << 27),
-    "ssm_backward": dict(B=1 << 15, T=17, C=1 << 12, N=16, G=1),
+    "ssm_backward": dict(B=1 << 16, T=17, C=1 << 12, N=16, G=1),
     "shortconv_step": dict(B=1 << 26, C=1, K=2, S=1 << 26),
     "shortconv_backward": dict(B=1 << 25, T=2, C=1),
     "groupnorm_forward": dict(B=1 << 23, T=2, C=2, G=2),
