@@ -1,7 +1,7 @@
 // Device helpers of the per-channel operators (ssm_*.hip, shortconv.hip,
 // groupnorm.hip): short vectors of consecutive channels, the order of
-// workgroups over the XCDs, exact-enough softplus and SiLU, and the
-// column sum that joins partial gradients.
+// workgroups over the XCDs, loads through descriptors, softplus and SiLU, row
+// broadcasts and halving sums, and the lookup of a step's states.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -220,7 +220,7 @@ __device__ __forceinline__ float bit_select(uint32_t m, float a, float b) {
 }
 
 // lo where bit M of the lane is 0, hi where it is 1, each summed over the pair of lanes that
-// differ in it (8 and 4: over mirrored lanes of 16 and 8, which differ in the lower bits too).
+// differ in it.
 template <int M>
 __device__ __forceinline__ float halve(float lo, float hi, int lane) {
     if constexpr (M == 32) {
@@ -230,7 +230,8 @@ __device__ __forceinline__ float halve(float lo, float hi, int lane) {
         const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(lo), __float_as_uint(hi), false, false);
         return __uint_as_float(r[0]) + __uint_as_float(r[1]);
     } else {
-        constexpr int ctrl = M == 8 ? kDppRowMirror : M == 4 ? kDppRowHalfMirror : M == 2 ? kDppQuadXor2 : kDppQuadXor1;
+        static_assert(M <= 2);
+        constexpr int ctrl = M == 2 ? kDppQuadXor2 : kDppQuadXor1;
         const bool b = lane & M;
         return (b ? hi : lo) + dpp<ctrl>(b ? lo : hi);
     }
