@@ -72,6 +72,10 @@ __device__ __forceinline__ rsrc_t buf_rsrc(const void* p, int64_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, int(bytes > 0 ? bytes : 0), 0x00020000);
 }
 
+// An offset past any descriptor's end (they have less than 2^31 bytes), also with the offsets within a
+// load added: those must not come round to the start.
+constexpr uint32_t kNowhere = 0x80000000u;
+
 // E consecutive elements as they were loaded, for loads that are in flight while other work
 // goes on: nothing is computed from the registers until get().  WHOLE: they start on 4 bytes and
 // come in loads of up to 16 bytes; else one by one, those past the first n as 0.
@@ -85,7 +89,7 @@ struct Raw {
         if constexpr (!kWhole) {
             #pragma unroll
             for (int i = 0; i < E; ++i) {
-                const uint32_t o = i < n ? off + uint32_t(sizeof(T)) * i : 0xfffffff0u;
+                const uint32_t o = i < n ? off + uint32_t(sizeof(T)) * i : kNowhere;
                 if constexpr (sizeof(T) == 4) w[i] = __builtin_amdgcn_raw_buffer_load_b32(r, o, 0, 0);
                 else w[i] = uint32_t(__builtin_amdgcn_raw_buffer_load_b16(r, o, 0, 0));
             }

@@ -137,7 +137,7 @@ __global__ __launch_bounds__(64 * WS * WT, waves_of(WS, WT, VEC)) void ssm_backw
     // Rows of a round through descriptors that end with the sequence: a padded token's values are 0.
     const int64_t erow = int64_t(g.C) * ES, vrow = int64_t(g.G) * g.N * ES, yrow = int64_t(g.C) * YS;
     const uint32_t eoff = el_in ? uint32_t((w * TW + te) * g.C + c0 + e0) : 0u;
-    const uint32_t voff = n0 < g.N ? uint32_t((w * TW + ch) * g.G * g.N + grp * g.N + n0) * ES : 0xfffffff0u;
+    const uint32_t voff = n0 < g.N ? uint32_t((w * TW + ch) * g.G * g.N + grp * g.N + n0) * ES : kNowhere;
     struct Inputs {
         Raw<Tin, E, VEC> x, dt, z;
         Raw<Ty, E, VEC> dy;
@@ -155,7 +155,7 @@ __global__ __launch_bounds__(64 * WS * WT, waves_of(WS, WT, VEC)) void ssm_backw
         nx.b.load(rows(g.Bm, vrow), voff, g.N - n0);
         nx.c.load(rows(g.Cm, vrow), voff, g.N - n0);
         const rsrc_t ck = buf_rsrc(ws.ck + ((b * g.nck + t0 / SSM_CHECKPOINT_TOKENS) * g.C + c0) * g.N, int64_t(nc) * g.N * 4);
-        nx.h.load(ck, n0 < g.N ? uint32_t(ch * g.N + n0) * 4 : 0xfffffff0u, g.N - n0);
+        nx.h.load(ck, n0 < g.N ? uint32_t(ch * g.N + n0) * 4 : kNowhere, g.N - n0);
     };
     auto store = [&](void* p, int t0, const float* v, uint32_t eoff, int ne) {
         const int n = min(g.T - t0, ROUND);

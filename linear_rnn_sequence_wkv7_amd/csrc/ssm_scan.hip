@@ -96,7 +96,7 @@ __global__ __launch_bounds__(64 * WT) void ssm_scan_kernel(SsmParams g) {
     // Rows of a round through descriptors that end with the sequence, at offsets that stay the same:
     // a padded token's x, z, B and C are 0.
     const uint32_t eoff = uint32_t((w * TW + te) * g.C + c0 + e0);
-    const uint32_t voff = n0 < g.N ? uint32_t((w * TW + ch) * g.G * g.N + grp * g.N + n0) * ES : 0xfffffff0u;
+    const uint32_t voff = n0 < g.N ? uint32_t((w * TW + ch) * g.G * g.N + grp * g.N + n0) * ES : kNowhere;
     const int64_t erow = int64_t(g.C) * ES, vrow = int64_t(g.G) * g.N * ES, yrow = int64_t(g.C) * (g.y_bf16 ? 2 : 4);
     const char *xp = static_cast<const char*>(g.x) + b * g.T * erow, *dtp = static_cast<const char*>(g.dt) + b * g.T * erow;
     const char *zp = g.z ? static_cast<const char*>(g.z) + b * g.T * erow : xp;

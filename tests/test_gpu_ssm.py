@@ -48,6 +48,11 @@ CASES = [
     (2, 130, 9, 20, 1, "f32", [7, 130], True, True),
     (1, 200, 13, 64, 1, "f32", None, True, True),
     (2, 70, 10, 33, 5, "bf16", [70, 69], True, True),
+    (2, 50, 20, 24, 1, "f32", [50, 9], True, True),      # rows of lanes without states
+    (1, 50, 20, 24, 2, "bf16", None, True, True),
+    (2, 50, 20, 48, 1, "f32", None, True, True),
+    (1, 50, 20, 48, 2, "bf16", None, True, True),
+    (1, 50, 20, 40, 1, "f32", None, True, True),
     (600, 33, 16, 16, 1, "bf16", None, True, False),     # many sequences: fewer waves over the tokens
     (70, 40, 520, 4, 1, "f32", None, False, True),
     (3, 50, 0, 16, 1, "f32", None, True, True),
