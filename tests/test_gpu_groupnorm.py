@@ -112,6 +112,28 @@ def test_variance_far_from_zero(B, T, C, G):
     S.check("rstd", to_host(rstd), r_ref, 1e-4 * r_ref)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [1, 2, 5, 33])
+def test_every_small_group(T, dtype):
+    """Groups of 1 to 72 channels and some around the widths of a wave, with and without a gate."""
+    for Cg in [*range(1, 73), 126, 128, 130, 255, 257, 514]:
+        G, B = 1 + Cg % 3, 3
+        act, lengths = ("silu", [T, 0, (T + 1) // 2]) if Cg % 2 else ("none", None)
+        m = make(Cg, B, T, G * Cg, dtype, True, Cg % 4 < 2)
+        (y_ref, m_ref, r_ref), (y_tol, m_tol, r_tol) = S.norm_bounds(m["x"], G, m["weight"], m["bias"], m["gate"], act == "silu", EPS, lengths)
+        kw = dict(weight=to_dev(m["weight"]), bias=to_dev(m["bias"]), gate=to_dev(m["gate"]), act=act, lengths=lens(lengths))
+        x = to_dev(m["x"])
+        y, mean, rstd = M().groupnorm_forward(x, G, eps=EPS, **kw)
+        S.check(f"y {Cg}", to_host(y), y_ref, y_tol, bf16=dtype == "bf16")
+        S.check(f"mean {Cg}", to_host(mean), m_ref, m_tol)
+        S.check(f"rstd {Cg}", to_host(rstd), r_ref, r_tol)
+        ref, tol = S.norm_bounds(m["x"], G, m["weight"], m["bias"], m["gate"], act == "silu", EPS, lengths, dy=m["dy"])
+        g = M().groupnorm_backward(x, G, to_dev(m["dy"]), mean, rstd, **kw)
+        for k in ref:
+            if g[k] is not None:
+                S.check(f"d{k} {Cg}", to_host(g[k]), ref[k], tol[k], bf16=g[k].dtype == torch().bfloat16)
+
+
 def test_constant_groups():
     """A group of equal values has variance 0: y is act(bias) gate, rstd 1 / sqrt(eps)."""
     x = np.full((3, 1, 64), 2.0, np.float32)

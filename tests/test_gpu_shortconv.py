@@ -83,6 +83,26 @@ def test_backward(case, act):
         S.check("d" + k, to_host(g[k]), ref[k], tol[k], bf16=g[k].dtype == torch().bfloat16)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("K", [2, 3, 4])
+def test_every_small_size(K, dtype):
+    """Channels and tokens around the widths of a load, a run of tokens and the taps."""
+    for C in (1, 2, 3, 4, 6, 7, 8, 12, 15, 16, 24, 40, 260):
+        for T in (1, 2, 3, 4, 5, 7, 8, 9, 17, 33):
+            lengths = [T, max(0, T - K + 1)]
+            m = make(C * T, 2, T, C, K, dtype, C % 3 != 0, T % 2 == 0)
+            (y_ref, s_ref), (y_tol, _) = S.conv_bounds(m["x"], m["w"], m["bias"], m["state"], lengths, True)
+            kw = dict(bias=to_dev(m["bias"]), state=to_dev(m["state"]), lengths=lens(lengths), act="silu")
+            y, s = M().shortconv_forward(to_dev(m["x"]), to_dev(m["w"]), **kw)
+            S.check(f"y {C} {T}", to_host(y), y_ref, y_tol, bf16=dtype == "bf16")
+            np.testing.assert_array_equal(to_host(s), s_ref)
+            ref, tol = S.conv_bounds(m["x"], m["w"], m["bias"], m["state"], lengths, True, m["dy"], m["dstate"])
+            g = M().shortconv_backward(to_dev(m["x"]), to_dev(m["w"]), to_dev(m["dy"]), dstate=to_dev(m["dstate"]), **kw)
+            for k in ref:
+                if g[k] is not None:
+                    S.check(f"d{k} {C} {T}", to_host(g[k]), ref[k], tol[k], bf16=g[k].dtype == torch().bfloat16)
+
+
 def test_padding_values_do_not_matter():
     B, T, C, K = 3, 21, 16, 4
     lengths = [10, 0, 2]

@@ -102,6 +102,34 @@ def test_backward(case, kept):
         S.check("d" + k, to_host(g[k]), ref[k], tol[k], bf16=g[k].dtype == torch().bfloat16)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N", range(1, 65))
+def test_every_number_of_states(N, dtype):
+    """Forward, gradients and a step, with channels and groups of odd and even sizes."""
+    G, Cg = (1, 17) if N % 3 == 0 else (2, 10) if N % 3 == 1 else (3, 18)
+    B, T, C = 2, 37 + N % 3 * 16, G * Cg
+    x = S.scan_inputs(N, B, T, C, N, G, dtype, state=True)
+    lengths = [T, T // 2]
+    dy = S.as_dtype(np.random.default_rng(N).standard_normal((B, T, C)), dtype)
+    a, kw = dev_args(x)
+    kw.update(state=to_dev(x["state"]), lengths=lens(lengths))
+    (y_ref, s_ref), (y_tol, s_tol) = S.scan_bounds(x, T, lengths, True, B=B, Cg=Cg)
+    y, s = M().ssm_forward(*a, **kw)
+    S.check("y", to_host(y), y_ref, y_tol, bf16=dtype == "bf16")
+    S.check("state", to_host(s), s_ref, s_tol)
+    ref, tol = S.scan_bounds(x, T, lengths, True, dy=dy, B=B, Cg=Cg)
+    g = M().ssm_backward(*a, to_dev(dy), **kw)
+    for k in ref:
+        S.check("d" + k, to_host(g[k]), ref[k], tol[k], bf16=g[k].dtype == torch().bfloat16)
+    first = {k: None if v is None else v[:, :1] if k in ("x", "dt", "Bm", "Cm", "z") else v for k, v in x.items()}
+    (y_ref, s_ref), (y_tol, s_tol) = S.scan_bounds(first, 1, None, True, B=B, Cg=Cg)
+    one = lambda t: t[:, 0].contiguous()
+    st = to_dev(x["state"])
+    y = M().ssm_step(one(a[0]), one(a[1]), a[2], one(a[3]), one(a[4]), st, D=kw["D"], dt_bias=kw["dt_bias"], z=one(kw["z"]))
+    S.check("step y", to_host(y), y_ref[:, 0], y_tol[:, 0], bf16=dtype == "bf16")
+    S.check("step state", to_host(st), s_ref, s_tol)
+
+
 def test_gradient_against_differences():
     """The gradient along a direction against the forward's own central difference.  In fp32 a
     step of 2^-6 is off by its square (times the third derivative) and by the loss' rounding
