@@ -30,6 +30,14 @@ struct SsmParams {
     float *dA, *dD, *dbias, *ds0;
     void* ws;
 };
+// Rows of channels, of every group and in each type that a kernel moves them in, start on 4 bytes.
+inline bool channels_on_words(const SsmParams& p) { return (!p.in_bf16 && !p.y_bf16) || (p.C % 2 == 0 && p.C / p.G % 2 == 0); }
+// The forward and the backward, with npl states of a lane: runs of channels and of states move as whole
+// words, and no lane has only some of its states.
+inline bool ssm_forward_words(const SsmParams& p, int npl) {
+    return p.N % npl == 0 && (!p.in_bf16 || p.N % 2 == 0) && channels_on_words(p);
+}
+inline bool ssm_backward_words(const SsmParams& p) { return p.N % 2 == 0 && channels_on_words(p); }
 int64_t ssm_backward_workspace(const SsmParams& p, bool own_checkpoints);
 // The threads of a call's largest launch: HIP takes less than 2^32.
 int64_t ssm_forward_threads(const SsmParams& p);

@@ -468,7 +468,6 @@ int64_t par_bytes(const SsmParams& p) { return up(int64_t(p.B) * (int64_t(p.C) *
 
 // Waves over the states, 8 to each.
 int states_waves(const SsmParams& p) { return p.N <= 8 ? 1 : p.N <= 16 ? 2 : p.N <= 32 ? 4 : 8; }
-bool vec_of(const SsmParams& p) { return p.N % 2 == 0 && ((!p.in_bf16 && !p.y_bf16) || (p.C % 2 == 0 && p.C / p.G % 2 == 0)); }
 // Token runs of a workgroup, as many as the chip has room for: 16 waves while it has a compute unit to
 // itself, then fewer, which saves the waits of many.  A round starts at a checkpoint, so more than 16
 // tokens take two runs or more.  1024 tokens, N = 16, us with 2, 4, 8 runs: 256 workgroups 145, 109, 99;
@@ -481,7 +480,7 @@ int runs_of(const SsmParams& p) {
     if (p.T <= TW) return 1;
     if (ws == 8) return 2;
     if (ws == 4) return blocks <= 256 ? 4 : 2;
-    if (blocks <= 256 && p.T > 16 * TW && vec_of(p)) return 8;
+    if (blocks <= 256 && p.T > 16 * TW && ssm_backward_words(p)) return 8;
     return ws == 1 || blocks <= 1024 ? 4 : 2;
 }
 
@@ -509,7 +508,7 @@ hipError_t launch_vec(const SsmParams& p, const BwdWs& ws, hipStream_t stream) {
 }
 template <typename Tin, typename Ty>
 hipError_t launch_types(const SsmParams& p, const BwdWs& ws, hipStream_t stream) {
-    return vec_of(p) ? launch_vec<Tin, Ty, true>(p, ws, stream) : launch_vec<Tin, Ty, false>(p, ws, stream);
+    return ssm_backward_words(p) ? launch_vec<Tin, Ty, true>(p, ws, stream) : launch_vec<Tin, Ty, false>(p, ws, stream);
 }
 
 }  // namespace

@@ -51,8 +51,8 @@ constexpr int CH = 16;   // channels of a wave
 constexpr int E = 4;     // channels of a lane where it loads and stores elements
 constexpr int TP = 20;   // LDS row of 16 tokens, padded
 
-// VEC: every row of channels and of states starts on 4 bytes, for each group too, and no lane has
-// only some of its NPL states.
+// VEC: every row of channels (of the inputs and of y) and of states starts on 4 bytes, for each group
+// too, and no lane has only some of its NPL states.
 template <typename Tin, int NPL, int WT, bool VEC>
 __global__ __launch_bounds__(64 * WT) void ssm_scan_kernel(SsmParams g) {
     constexpr int ROUND = TW * WT, ES = int(sizeof(Tin));
@@ -287,8 +287,7 @@ hipError_t launch_scan_wt(const SsmParams& p, hipStream_t stream) {
 }
 template <typename Tin, int NPL>
 hipError_t launch_scan_n(const SsmParams& p, hipStream_t stream) {
-    const bool vec = p.N % NPL == 0 && (!p.in_bf16 || (p.C % 2 == 0 && p.C / p.G % 2 == 0 && p.N % 2 == 0));
-    return vec ? launch_scan_wt<Tin, NPL, true>(p, stream) : launch_scan_wt<Tin, NPL, false>(p, stream);
+    return ssm_forward_words(p, NPL) ? launch_scan_wt<Tin, NPL, true>(p, stream) : launch_scan_wt<Tin, NPL, false>(p, stream);
 }
 
 template <typename Tin>
