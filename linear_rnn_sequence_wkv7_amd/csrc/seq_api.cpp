@@ -6,6 +6,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 
 #include "../../include/wkv7.h"
 #include "seq_internal.h"
@@ -37,13 +38,13 @@ struct Arrays {
     void index(const int32_t* p, int64_t count, const char* name) {
         if (p) it[n++] = {{p, count * 4, name}, false};
     }
-    // Every written array shares no byte with another; `a` may be `b` itself (in place).
-    int disjoint(const void* a = nullptr, const void* b = nullptr) const {
+    // Every written array shares no byte with another; with `in_place`, state_out may be state_in itself.
+    int disjoint(bool in_place = false) const {
         for (int i = 0; i < n; ++i)
             for (int j = 0; j < n; ++j) {
                 if (i == j || !it[i].written || (it[j].written && j < i)) continue;
                 const Span &x = it[i].s, &y = it[j].s;
-                if (a && a == b && x.p == a && y.p == a) continue;
+                if (in_place && x.p == y.p && !std::strcmp(x.name, "state_out") && !std::strcmp(y.name, "state_in")) continue;
                 if (overlap(x.p, x.bytes, y.p, y.bytes)) return fail(WKV7_EINVAL, "%s overlaps %s", x.name, y.name);
             }
         return WKV7_OK;
@@ -222,7 +223,7 @@ int ssm_forward(const ssm_desc* desc, const void* x, const void* dt, const float
     WKV7_TRY(a.add(y, int64_t(p.B) * p.T * p.C * esize(p.y_bf16), "y", true, true));
     WKV7_TRY(a.add(state_out, st, "state_out", false, true));
     WKV7_TRY(a.add(checkpoints, ssm_ck_bytes(p), "checkpoints", false, true));
-    WKV7_TRY(a.disjoint(state_in, state_out));
+    WKV7_TRY(a.disjoint(true));
     if (int64_t(p.B) * p.C == 0 || (p.T == 0 && !state_out)) return WKV7_OK;
     WKV7_TRY(check_threads(ssm_forward_threads(p)));
     WKV7_TRY(check_device());
@@ -310,7 +311,7 @@ int shortconv_forward(const shortconv_desc* desc, const void* x, const float* w,
     WKV7_TRY(a.add(state_in, st, "state_in", false, false));
     WKV7_TRY(a.add(y, int64_t(p.B) * p.T * p.C * esize(p.y_bf16), "y", true, true));
     WKV7_TRY(a.add(state_out, st, "state_out", false, true));
-    WKV7_TRY(a.disjoint(state_in, state_out));
+    WKV7_TRY(a.disjoint(true));
     if (int64_t(p.B) * p.C == 0) return WKV7_OK;
     WKV7_TRY(check_threads(shortconv_forward_threads(p)));
     WKV7_TRY(check_device());

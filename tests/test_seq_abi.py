@@ -143,6 +143,18 @@ def test_written_arrays_share_no_byte(fn):
         assert "overlaps" in message()
 
 
+@pytest.mark.parametrize("fn", ["ssm_forward", "shortconv_forward"])
+def test_nothing_else_joins_a_state_in_place(fn):
+    """A state that is moved in place shares its bytes with no third array, at its start either."""
+    _, names, _, _ = CALLS[fn]
+    names = names.split()
+    st = BASE + names.index("state_in") * SP
+    for o in names:
+        if o not in ("state_in", "state_out"):
+            assert call(fn, state_out=st, **{o: st}) == W.WKV7_EINVAL, o
+            assert "overlaps" in message() and o in message(), o
+
+
 @pytest.mark.parametrize("fn", [f for f in CALLS if "workspace" in CALLS[f][1]])
 def test_workspace_sizes(fn):
     kind = CALLS[fn][0]
