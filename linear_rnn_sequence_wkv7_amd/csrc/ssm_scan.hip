@@ -122,8 +122,8 @@ __global__ __launch_bounds__(64 * WT) void ssm_scan_kernel(SsmParams g) {
         cp += ROUND * vrow;
         left -= ROUND;
     };
-    auto store_y = [&](int t0, const float* v) {
-        const rsrc_t r = buf_rsrc(yp + t0 * yrow, (t0 < 0 ? 0 : max(0, min(g.T - t0, ROUND)) * int(yrow)) & ykeep);
+    auto store_y = [&](int t0, int end, const float* v) {   // of the tokens before `end`
+        const rsrc_t r = buf_rsrc(yp + t0 * yrow, (t0 < 0 ? 0 : max(0, min(end - t0, ROUND)) * int(yrow)) & ykeep);
         if (g.y_bf16) buf_store<bf16_t, E, VEC>(r, eoff * 2, v, ne);
         else buf_store<float, E, true>(r, eoff * 4, v, ne);
     };
@@ -156,7 +156,7 @@ __global__ __launch_bounds__(64 * WT) void ssm_scan_kernel(SsmParams g) {
             const float z = z_p.get(i);
             out[i] = y * fmaf(z, sigmoidf_(z), no_z);
         }
-        store_y(t0, out);
+        store_y(t0, len, out);
     };
     load();
     int par = 0;
@@ -250,10 +250,11 @@ __global__ __launch_bounds__(64 * WT) void ssm_scan_kernel(SsmParams g) {
         }
     }
     if (WT == 1 && len > 0) output((len + ROUND - 1) / ROUND * ROUND - ROUND);
-    // Padding after the last round: y = 0, and the state as it is at the checkpoints there.
+    // Padding: y = 0, also where the state is no number, and after the last round the state as it is at the
+    // checkpoints there.
     const int done = (len + ROUND - 1) / ROUND * ROUND;
     const float zero[E] = {};
-    for (int t0 = done; t0 < g.T; t0 += ROUND) store_y(t0, zero);
+    for (int t0 = len; t0 < g.T; t0 += ROUND) store_y(t0, g.T, zero);
     if (w != 0) return;
     if (g.ck)
         for (int k = (done + SSM_CHECKPOINT_TOKENS - 1) / SSM_CHECKPOINT_TOKENS; k < g.nck; ++k)

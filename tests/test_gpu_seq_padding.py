@@ -1,0 +1,79 @@
+"""Padding behind a sequence's end, where what the sequence itself brings is not finite:
+its y and its gradients are 0 all the same."""
+import numpy as np
+import pytest
+
+from tests import seq_util as S
+from tests.gpu_util import announce, to_dev, to_host, torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _gpu_and_name(request):
+    if not torch().cuda.is_available():
+        pytest.skip("no GPU")
+    announce(request.node.nodeid)
+    yield
+
+
+def mods():
+    from linear_rnn_sequence_wkv7_amd import groupnorm, shortconv, ssm
+    return shortconv, ssm, groupnorm
+
+
+def lens(lengths):
+    return torch().tensor(lengths, dtype=torch().int32, device="cuda")
+
+
+def padding_is_zero(what, t, lengths):
+    got = to_host(t)
+    for b, n in enumerate(lengths):
+        assert np.all(got[b, n:] == 0), f"{what}: padding of sequence {b}"
+
+
+SCANS = [(16, 16, 1), (40, 16, 1), (40, 16, 200), (300, 16, 1), (40, 32, 1), (40, 64, 1), (90, 8, 300), (40, 15, 1)]   # T, N, copies
+
+
+def scan_case(T, N, copies, z, bad):
+    """Four sequences, `copies` times, two of them from states with one value that is not finite."""
+    C = 24
+    x = S.scan_inputs(T + N, 4, T, C, N, 1, "f32", z=z, state=True)
+    x["state"][0, 3, 1] = x["state"][1, 3, 0] = bad
+    rep = lambda v: None if v is None else to_dev(np.concatenate([v] * copies))
+    a = (rep(x["x"]), rep(x["dt"]), to_dev(x["A"]), rep(x["Bm"]), rep(x["Cm"]))
+    lengths = [T - 3, 5, 0, T - 9] * copies
+    return a, dict(D=to_dev(x["D"]), dt_bias=to_dev(x["dt_bias"]), z=rep(x["z"]), state=rep(x["state"]), lengths=lens(lengths)), lengths, rep, C
+
+
+@pytest.mark.parametrize("bad", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("z", [True, False])
+@pytest.mark.parametrize("T,N,copies", SCANS)
+def test_scan_forward(T, N, copies, z, bad):
+    """For each number of waves to a block of channels."""
+    a, kw, lengths, _, _ = scan_case(T, N, copies, z, bad)
+    y, s = mods()[1].ssm_forward(*a, **kw)
+    torch().cuda.synchronize()
+    padding_is_zero("y", y, lengths)
+    s = to_host(s)
+    assert not np.isfinite(s[0, 3, 1])
+    assert np.all(np.isfinite(s[2])) and np.all(np.isfinite(s[:, 4:]))   # an empty sequence, other channels
+
+
+@pytest.mark.parametrize("bad", [np.inf, np.nan])
+@pytest.mark.parametrize("T,C,G", [(1, 64, 2), (1, 30, 2), (9, 24, 3), (9, 22, 1), (3000, 96, 2), (1, 4096, 1)])
+def test_norm(T, C, G, bad):
+    _, _, gn = mods()
+    B = 3
+    rng = np.random.default_rng(C)
+    x, dy, gate = (rng.standard_normal((B, T, C)).astype(np.float32) for _ in range(3))
+    weight, bias = rng.standard_normal(C).astype(np.float32), rng.standard_normal(C).astype(np.float32)
+    weight[1], bias[C - 1] = bad, bad
+    lengths = [T // 2, 0, T]
+    kw = dict(weight=to_dev(weight), bias=to_dev(bias), gate=to_dev(gate), act="silu", lengths=lens(lengths))
+    y, mean, rstd = gn.groupnorm_forward(to_dev(x), G, **kw)
+    g = gn.groupnorm_backward(to_dev(x), G, to_dev(dy), mean, rstd, **kw)
+    torch().cuda.synchronize()
+    padding_is_zero("y", y, lengths)
+    padding_is_zero("dx", g["x"], lengths)
+    padding_is_zero("dgate", g["gate"], lengths)
