@@ -157,17 +157,17 @@ __global__ __launch_bounds__(64 * WS * WT, waves_of(WS, WT, VEC)) void ssm_backw
         const rsrc_t ck = buf_rsrc(ws.ck + ((b * g.nck + t0 / SSM_CHECKPOINT_TOKENS) * g.C + c0) * g.N, int64_t(nc) * g.N * 4);
         nx.h.load(ck, n0 < g.N ? uint32_t(ch * g.N + n0) * 4 : kNowhere, g.N - n0);
     };
-    auto store = [&](void* p, int t0, const float* v, uint32_t eoff, int ne) {
-        const int n = min(g.T - t0, ROUND);
+    auto store = [&](void* p, int t0, int end, const float* v, uint32_t eoff, int ne) {   // of the tokens before `end`
+        const int n = min(end - t0, ROUND);
         buf_store<Tin, E, VEC>(buf_rsrc(static_cast<char*>(p) + (b * g.T + t0) * erow, n * erow), eoff * ES, v, ne);
     };
 
     const int rounds = (len + ROUND - 1) / ROUND;
-    for (int t0 = rounds * ROUND; t0 < g.T; t0 += ROUND) {   // padding after the last round
+    for (int t0 = len; t0 < g.T; t0 += ROUND) {   // padding: 0, also where a state or its gradient is no number
         const float zero[E] = {};
-        store(g.dx, t0, zero, eoff, ne);
-        store(g.ddt, t0, zero, eoff, ne);
-        if (g.z) store(g.dz, t0, zero, eoff, ne);
+        store(g.dx, t0, g.T, zero, eoff, ne);
+        store(g.ddt, t0, g.T, zero, eoff, ne);
+        if (g.z) store(g.dz, t0, g.T, zero, eoff, ne);
     }
     if (rounds > 0) load((rounds - 1) * ROUND);
     for (int rd = rounds - 1; rd >= 0; --rd) {
@@ -355,9 +355,9 @@ __global__ __launch_bounds__(64 * WS * WT, waves_of(WS, WT, VEC)) void ssm_backw
                 dD[i] = fmaf(o, x, dD[i]);
                 dbias[i] += ddt[i];
             }
-            store(g.dx, t0, dx, eoff, ne);
-            store(g.ddt, t0, ddt, eoff, ne);
-            if (g.z) store(g.dz, t0, dz, eoff, ne);
+            store(g.dx, t0, len, dx, eoff, ne);
+            store(g.ddt, t0, len, ddt, eoff, ne);
+            if (g.z) store(g.dz, t0, len, dz, eoff, ne);
         }
         // dB and dC of the run, 4 tokens at once.
         {

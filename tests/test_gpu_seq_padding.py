@@ -60,6 +60,23 @@ def test_scan_forward(T, N, copies, z, bad):
     assert np.all(np.isfinite(s[2])) and np.all(np.isfinite(s[:, 4:]))   # an empty sequence, other channels
 
 
+@pytest.mark.parametrize("bad", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("z", [True, False])
+@pytest.mark.parametrize("T,N,copies", SCANS)
+def test_scan_backward(T, N, copies, z, bad):
+    """For each number of runs; gradients of the state that are not finite too."""
+    a, kw, lengths, rep, C = scan_case(T, N, copies, z, bad)
+    rng = np.random.default_rng(T)
+    dy, ds = rng.standard_normal((4, T, C)).astype(np.float32), rng.standard_normal((4, C, N)).astype(np.float32)
+    ds[0, 5, 0] = ds[3, 5, 1] = bad
+    g = mods()[1].ssm_backward(*a, rep(dy), dstate=rep(ds), **kw)
+    torch().cuda.synchronize()
+    for k in ("x", "dt", "z", "B", "C"):
+        if g[k] is not None:
+            padding_is_zero("d" + k, g[k], lengths)
+    assert np.all(np.isfinite(to_host(g["state"])[:, 0])) and np.all(np.isfinite(to_host(g["dt_bias"])[[0, 1, 2, 4]]))
+
+
 @pytest.mark.parametrize("bad", [np.inf, np.nan])
 @pytest.mark.parametrize("T,C,G", [(1, 64, 2), (1, 30, 2), (9, 24, 3), (9, 22, 1), (3000, 96, 2), (1, 4096, 1)])
 def test_norm(T, C, G, bad):
