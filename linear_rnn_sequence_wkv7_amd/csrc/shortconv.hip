@@ -246,6 +246,7 @@ __global__ __launch_bounds__(NTC) void conv_backward_kernel(ConvParams g, Runs r
                     dx[j] = 0.f;
                     #pragma unroll
                     for (int k = 0; k < K; ++k) dx[j] = fmaf(w[K - 1 - k][j], dp[k][j], dx[j]);
+                    if (ti >= len) dx[j] = 0.f;   // padding: also where a tap is no number
                 }
                 const int k1 = ti - (len - (K - 1));   // its place in state_out
                 if (g.ds1 && k1 >= 0 && k1 < K - 1) {

@@ -78,6 +78,24 @@ def test_scan_backward(T, N, copies, z, bad):
 
 
 @pytest.mark.parametrize("bad", [np.inf, np.nan])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_convolution(dtype, bad):
+    cv, _, _ = mods()
+    B, T, C, K = 3, 37, 24, 4
+    rng = np.random.default_rng(1)
+    x, dy = (S.as_dtype(rng.standard_normal((B, T, C)), dtype) for _ in range(2))
+    w, bias = rng.standard_normal((C, K)).astype(np.float32), rng.standard_normal(C).astype(np.float32)
+    w[2, 1] = w[5, 3] = bias[7] = bad
+    lengths = [20, 0, 36]
+    kw = dict(bias=to_dev(bias), lengths=lens(lengths))
+    y, _ = cv.shortconv_forward(to_dev(x), to_dev(w), **kw)
+    g = cv.shortconv_backward(to_dev(x), to_dev(w), to_dev(dy), **kw)
+    torch().cuda.synchronize()
+    padding_is_zero("y", y, lengths)
+    padding_is_zero("dx", g["x"], lengths)
+
+
+@pytest.mark.parametrize("bad", [np.inf, np.nan])
 @pytest.mark.parametrize("T,C,G", [(1, 64, 2), (1, 30, 2), (9, 24, 3), (9, 22, 1), (3000, 96, 2), (1, 4096, 1)])
 def test_norm(T, C, G, bad):
     _, _, gn = mods()
