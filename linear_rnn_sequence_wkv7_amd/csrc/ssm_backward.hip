@@ -461,6 +461,11 @@ __global__ __launch_bounds__(256) void ssm_sum_batch_kernel(SsmParams g, const f
     } else if (g.dbias) g.dbias[m - CN - g.C] = s;
 }
 
+// Without tokens: the state's gradient goes back as it came (or 0).
+__global__ __launch_bounds__(256) void ssm_no_tokens_kernel(const float* from, float* to, int64_t n) {
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) to[i] = from ? from[i] : 0.f;
+}
+
 int blocks_of(const SsmParams& p) { return (p.C / p.G + CH - 1) / CH; }
 int64_t up(int64_t x) { return (x + 255) & ~int64_t(255); }
 int64_t bc_bytes(const SsmParams& p) { return up(int64_t(blocks_of(p)) * p.B * p.T * p.G * 2 * p.N * 4); }
@@ -514,7 +519,7 @@ hipError_t launch_types(const SsmParams& p, const BwdWs& ws, hipStream_t stream)
 }  // namespace
 
 int64_t ssm_backward_workspace(const SsmParams& p, bool own_checkpoints) {
-    if (int64_t(p.B) * p.C == 0) return 0;
+    if (int64_t(p.B) * p.T * p.C == 0) return 0;
     return bc_bytes(p) + par_bytes(p) + (own_checkpoints ? up(int64_t(p.B) * p.nck * p.C * p.N * 4) : 0);
 }
 
@@ -526,6 +531,16 @@ int64_t ssm_backward_threads(const SsmParams& p) {
 }
 
 hipError_t launch_ssm_backward(const SsmParams& p, hipStream_t stream) {
+    const int64_t Mp = int64_t(p.C) * p.N + 2 * p.C;
+    const dim3 batch{unsigned((Mp + 255) / 256)};
+    if (p.T == 0) {   // nothing to add up, and no workspace
+        const int64_t n = p.ds0 ? int64_t(p.B) * p.C * p.N : 0, nb = (n + 255) / 256;
+        if (n > 0) hipLaunchKernelGGL(ssm_no_tokens_kernel, dim3(unsigned(nb < 4096 ? nb : 4096)), dim3(256), 0, stream, p.ds1, p.ds0, n);
+        SsmParams none = p;
+        none.B = 0;
+        if (Mp > 0) hipLaunchKernelGGL(ssm_sum_batch_kernel, batch, dim3(256), 0, stream, none, static_cast<const float*>(nullptr));
+        return hipGetLastError();
+    }
     char* at = static_cast<char*>(p.ws);
     BwdWs ws{reinterpret_cast<float*>(at), reinterpret_cast<float*>(at + bc_bytes(p)), p.ck};
     if (!p.ck && int64_t(p.B) * p.T * p.C > 0) {   // the states first
@@ -544,12 +559,12 @@ hipError_t launch_ssm_backward(const SsmParams& p, hipStream_t stream) {
     }
     // The sums; without channels or sequences, the zeros.
     const int ncb = blocks_of(p);
-    const int64_t M = int64_t(p.B) * p.T * p.G * 2 * p.N, Mp = int64_t(p.C) * p.N + 2 * p.C;
+    const int64_t M = int64_t(p.B) * p.T * p.G * 2 * p.N;
     if (M > 0) {
         if (p.N % 4 == 0) hipLaunchKernelGGL((ssm_sum_bc_kernel<4>), dim3(unsigned((M / 4 + 63) / 64)), dim3(256), 0, stream, p, ws.bc, ncb);
         else hipLaunchKernelGGL((ssm_sum_bc_kernel<1>), dim3(unsigned((M + 63) / 64)), dim3(256), 0, stream, p, ws.bc, ncb);
     }
-    if (Mp > 0) hipLaunchKernelGGL(ssm_sum_batch_kernel, dim3(unsigned((Mp + 255) / 256)), dim3(256), 0, stream, p, ws.par);
+    if (Mp > 0) hipLaunchKernelGGL(ssm_sum_batch_kernel, batch, dim3(256), 0, stream, p, ws.par);
     return hipGetLastError();
 }
 

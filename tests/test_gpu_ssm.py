@@ -199,6 +199,23 @@ def test_no_tokens():
     assert all(bool((g[k] == 0).all()) for k in ("A", "D", "dt_bias"))
 
 
+@pytest.mark.parametrize("B,C,N,dtype", [(2, 20, 16, "bf16"), (3, 7, 5, "f32"), (700, 600, 16, "f32")])
+def test_gradients_without_tokens_need_no_workspace(B, C, N, dtype):
+    """T = 0, with and without a gradient of the state, into outputs that held something."""
+    t = torch()
+    x = S.scan_inputs(2, B, 0, C, N, dtype=dtype)
+    a, kw = dev_args(x)
+    ds = t.randn(B, C, N, device="cuda")
+    full = lambda *s: t.full(s, 7.0, device="cuda")
+    assert M().ssm_backward_workspace_bytes(B, 0, C, N) == M().ssm_backward_workspace_bytes(B, 0, C, N, checkpoints=False) == 0
+    for given in (ds, None):
+        grads = {"A": full(C, N), "D": full(C), "dt_bias": full(C), "state": full(B, C, N)}
+        g = M().ssm_backward(*a, a[0], dstate=given, grads=grads, **kw)
+        assert all(g[k] is grads[k] for k in grads)
+        assert t.equal(g["state"], ds if given is not None else t.zeros_like(ds))
+        assert all(bool((g[k] == 0).all()) for k in ("A", "D", "dt_bias"))
+
+
 def test_lengths_from_the_middle_of_a_tensor():
     t = torch()
     x = S.scan_inputs(3, 2, 20, 8, 16, dtype="f32")

@@ -265,6 +265,16 @@ def test_size_queries():
             q()
 
 
+def test_no_tokens_need_no_workspace():
+    """The sizes that the headers give as 0 when B T C == 0."""
+    for B, T, C in ((2, 0, 64), (0, 70, 64), (2, 70, 0)):
+        for own in (True, False):
+            assert S.ssm_backward_workspace_bytes(B, T, C, 16, checkpoints=own) == 0
+        assert K.shortconv_backward_workspace_bytes(B, T, C, 4) == 0
+        assert N.groupnorm_workspace_bytes(B, T, C, 4) == 0
+        assert N.groupnorm_backward_workspace_bytes(B, T, C, 4) == 0
+
+
 def test_nothing_to_do_needs_no_device():
     assert call("ssm_forward", desc("ssm", B=0)) == W.WKV7_OK
     assert call("ssm_forward", desc("ssm", T=0), state_out=None) == W.WKV7_OK
