@@ -43,8 +43,9 @@ typedef struct groupnorm_desc {
     const int32_t* lengths; /* [B] device int32, 4-byte aligned, or NULL */
 } groupnorm_desc;
 
-/* Workspace bytes of groupnorm_forward (partial statistics; 0 where rows are normalised by themselves and when there is
- * nothing to compute).  Host only. */
+/* Workspace bytes of groupnorm_forward: partial statistics of groups that are too large for the registers of
+ * one wave (T = 1) or one workgroup (T > 1).  0 when there is nothing to compute, and at T = 1 for groups of up
+ * to 1024 channels, of up to 2048 where their number is even.  Host only. */
 int64_t groupnorm_workspace_bytes(const groupnorm_desc* desc);
 
 /* y, and mean and rstd where they are not NULL (both or neither). */
@@ -52,7 +53,7 @@ int groupnorm_forward(const groupnorm_desc* desc, const void* x, const float* we
                       const void* gate, void* y, float* mean, float* rstd,
                       void* workspace, int64_t workspace_bytes, void* stream);
 
-/* Workspace bytes of groupnorm_backward.  Host only. */
+/* Workspace bytes of groupnorm_backward; 0 when B T C == 0.  Host only. */
 int64_t groupnorm_backward_workspace_bytes(const groupnorm_desc* desc);
 
 /* The gradients of <dy, y>, with mean and rstd as the forward wrote them: dx [B, T, C] of

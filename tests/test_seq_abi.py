@@ -265,6 +265,15 @@ def test_size_queries():
             q()
 
 
+def test_norm_workspace_of_single_rows():
+    """At T = 1 the forward needs none for the groups that the header names, and some past them."""
+    for Cg in (1, 8, 63, 96, 512, 1000, 1023, 1024, 1026, 2046, 2048):
+        for G in (1, 3):
+            assert N.groupnorm_workspace_bytes(8, 1, G * Cg, G) == 0, Cg
+    for Cg in (1025, 2047, 2049, 2050, 4096):
+        assert N.groupnorm_workspace_bytes(8, 1, Cg, 1) > 0, Cg
+
+
 def test_no_tokens_need_no_workspace():
     """The sizes that the headers give as 0 when B T C == 0."""
     for B, T, C in ((2, 0, 64), (0, 70, 64), (2, 70, 0)):
