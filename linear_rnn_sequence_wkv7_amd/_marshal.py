@@ -108,9 +108,15 @@ def scratch(workspace, need, dev):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
+def _public_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
 # The current stream's handle and the current device's index, without the wrapper objects
-# that torch.cuda's own functions make (2 of the 13 microseconds of a small call).
-_raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+# that torch.cuda's own functions make (2 of the 13 microseconds of a small call), where this
+# torch has the names that those functions call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_stream)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def call(fn, dev, *args):

@@ -209,6 +209,25 @@ def test_two_streams_at_once():
                 assert t.equal(g[k], alone[i][1][k]), k
 
 
+def test_bindings_by_torchs_public_names(monkeypatch):
+    """The public names of the current stream and device give what the short ways give, on a side stream too."""
+    t = torch()
+    from linear_rnn_sequence_wkv7_amd import _marshal
+    cv, _, _ = mods()
+    d = {k: to_dev(v) for k, v in block_inputs(1, 2, 40, 64, 16, 4, "bf16").items()}
+    want, _ = cv.shortconv_forward(d["x"], d["w"], bias=d["cb"])
+    side = t.cuda.Stream()
+    t.cuda.synchronize()
+    with t.cuda.stream(side):
+        assert _marshal._public_stream(side.device_index) == side.cuda_stream == _marshal._raw_stream(side.device_index)
+    monkeypatch.setattr(_marshal, "_raw_stream", _marshal._public_stream)
+    monkeypatch.setattr(_marshal, "_device", t.cuda.current_device)
+    with t.cuda.stream(side):
+        got, _ = cv.shortconv_forward(d["x"], d["w"], bias=d["cb"])
+    t.cuda.synchronize()
+    assert t.equal(got, want)
+
+
 def test_bindings_refuse():
     t = torch()
     cv, sm, gn = mods()

@@ -5,6 +5,7 @@ import ctypes
 import os
 import re
 import subprocess
+import sys
 
 import pytest
 
@@ -293,6 +294,26 @@ def test_nothing_to_do_needs_no_device():
     assert call("groupnorm_forward", desc("norm", B=0)) == W.WKV7_OK
     assert call("shortconv_backward", desc("conv", C=0)) == W.WKV7_OK
     assert call("groupnorm_backward", desc("norm", C=0, G=1)) == W.WKV7_OK
+
+
+def test_bindings_import_without_torchs_private_names():
+    """A torch without the short ways to the current stream and device: the modules are there and refuse as ever."""
+    code = """
+import torch
+for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+    if hasattr(torch._C, n):
+        delattr(torch._C, n)
+from linear_rnn_sequence_wkv7_amd import _marshal, groupnorm, shortconv, ssm
+assert _marshal._raw_stream is _marshal._public_stream and _marshal._device is torch.cuda.current_device
+x = torch.zeros(2, 3, 8)
+try:
+    groupnorm.groupnorm_forward(x, 2)
+except ValueError as e:
+    assert "GPU" in str(e)
+    print("refused")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "refused", r.stderr
 
 
 def test_python_bindings_refuse_wrong_tensors():
