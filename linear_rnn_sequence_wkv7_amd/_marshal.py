@@ -74,6 +74,9 @@ def output(name, t, like, y_dtype, dev):
 def gradients(grads, wanted, dev):
     """The output tensors of a backward: for each (key, like, shape, dtype) None where like is, else the
     caller's, checked, or a new one (of like itself where shape is None)."""
+    others = set(grads) - {w[0] for w in wanted} if grads else None
+    if others:   # a tensor under a name of another's would be left as it was
+        raise ValueError(f"grads has no {', '.join(sorted(map(str, others)))}; its keys are {', '.join(w[0] for w in wanted)}")
     out = {}
     for key, like, shape, dtype in wanted:
         given = grads.get(key) if grads else None

@@ -104,7 +104,7 @@ def groupnorm_backward(x, G: int, dy, mean, rstd, *, weight=None, bias=None, gat
                        workspace=None, grads=None) -> dict:
     """Gradients of <dy, y> for groupnorm_forward with the same arguments, mean and rstd as it
     returned them.  Returns a dict: x and gate of x's dtype, weight and bias [C] float32 (None
-    where they are not inputs).  `grads` may supply output tensors under these keys."""
+    where they are not inputs).  `grads` may supply output tensors under these keys (others: ValueError)."""
     dev, B, T, C = _inputs(x, G, weight, bias, gate, lengths)
     f32 = torch.float32
     M.check("dy", dy, x.shape, dy.dtype, dev)

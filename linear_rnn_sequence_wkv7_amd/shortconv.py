@@ -106,7 +106,7 @@ def shortconv_backward(x, w, dy, *, bias=None, state=None, dstate=None, lengths=
     """Gradients of <dy, y> + <dstate, state_out> for shortconv_forward with the same
     arguments.  dy of the y dtype, dstate [B, K - 1, C] float32 or None.  Returns a dict: x of
     x's dtype, w [C, K], bias [C] (None without bias), state [B, K - 1, C] float32 (None when
-    return_dstate is False).  `grads` may supply output tensors under these keys."""
+    return_dstate is False).  `grads` may supply output tensors under these keys (others: ValueError)."""
     dev, B, T, C, K = _inputs(x, w, bias, lengths, False)
     f32 = torch.float32
     M.check_if("state", state, (B, K - 1, C), x.dtype, dev)

@@ -155,7 +155,7 @@ def ssm_backward(x, dt, A, Bm, Cm, dy, *, D=None, dt_bias=None, z=None, state=No
     filled them (None: the states are computed again, into the workspace).  Returns a dict:
     x, dt, z, B, C of the input dtype, A [C, N], D, dt_bias [C], state [B, C, N] float32 (z, D
     and dt_bias None where they are not inputs, state None when return_dstate is False).
-    `grads` may supply output tensors under these keys."""
+    `grads` may supply output tensors under these keys (others: ValueError)."""
     dev, B, T, C, N, G = _inputs(x, dt, A, Bm, Cm, D, dt_bias, z, lengths, False)
     f32 = torch.float32
     M.check_if("state", state, (B, C, N), f32, dev)

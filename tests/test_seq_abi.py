@@ -316,6 +316,19 @@ except ValueError as e:
     assert r.returncode == 0 and r.stdout.strip() == "refused", r.stderr
 
 
+def test_gradients_under_other_names_are_refused():
+    """A caller's output tensor under a name that is no gradient's would stay as it was."""
+    import torch
+    from linear_rnn_sequence_wkv7_amd import _marshal
+    x, w = torch.zeros(2, 3, 8), torch.zeros(8, 4)
+    wanted = (("x", x, None, None), ("w", w, None, None), ("bias", None, None, None))
+    out = _marshal.gradients({"x": x.clone(), "w": None, "bias": None}, wanted, x.device)
+    assert out["w"] is not None and out["bias"] is None
+    for name in ("X", "dw", "dx"):
+        with pytest.raises(ValueError, match=f"no {name}; its keys are x, w, bias"):
+            _marshal.gradients({name: x}, wanted, x.device)
+
+
 def test_python_bindings_refuse_wrong_tensors():
     """Shapes, types and devices are checked before the library is called."""
     import torch
