@@ -3,6 +3,7 @@ other type than x: fp32 inputs with bf16 y and dy, bf16 inputs with fp32 y and d
 import numpy as np
 import pytest
 
+from oracle import seq_oracle as O
 from tests import seq_util as S
 from tests.gpu_util import announce, to_dev, to_host, torch
 
@@ -79,3 +80,117 @@ def test_scan_step(C, N, G, dtype):
     (y_ref, s_ref), (y_tol, s_tol) = S.scan_bounds(one, 1, None, True)
     S.check("y", to_host(y), y_ref[:, 0], y_tol[:, 0], bf16=dtype == "f32")
     S.check("state", to_host(st), s_ref, s_tol)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kept", [True, False])
+@pytest.mark.parametrize("case", SCANS + [(1, 300, 33, 16, 1, None), (130, 40, 34, 16, 1, None), (600, 20, 30, 15, 2, None)],
+                         ids=SCAN_IDS + ["eight_runs_odd", "four_runs", "two_runs"])
+def test_scan_backward(case, kept, dtype):
+    """dy of the other type, with checkpoints from a forward that wrote y in it, for each number of runs."""
+    B, T, C, N, G, lengths = case
+    copies, B = (B // 2, 2) if B > 100 else (1, B)
+    x = S.scan_inputs(T * 3 + C, B, T, C, N, G, dtype, state=True)
+    rng = np.random.default_rng(C)
+    dy, ds = S.as_dtype(rng.standard_normal((B, T, C)), OTHER[dtype]), rng.standard_normal((B, C, N)).astype(np.float32)
+    ref, tol = S.scan_bounds(x, T, lengths, True, dy=dy, dstate=ds, B=B * copies, Cg=C // G)
+    if copies > 1:
+        rep = lambda v: np.concatenate([v] * copies)
+        x = {k: rep(v) if k in ("x", "dt", "Bm", "Cm", "z", "state") else v for k, v in x.items()}
+        dy, ds = rep(dy), rep(ds)
+    a, kw = dev_args(x)
+    kw["lengths"] = lens(lengths)
+    saved = None
+    if kept:
+        saved = torch().empty(M().ssm_checkpoint_bytes(B * copies, T, C, N), dtype=torch().uint8, device="cuda")
+        M().ssm_forward(*a, **kw, checkpoints=saved, y_dtype=OTHER[dtype])
+    g = M().ssm_backward(*a, to_dev(dy), dstate=to_dev(ds), checkpoints=saved, **kw)
+    torch().cuda.synchronize()
+    for k in ref:
+        if k in ("A", "D", "dt_bias"):
+            S.check("d" + k, to_host(g[k]), copies * ref[k], copies * tol[k])
+        else:
+            S.check("d" + k, to_host(g[k])[-B:], ref[k], tol[k], bf16=dtype == "bf16" and k != "state")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,N", [(40, 16), (200, 8)])
+def test_scan_backward_of_given_steps(T, N, dtype):
+    """The steps themselves as inputs (no softplus), some of them 0."""
+    B, C = 2, 20
+    x = S.scan_inputs(T, B, T, C, N, 1, dtype, state=True, bias=False)
+    d = np.abs(O.as_f64(x["dt"])) * 0.3
+    d[:, ::5] = 0
+    x["dt"] = S.as_dtype(d, dtype)
+    dy = S.as_dtype(np.random.default_rng(N).standard_normal((B, T, C)), OTHER[dtype])
+    ref, tol = S.scan_bounds(x, T, None, False, dy=dy, B=B, Cg=C)
+    a, kw = dev_args(x)
+    g = M().ssm_backward(*a, to_dev(dy), softplus=False, **kw)
+    torch().cuda.synchronize()
+    for k in ref:
+        if k != "dt_bias":
+            S.check("d" + k, to_host(g[k]), ref[k], tol[k], bf16=g[k].dtype == torch().bfloat16)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,T,C,K,lengths", [(2, 33, 7, 4, [33, 9]), (3, 40, 10, 3, None), (2, 65, 24, 2, [1, 65]), (2, 300, 72, 4, None)])
+def test_convolution(B, T, C, K, lengths, dtype):
+    from linear_rnn_sequence_wkv7_amd import shortconv
+    rng = np.random.default_rng(T)
+    r = lambda *s: rng.standard_normal(s)
+    x, state, dy = S.as_dtype(r(B, T, C), dtype), S.as_dtype(r(B, K - 1, C), dtype), S.as_dtype(r(B, T, C), OTHER[dtype])
+    w, bias, ds = r(C, K).astype(np.float32), r(C).astype(np.float32), r(B, K - 1, C).astype(np.float32)
+    (y_ref, s_ref), (y_tol, _) = S.conv_bounds(x, w, bias, state, lengths, True)
+    kw = dict(bias=to_dev(bias), state=to_dev(state), lengths=lens(lengths))
+    y, s = shortconv.shortconv_forward(to_dev(x), to_dev(w), y_dtype=OTHER[dtype], **kw)
+    S.check("y", to_host(y), y_ref, y_tol, bf16=dtype == "f32")
+    np.testing.assert_array_equal(to_host(s), s_ref)
+    ref, tol = S.conv_bounds(x, w, bias, state, lengths, True, dy, ds)
+    g = shortconv.shortconv_backward(to_dev(x), to_dev(w), to_dev(dy), dstate=to_dev(ds), **kw)
+    torch().cuda.synchronize()
+    for k in ref:
+        S.check("d" + k, to_host(g[k]), ref[k], tol[k], bf16=dtype == "bf16" and k == "x")
+    st = to_dev(state)
+    y1 = shortconv.shortconv_step(to_dev(x[:, 0]), to_dev(w), st, bias=to_dev(bias), y_dtype=OTHER[dtype])
+    (y_ref, s_ref), (y_tol, _) = S.conv_bounds(x[:, :1], w, bias, state, None, True)
+    S.check("step y", to_host(y1), y_ref[:, 0], y_tol[:, 0], bf16=dtype == "f32")
+    np.testing.assert_array_equal(to_host(st), s_ref)
+
+
+NORMS = [
+    # B, T, C, G, lengths: rows, waves, a workgroup's registers, partial sums
+    (5, 1, 128, 4, None),
+    (3, 1, 1024, 2, [1, 0, 1]),
+    (5, 1, 96, 1, None),
+    (4, 1, 1599, 1, None),
+    (3, 1, 21, 3, [1, 1, 0]),
+    (3, 40, 48, 2, [40, 7, 0]),
+    (2, 130, 60, 4, None),
+    (2, 33, 15, 5, None),
+    (2, 1100, 32, 2, [1100, 600]),
+    (2, 3000, 96, 2, [2999, 3000]),
+    (1, 1000, 514, 1, None),
+    (2, 1, 9000, 2, None),
+    (1, 130, 1999, 1, [77]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,T,C,G,lengths", NORMS, ids=["B{}_T{}_C{}_G{}".format(*c[:4]) for c in NORMS])
+def test_norm(B, T, C, G, lengths, dtype):
+    from linear_rnn_sequence_wkv7_amd import groupnorm
+    rng = np.random.default_rng(C)
+    r = lambda *s: rng.standard_normal(s)
+    x, gate, dy = S.as_dtype(r(B, T, C) * 0.8 + 0.3, dtype), S.as_dtype(r(B, T, C), dtype), S.as_dtype(r(B, T, C), OTHER[dtype])
+    weight, bias = (1 + 0.3 * r(C)).astype(np.float32), (0.3 * r(C)).astype(np.float32)
+    (y_ref, m_ref, r_ref), (y_tol, m_tol, r_tol) = S.norm_bounds(x, G, weight, bias, gate, True, 1e-5, lengths)
+    kw = dict(weight=to_dev(weight), bias=to_dev(bias), gate=to_dev(gate), act="silu", lengths=lens(lengths))
+    y, mean, rstd = groupnorm.groupnorm_forward(to_dev(x), G, y_dtype=OTHER[dtype], **kw)
+    S.check("y", to_host(y), y_ref, y_tol, bf16=dtype == "f32")
+    S.check("mean", to_host(mean), m_ref, m_tol)
+    S.check("rstd", to_host(rstd), r_ref, r_tol)
+    ref, tol = S.norm_bounds(x, G, weight, bias, gate, True, 1e-5, lengths, dy=dy)
+    g = groupnorm.groupnorm_backward(to_dev(x), G, to_dev(dy), mean, rstd, **kw)
+    torch().cuda.synchronize()
+    for k in ref:
+        S.check("d" + k, to_host(g[k]), ref[k], tol[k], bf16=dtype == "bf16" and k in ("x", "gate"))
