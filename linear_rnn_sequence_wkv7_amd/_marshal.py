@@ -52,6 +52,13 @@ def gpu(name, t, dims):
     return t.device
 
 
+def sizes(*n):
+    """The sizes of a descriptor, whose fields are int32 (ctypes would keep the low 32 bits of larger ones)."""
+    if max(n) > 0x7FFFFFFF or min(n) < -0x80000000:
+        raise ValueError(f"sizes of 2^31 and more are not supported (got {max(n, key=abs)})")
+    return n
+
+
 def ptr(t):
     return None if t is None else t.data_ptr()
 

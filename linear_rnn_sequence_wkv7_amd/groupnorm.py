@@ -55,12 +55,12 @@ def _lib():
 
 def groupnorm_workspace_bytes(B: int, T: int, C: int, G: int) -> int:
     """Workspace bytes of groupnorm_forward for these sizes, of either dtype."""
-    return max(M.size(_lib().groupnorm_workspace_bytes, ctypes.byref(GroupnormDesc(B, T, C, G, d, d, eps=1.0))) for d in (0, 1))
+    return max(M.size(_lib().groupnorm_workspace_bytes, ctypes.byref(GroupnormDesc(*M.sizes(B, T, C, G), d, d, eps=1.0))) for d in (0, 1))
 
 
 def groupnorm_backward_workspace_bytes(B: int, T: int, C: int, G: int) -> int:
     """Workspace bytes of groupnorm_backward for these sizes, of either dtype."""
-    return max(M.size(_lib().groupnorm_backward_workspace_bytes, ctypes.byref(GroupnormDesc(B, T, C, G, d, d, eps=1.0))) for d in (0, 1))
+    return max(M.size(_lib().groupnorm_backward_workspace_bytes, ctypes.byref(GroupnormDesc(*M.sizes(B, T, C, G), d, d, eps=1.0))) for d in (0, 1))
 
 
 def _inputs(x, G, weight, bias, gate, lengths):
@@ -81,6 +81,11 @@ def _act(act) -> int:
     return ACTS[act]
 
 
+def _desc(x, y, B, T, C, G, act, eps, lengths):
+    M.sizes(B, T, C, G)
+    return GroupnormDesc(B, T, C, G, M.dtype_code(x), M.dtype_code(y), _act(act), eps, M.ptr(lengths))
+
+
 def groupnorm_forward(x, G: int, *, weight=None, bias=None, gate=None, act: str = "none", eps: float = 1e-5, lengths=None,
                       y_dtype: Optional[str] = None, y=None, mean=None, rstd=None, return_stats: bool = True,
                       workspace=None) -> Tuple[torch.Tensor, Optional[torch.Tensor], Optional[torch.Tensor]]:
@@ -93,7 +98,7 @@ def groupnorm_forward(x, G: int, *, weight=None, bias=None, gate=None, act: str 
         rstd = torch.empty((B, G), dtype=torch.float32, device=dev) if rstd is None else rstd
     M.check_if("mean", mean, (B, G), torch.float32, dev)
     M.check_if("rstd", rstd, (B, G), torch.float32, dev)
-    desc = GroupnormDesc(B, T, C, G, M.dtype_code(x), M.dtype_code(y), _act(act), eps, M.ptr(lengths))
+    desc = _desc(x, y, B, T, C, G, act, eps, lengths)
     lib = _lib()
     ws, ws_bytes, keep = M.scratch(workspace, M.size(lib.groupnorm_workspace_bytes, ctypes.byref(desc)), dev)
     M.call(lib.groupnorm_forward, dev, ctypes.byref(desc), *M.ptrs(x, weight, bias, gate, y, mean, rstd), ws, ws_bytes)
@@ -112,7 +117,7 @@ def groupnorm_backward(x, G: int, dy, mean, rstd, *, weight=None, bias=None, gat
     M.check("rstd", rstd, (B, G), f32, dev)
     out = M.gradients(grads, (("x", x, None, None), ("weight", weight, None, None), ("bias", bias, None, None),
                               ("gate", gate, None, None)), dev)
-    desc = GroupnormDesc(B, T, C, G, M.dtype_code(x), M.dtype_code(dy), _act(act), 1.0, M.ptr(lengths))
+    desc = _desc(x, dy, B, T, C, G, act, 1.0, lengths)
     lib = _lib()
     ws, ws_bytes, keep = M.scratch(workspace, M.size(lib.groupnorm_backward_workspace_bytes, ctypes.byref(desc)), dev)
     M.call(lib.groupnorm_backward, dev, ctypes.byref(desc),

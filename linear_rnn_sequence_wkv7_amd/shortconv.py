@@ -51,13 +51,18 @@ def _lib():
 
 def shortconv_backward_workspace_bytes(B: int, T: int, C: int, K: int) -> int:
     """Workspace bytes of shortconv_backward for these sizes."""
-    return M.size(_lib().shortconv_backward_workspace_bytes, ctypes.byref(ShortconvDesc(B, T, C, K)))
+    return M.size(_lib().shortconv_backward_workspace_bytes, ctypes.byref(ShortconvDesc(*M.sizes(B, T, C, K))))
 
 
 def _act(act) -> int:
     if act not in ACTS:
         raise ValueError(f"act must be one of {sorted(ACTS)}")
     return ACTS[act]
+
+
+def _desc(x, y, B, T, C, K, act, S=0, lengths=None):
+    M.sizes(B, T, C, K, S)
+    return ShortconvDesc(B, T, C, K, M.dtype_code(x), M.dtype_code(y), _act(act), S, M.ptr(lengths))
 
 
 def _inputs(x, w, bias, lengths, step):
@@ -82,7 +87,7 @@ def shortconv_forward(x, w, *, bias=None, state=None, lengths=None, act: str = "
         M.check("state_out", state_out, (B, K - 1, C), x.dtype, dev)
     elif return_state:
         state_out = torch.empty((B, max(K - 1, 0), C), dtype=x.dtype, device=dev)
-    desc = ShortconvDesc(B, T, C, K, M.dtype_code(x), M.dtype_code(y), _act(act), 0, M.ptr(lengths))
+    desc = _desc(x, y, B, T, C, K, act, 0, lengths)
     M.call(_lib().shortconv_forward, dev, ctypes.byref(desc), *M.ptrs(x, w, bias, state, y, state_out))
     return y, state_out
 
@@ -96,7 +101,7 @@ def shortconv_step(x, w, state, *, bias=None, state_index=None, act: str = "silu
     M.check("state", state, (S, K - 1, C), x.dtype, dev)
     M.check_if("state_index", state_index, (B,), torch.int32, dev)
     y = M.output("y", y, x, y_dtype, dev)
-    desc = ShortconvDesc(B, 1, C, K, M.dtype_code(x), M.dtype_code(y), _act(act), S, None)
+    desc = _desc(x, y, B, 1, C, K, act, S)
     M.call(_lib().shortconv_step, dev, ctypes.byref(desc), *M.ptrs(x, w, bias, state, state_index, y))
     return y
 
@@ -114,7 +119,7 @@ def shortconv_backward(x, w, dy, *, bias=None, state=None, dstate=None, lengths=
     M.check_if("dstate", dstate, (B, K - 1, C), f32, dev)
     out = M.gradients(grads, (("x", x, None, None), ("w", w, None, None), ("bias", bias, None, None),
                               ("state", x if return_dstate else None, (B, max(K - 1, 0), C), f32)), dev)
-    desc = ShortconvDesc(B, T, C, K, M.dtype_code(x), M.dtype_code(dy), _act(act), 0, M.ptr(lengths))
+    desc = _desc(x, dy, B, T, C, K, act, 0, lengths)
     lib = _lib()
     need = M.size(lib.shortconv_backward_workspace_bytes, ctypes.byref(desc))
     ws, ws_bytes, keep = M.scratch(workspace, need, dev)

@@ -55,7 +55,7 @@ def _lib():
 
 
 def _sizes(B, T, C, N, G=1, dtype=0):
-    return SsmDesc(B=B, T=T, C=C, N=N, G=G, in_dtype=dtype, y_dtype=dtype, dt_softplus=1)
+    return SsmDesc(*M.sizes(B, T, C, N, G), in_dtype=dtype, y_dtype=dtype, dt_softplus=1)
 
 
 def ssm_checkpoint_bytes(B: int, T: int, C: int, N: int) -> int:
@@ -98,6 +98,7 @@ def _inputs(x, dt, A, Bm, Cm, D, dt_bias, z, lengths, step):
 
 
 def _desc(x, y, B, T, C, N, G, softplus, lengths=None, S=0):
+    M.sizes(B, T, C, N, G, S)
     return SsmDesc(B, T, C, N, G, M.dtype_code(x), M.dtype_code(y), 1 if softplus else 0, S, 0, M.ptr(lengths))
 
 

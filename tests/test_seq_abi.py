@@ -316,6 +316,23 @@ except ValueError as e:
     assert r.returncode == 0 and r.stdout.strip() == "refused", r.stderr
 
 
+def test_bindings_refuse_sizes_past_an_int32():
+    """2^32 + 5 rows are not 5."""
+    import torch
+    x, many = torch.zeros(2, 3, 8), (1 << 32) + 5
+    for q in (lambda n: S.ssm_checkpoint_bytes(n, 1, 1, 1), lambda n: S.ssm_checkpoint_bytes(1, n, 1, 1),
+              lambda n: S.ssm_backward_workspace_bytes(1, 1, n, 1), lambda n: S.ssm_backward_workspace_bytes(1, 1, 1, 1, G=n),
+              lambda n: K.shortconv_backward_workspace_bytes(n, 1, 1, 4), lambda n: N.groupnorm_workspace_bytes(n, 1, 1, 1),
+              lambda n: N.groupnorm_backward_workspace_bytes(1, 1, n, 1),
+              # what the calls make of their tensors' shapes
+              lambda n: S._desc(x, x, n, 1, 1, 1, 1, True), lambda n: S._desc(x, x, 1, 1, 1, 1, 1, True, None, n),
+              lambda n: K._desc(x, x, n, 1, 1, 4, "silu"), lambda n: K._desc(x, x, 1, 1, 1, 4, "silu", n),
+              lambda n: N._desc(x, x, n, 1, 1, 1, "none", 1e-5, None)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            q(many)
+        q(1)
+
+
 def test_gradients_under_other_names_are_refused():
     """A caller's output tensor under a name that is no gradient's would stay as it was."""
     import torch
