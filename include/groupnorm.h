@@ -11,6 +11,10 @@
  * row by itself: a recurrence's output [batch, tokens, H, D] is [batch * tokens,
  * 1, H D] with G = H here.
  *
+ * The gate is for act(norm) * gate only.  A layer that adds something between the norm and
+ * the gate, such as a bonus of the token itself, calls this without a gate, adds, and gates
+ * by itself; wkv7_forward's r_k adds its bonus to y, so before any norm that follows.
+ *
  * weight, bias [C] fp32 (NULL: 1 and 0); gate of in_dtype or NULL; mean, rstd
  * [B, G] fp32.
  *

@@ -11,15 +11,17 @@
 // has 8 channels of a row, LG neighbouring lanes a group.  The variance is that of the
 // differences from the mean.  A workgroup takes several rows, so that weights are
 // loaded once and, in the backward, a thread sums its channels' parameter gradients
-// over its rows.  32768 x 4096 bf16 in 64 groups with a gate, 805 MB: forward 165 us
-// (4.9 TB/s, a copy's rate); 8192 x 2048 forward and backward 62 us.
+// over its rows.  32768 x 4096 bf16 in 64 groups with a gate, 805 MB (as counted): forward 162 us
+// (5.0 TB/s, a copy's rate); 8192 x 2048 forward and backward 61 us, the kernels at 5.1 TB/s.
 //
 // T = 1, other groups of up to 1024 or, even, 2048 channels: the same with one wave
-// to a group.
+// to a group, one load of 4 bytes a lane and run: far from a copy.  32768 rows of about 4000 channels, bf16
+// with a gate: groups of 80 604 us (1.3 TB/s), of 96 516, of 160 421, of 192 382 (2.1 TB/s).  Whole rows of
+// 4096 go through the three passes below: 370 us (2.2 TB/s).
 //
 // T > 1, a group's values within the registers of a workgroup of 1024: one pass, the
-// sums over the workgroup; 3 x 1531 x 960 fp32 in 30 groups 12.9 us, which the 90
-// workgroups bound (35 MB).
+// sums over the workgroup; 3 x 1531 x 960 fp32 in 30 groups 13.0 us (bf16 12.8),
+// which the 90 workgroups bound (35 MB at most, vector units 9% busy).
 //
 // Otherwise three passes: partial (mean, sum of squared differences) of up to 64
 // positions of a channel slot (8 channels of one group, or 1), formed block by

@@ -2,15 +2,17 @@
 // channel, for prompts, single tokens and training.
 //
 // Every direction reads and writes each element once and does a few operations
-// on it, so memory is what bounds it.  A thread has V consecutive channels (16
+// on it, so memory bounds it first.  A thread has V consecutive channels (16
 // bytes of bf16 inputs where C allows) and a run of tokens; the last K - 1 inputs
 // stay in its registers, so a token's row is loaded once and only the K - 1 rows
 // before a run are read twice.  The backward goes over a run once more from the
 // same loads: it recomputes the value before the activation, and the gradient of
 // input t is complete when output t + K - 1 has been passed.  Measured with K = 4,
-// bf16: forward 8 x 4096 x 4096 (537 MB) 123 us, 4.4 TB/s where a copy of that size
-// makes 5.2; forward and backward 4 x 2048 x 2048 51 us; a step of 256 x 4096 8.5 us,
-// most of it the launch.
+// bf16: forward 8 x 4096 x 4096 (537 MB; counted 564, the rows before each run with them)
+// 118 to 122 us, 4.4 to 4.6 TB/s where a copy of that size makes 5.2, vector units 62% busy; forward and
+// backward 4 x 2048 x 2048 51 us, the backward's kernel 29 to 31 of them: counted 146 MB, 1.4
+// times what it needs (a run of 16 tokens loads 22 rows of x and 19 of dy), at 4.9 TB/s, vector units 69% busy; a
+// step of 256 x 4096 8.6 us, most of it the launch.
 #include "seq_device.h"
 #include "seq_internal.h"
 

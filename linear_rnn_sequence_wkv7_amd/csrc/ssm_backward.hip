@@ -22,10 +22,11 @@
 // registers, which is what lets four waves share a SIMD: with four states a lane and
 // two waves the same work issued a fifth more slowly.
 //
-// Bound: the vector units, busy 84% of the time.  34 instructions per state and token:
+// Bound: the vector units, busy 83% of the time.  33 instructions per state and token:
 // 9 run the gradients back and 6 or 7 are the sums over rows and channels; the others are
 // the decays, the states from zero and once more, the gradients from zero, the exchange and
-// the elements.  4 x 2048 tokens x 2048 channels of 16 states, bf16: 307 us.
+// the elements.  4 x 2048 tokens x 2048 channels of 16 states, bf16: 306 to 320 us,
+// 154 MB read and 236 MB written, 134 of which are the blocks' dB and dC.
 //
 // Sums over the rows and over a row's channels are transposing butterflies: a step
 // halves the values that a lane holds while it doubles the lanes summed.  dB and dC of

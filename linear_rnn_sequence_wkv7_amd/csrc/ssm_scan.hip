@@ -36,8 +36,9 @@
 // Bound: the vector units.  A state and token needs a multiplication and an
 // exponential for its decay, a product, an update and a readout (two updates where
 // WT > 1); an exponential takes the time of two of the others and a half.  Measured at
-// N = 16, G = 1, bf16: 8 x 4096 tokens x 4096 channels 635 us (1.7 TB/s; 3.4e12
-// updates of a state a second), 1 x 2048 x 4096 54 us.  Tried and left: 2 states a
+// N = 16, G = 1, bf16: 8 x 4096 tokens x 4096 channels 625 us (vector units 81% busy, 8.3
+// instructions a state and token; 1.7 TB/s), 1 x 2048 x 4096 54 us (67% busy: a round's
+// barrier and LDS traffic stand open with two waves to a SIMD).  Tried and left: 2 states a
 // lane and twice the waves (786 and 72 us: the elements and barriers count twice), the
 // next round's elements formed between this one's updates (no faster).
 #include "seq_device.h"
@@ -269,7 +270,10 @@ __global__ __launch_bounds__(64 * WT) void ssm_scan_kernel(SsmParams g) {
 int64_t scan_blocks(const SsmParams& p) { return int64_t(p.B) * p.G * ((p.C / p.G + CH - 1) / CH); }
 // Waves over the tokens while the chip has room for them: 8 while each workgroup has a compute unit
 // to itself, 1 from two waves for every SIMD on.  1024 tokens, N = 16, bf16, us with 1, 4, 8 waves: 256
-// workgroups 112, 41, 32; 320: 120, 56, 58; 1024: 118, 102, 110; 2048: 161, 192, 217.
+// workgroups 112, 41, 32; 320: 120, 56, 58; 1024: 118, 102, 110; 2048: 161, 192, 217.  More than 16 states
+// are 8 or 16 of a lane, and the decays and inputs of 16 tokens that several waves keep for their second run
+// would be 256 registers or more: always one wave, however few channels (1 x 2048 x 4096 with N = 16, 32, 64:
+// 60, 301, 500 us; 8 x 4096 x 4096 with 16, 32: 624, 988).
 int scan_waves(const SsmParams& p) {
     const int64_t blocks = scan_blocks(p);
     return p.N > 16 || blocks >= 2048 || p.T <= TW ? 1 : blocks > 256 || p.T <= 4 * TW ? 4 : 8;
