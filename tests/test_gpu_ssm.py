@@ -377,3 +377,28 @@ def test_step_sizes_at_the_ends():
     S.check("state", to_host(s), s_ref, s_tol)
     # each channel to its own scale
     assert np.max(np.abs(to_host(s) - s_ref).max(-1) / np.abs(s_ref).max(-1)) <= 600 * S.U
+
+
+@pytest.mark.parametrize("T,C,N,softplus", [(17, 16, 16, True), (150, 20, 16, True), (150, 20, 24, True), (70, 18, 7, False)])
+def test_growing_states(T, C, N, softplus):
+    """Rates of both signs, 0 among them, and given steps of both signs: states that grow up to some e^10."""
+    B = 2
+    x = S.scan_inputs(T, B, T, C, N, 1, "f32", state=True, bias=softplus)
+    rng = np.random.default_rng(N)
+    x["A"] = rng.uniform(-0.5, 0.1, (C, N)).astype(np.float32)
+    x["A"][0], x["A"][1, 0] = 0.0, 0.1
+    if not softplus:
+        x["dt"] = (rng.standard_normal((B, T, C)) * 0.4).astype(np.float32)
+    dy, ds = rng.standard_normal((B, T, C)).astype(np.float32), rng.standard_normal((B, C, N)).astype(np.float32)
+    a, kw = dev_args(x)
+    kw["state"] = to_dev(x["state"])
+    (y_ref, s_ref), (y_tol, s_tol) = S.scan_bounds(x, T, None, softplus, B=B, Cg=C)
+    y, s = M().ssm_forward(*a, softplus=softplus, **kw)
+    S.check("y", to_host(y), y_ref, y_tol)
+    S.check("state", to_host(s), s_ref, s_tol)
+    ref, tol = S.scan_bounds(x, T, None, softplus, dy=dy, dstate=ds, B=B, Cg=C)
+    g = M().ssm_backward(*a, to_dev(dy), dstate=to_dev(ds), softplus=softplus, **kw)
+    torch().cuda.synchronize()
+    for k in ref:
+        if g[k] is not None:
+            S.check("d" + k, to_host(g[k]), ref[k], tol[k])
