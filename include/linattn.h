@@ -1,0 +1,95 @@
+/*
+ * linattn.h -- C ABI of linear attention with a decay for each head in libwkv7.so
+ * (AMD MI355X, gfx950): a matrix state per head that decays by one factor a token
+ * and takes up the token's key and value.
+ *
+ * Per batch b and head h, with S of Dk x Dv, over tokens t:
+ *
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T
+ *     y_t = scale S_t^T q_t
+ *
+ * Heads: H for g, y and the states; q has Hq, k has Hk and v has Hv heads, each a divisor
+ * of H: head h uses head h / (H / Hq) of q, and so on.
+ *
+ * Layouts (row-major, contiguous):
+ *     q [B, T, Hq, Dk]   k [B, T, Hk, Dk]   v [B, T, Hv, Dv]   y [B, T, H, Dv]
+ *     g : the logarithm of the decay, fp32, [B, T, H], or [H] (desc->g_per_token 0)
+ *     states : [B, H, Dk, Dv] fp32
+ * q, k and v have desc->in_dtype.
+ *
+ * Chunks of 64 tokens (32 where an array is fp32) are computed together, so a token that
+ * is not finite, and products past fp32's range, reach every output of their chunk and the
+ * ones behind it.  A growing state (g > 0) has to grow by a finite factor over a chunk.
+ * g = -inf empties the state; a g below about -1386 counts as -inf.
+ *
+ * Ragged batches (desc->lengths): tokens t >= lengths[b] of sequence b are padding: they
+ * leave the state as it was, their y is 0, and their gradients are 0; nothing about their
+ * input values matters.  A length below 0 counts as 0, one above T as T.
+ *
+ * Ownership, streams, errors, overlaps: as in ssm.h.
+ */
+#ifndef LINATTN_H
+#define LINATTN_H
+
+#include <stdint.h>
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef struct linattn_desc {
+    int32_t B;           /* batch, >= 0 */
+    int32_t T;           /* tokens, >= 0 (linattn_step: 1) */
+    int32_t H;           /* heads, >= 0 */
+    int32_t Hq, Hk, Hv;  /* heads of q, k and v, divisors of H (0 means H) */
+    int32_t Dk, Dv;      /* 1 .. 128 (larger: EUNSUPPORTED) */
+    int32_t in_dtype;    /* wkv7_dtype of q, k, v */
+    int32_t y_dtype;     /* wkv7_dtype of y (and of dy in the backward) */
+    int32_t g_per_token; /* 1: g is [B, T, H]; 0: [H] */
+    int32_t S;           /* linattn_step: states in the pool; ignored elsewhere */
+    float   scale;       /* finite */
+    int32_t reserved;    /* 0 */
+    const int32_t* lengths; /* [B] device int32, 4-byte aligned, or NULL: every sequence has T tokens
+                               (linattn_step: must be NULL) */
+} linattn_desc;
+
+/* Workspace bytes of linattn_forward: states between the parts of sequences that are
+ * computed side by side when there are few heads; often 0.  A negative wkv7_status if the
+ * descriptor is invalid.  Host only. */
+int64_t linattn_workspace_bytes(const linattn_desc* desc);
+
+/* y over T tokens from state_in (or zeros); state_out (may be NULL) gets the state after
+ * the last token of each sequence.  state_in == state_out is allowed.  T == 0 copies
+ * state_in (or zeros) to state_out. */
+int linattn_forward(const linattn_desc* desc, const void* q, const void* k, const void* v, const float* g,
+                    const float* state_in, void* y, float* state_out,
+                    void* workspace, int64_t workspace_bytes, void* stream);
+
+/* One token per row, on a pool of states: q [B, Hq, Dk], k [B, Hk, Dk], v [B, Hv, Dv],
+ * g [B, H] or [H], y [B, H, Dv], state [S, H, Dk, Dv] updated in place.  state_index as in
+ * ssm_step: rows without a request and later rows of the same state have y 0 and touch no
+ * state. */
+int linattn_step(const linattn_desc* desc, const void* q, const void* k, const void* v, const float* g,
+                 float* state, const int32_t* state_index, void* y, void* stream);
+
+/* Workspace bytes of linattn_backward; 0 when there is nothing to compute.  Host only. */
+int64_t linattn_backward_workspace_bytes(const linattn_desc* desc);
+
+/* The gradients of <dy, y> + <dstate_out, state_out> for linattn_forward with these inputs.
+ *   dy         : [B, T, H, Dv] of y_dtype
+ *   dstate_out : [B, H, Dk, Dv] fp32 or NULL (zero)
+ *   dq, dk, dv : as q, k, v, of in_dtype, summed over the heads that share one
+ *   dg         : as g, fp32, or NULL (not computed); [H]: summed over batch and tokens
+ *   dstate_in  : [B, H, Dk, Dv] fp32 or NULL (not computed)
+ *   workspace  : at least linattn_backward_workspace_bytes(desc) bytes.
+ * dg is 0 where g counts as -inf.  T == 0: dg [H] is 0 and dstate_in is dstate_out (or 0). */
+int linattn_backward(const linattn_desc* desc, const void* q, const void* k, const void* v, const float* g,
+                     const float* state_in, const void* dy, const float* dstate_out,
+                     void* dq, void* dk, void* dv, float* dg, float* dstate_in,
+                     void* workspace, int64_t workspace_bytes, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* LINATTN_H */

@@ -7,5 +7,6 @@ Submodules:
   ssm       -- the same for the selective state space scan (prompt, step, backward)
   shortconv -- the short causal convolution in front of a recurrence
   groupnorm -- the group norm, activation and gate behind one
+  linattn   -- linear attention with a decay for each head (prompt, step, backward)
 """
-__all__ = ["inputs", "wkv7", "ssm", "shortconv", "groupnorm"]
+__all__ = ["inputs", "wkv7", "ssm", "shortconv", "groupnorm", "linattn"]

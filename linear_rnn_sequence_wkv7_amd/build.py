@@ -26,7 +26,8 @@ ARCH = "gfx950"
 
 SOURCES = ["wkv7_api.cpp", "wkv7_scan.hip", "wkv7_decode.hip", "wkv7_chunked.hip", "wkv7_chunked128.hip",
            "wkv7_twopass128.hip", "wkv7_twopass128_scan.hip", "wkv7_backward.hip", "wkv4.hip",
-           "seq_api.cpp", "ssm_scan.hip", "ssm_backward.hip", "shortconv.hip", "groupnorm.hip"]
+           "seq_api.cpp", "ssm_scan.hip", "ssm_backward.hip", "shortconv.hip", "groupnorm.hip",
+           "linattn/linattn.hip", "linattn/linattn_bf16.hip", "linattn/linattn_f32.hip"]
 
 COMMON = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
@@ -59,6 +60,10 @@ def hipcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("hipcc not found")
+
+
+def _stem(src: str) -> str:
+    return os.path.splitext(os.path.basename(src))[0]
 
 
 def _run(cmd):
@@ -95,7 +100,7 @@ def build(asm: bool = False, verbose: bool = False) -> str:
     jobs = []
     objs = []
     for src in SOURCES:
-        obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
+        obj = os.path.join(BUILD, _stem(src) + ".o")
         objs.append(obj)
         lang = ["-x", "hip"] if src.endswith(".hip") else []
         extra = EXTRA.get(src, [])
@@ -104,7 +109,7 @@ def build(asm: bool = False, verbose: bool = False) -> str:
         if asm and src.endswith(".hip"):
             jobs.append([cc, *COMMON, *extra, "-x", "hip", "--cuda-device-only", "-S",
                          os.path.join(CSRC, src), "-o",
-                         os.path.join(BUILD, os.path.splitext(src)[0] + f"-{ARCH}.s")])
+                         os.path.join(BUILD, _stem(src) + f"-{ARCH}.s")])
     scratch = {}
     with cf.ThreadPoolExecutor(max_workers=min(8, len(jobs))) as ex:
         for out in ex.map(_run, jobs):
@@ -139,7 +144,7 @@ def build_host_sanitized(out_dir: str) -> str:
     common = [f for f in COMMON if f != "-O3"] + ["-O1", "-g"]
     jobs, objs = [], []
     for src in SOURCES:
-        obj = os.path.join(out_dir, os.path.splitext(src)[0] + ".o")
+        obj = os.path.join(out_dir, _stem(src) + ".o")
         objs.append(obj)
         lang = ["-x", "hip"] if src.endswith(".hip") else []
         jobs.append([cc, *common, *EXTRA.get(src, []), *SANITIZE_HOST, *lang, "-c", os.path.join(CSRC, src), "-o", obj])

@@ -1,0 +1,405 @@
+// Linear attention with a decay for each head: how a call is split up, and what runs beside the
+// sweeps of linattn_core.h: the chain of the segments' states, the gradient of g, sums over heads
+// that share an operand, and the step on a pool of states.
+#include "../seq_device.h"
+#include "linattn_internal.h"
+#include "wave_sum64.h"
+
+namespace wkv7 {
+namespace linattn {
+namespace {
+
+constexpr int kThreads = 256;
+
+// ---------------------------------------------------------------- chain of segments
+
+struct Chain {
+    float* ws;            // [B, H, segs, Dk, Dv]: what the segments add; becomes the state before each
+    const float* kept;    // [B, H, segs]
+    const float* first;   // [B, H, Dk, Dv] or null
+    float* last;
+};
+// A thread per element of a state.  Eight segments' parts are read before the first is needed.
+__global__ __launch_bounds__(kThreads) void chain_kernel(Chain f, Chain r, int segs, int elems) {
+    const bool back = blockIdx.z;
+    const Chain c = back ? r : f;
+    const int e = blockIdx.x * kThreads + threadIdx.x;
+    const int64_t bh = blockIdx.y;
+    if (e >= elems) return;
+    float s = c.first ? c.first[bh * elems + e] : 0.f;
+    float* p = c.ws + bh * segs * int64_t(elems) + e;
+    const float* k = c.kept + bh * segs;
+    for (int i0 = 0; i0 < segs; i0 += 8) {
+        float u[8];
+        #pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int at = back ? segs - 1 - i0 - i : i0 + i;
+            u[i] = i0 + i < segs ? p[int64_t(at) * elems] : 0.f;
+        }
+        #pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i0 + i >= segs) break;
+            const int at = back ? segs - 1 - i0 - i : i0 + i;
+            p[int64_t(at) * elems] = s;
+            s = fmaf(k[at], s, u[i]);
+        }
+    }
+    if (c.last) c.last[bh * elems + e] = s;
+}
+
+// ---------------------------------------------------------------- gradient of g
+
+// The gradient of g_t is the sum over u >= t of <q_u, dq_u> - <k_u, dk_u>, and <state, its
+// gradient> behind the last token: what a change of every running sum from t on does.  A
+// workgroup per sequence and head, from the end, 4096 tokens at a time, summed in 64 bits.
+constexpr int kDgThreads = 1024, kDgPer = 4;
+__global__ __launch_bounds__(kDgThreads) void dg_kernel(const float* qd, const float* kd, const float* end, Chunks w, float* dg, float* part) {
+    __shared__ double sums[kDgThreads / 64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int h = int(blockIdx.x % w.H);
+    const int64_t b = blockIdx.x / w.H, bh = blockIdx.x;
+    const int len = seq_length(w.lengths, b, w.T);
+    double run = end ? end[bh] : 0.f, total = 0.0;
+    for (int r0 = 0; r0 < w.T; r0 += kDgThreads * kDgPer) {
+        const int r = r0 + tid * kDgPer;   // tokens counted from the end
+        double v[kDgPer], sum = 0.0;
+        #pragma unroll
+        for (int i = 0; i < kDgPer; ++i) {
+            const int t = w.T - 1 - r - i;
+            if (t >= 0) sum += double(qd[bh * w.T + t]) - double(kd[bh * w.T + t]);
+            v[i] = sum;
+        }
+        const double in = running_sum(sum, lane);
+        __syncthreads();
+        if (lane == 63) sums[wave] = in;
+        __syncthreads();
+        double before = run + (in - sum), all = 0.0;
+        for (int i = 0; i < kDgThreads / 64; ++i) {
+            if (i < wave) before += sums[i];
+            all += sums[i];
+        }
+        run += all;
+        #pragma unroll
+        for (int i = 0; i < kDgPer; ++i) {
+            const int t = w.T - 1 - r - i;
+            if (t < 0) continue;
+            const float g = w.g_per_token ? w.g[(b * w.T + t) * w.H + h] : w.g[h];
+            const double d = t >= len || double(g) * 1.4426950408889634074 < kNoDecayLog2 ? 0.0 : before + v[i];
+            if (w.g_per_token) dg[(b * w.T + t) * w.H + h] = float(d);
+            else total += d;
+        }
+    }
+    if (!w.g_per_token) {
+        const double in = running_sum(total, lane);
+        __syncthreads();
+        if (lane == 63) sums[wave] = in;
+        __syncthreads();
+        if (tid == 0) {
+            total = 0.0;
+            for (int i = 0; i < kDgThreads / 64; ++i) total += sums[i];
+            part[bh] = float(total);
+        }
+    }
+}
+__global__ __launch_bounds__(64) void dg_heads_kernel(const float* part, float* dg, int B, int H) {
+    const int h = blockIdx.x * 64 + threadIdx.x;
+    if (h >= H) return;
+    double s = 0.0;
+    for (int64_t b = 0; b < B; ++b) s += part[b * H + h];
+    dg[h] = float(s);
+}
+
+// ---------------------------------------------------------------- sums over shared heads
+
+// out [rows, heads, D] = the sum over each head's H / heads gradients in x [rows, H, D], in their order.
+template <int E>
+__global__ __launch_bounds__(kThreads) void shared_sum_kernel(const float* x, void* out, int64_t items, int group, int D, bool bf16) {
+    const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+    if (i >= items) return;
+    const int64_t at = i * E, head = at / D;
+    const float* p = x + head * group * D + at % D;
+    float s[E] = {};
+    for (int j = 0; j < group; ++j) {
+        const Pack<float, E> v = ld_pack<E>(p + int64_t(j) * D, true, E);
+        #pragma unroll
+        for (int e = 0; e < E; ++e) s[e] += v.e[e];
+    }
+    st_pack_as<E>(out, at, bf16, s, true, E);
+}
+
+// ---------------------------------------------------------------- step
+
+// Columns of a state for a workgroup: 64, or 16 where that is needed to occupy the chip.
+// A thread has 4 columns (VEC: in one piece) of every RG-th row; the state is read once, kept in
+// registers and written once, everything else is small beside it.
+template <typename T, int CB, int ROWS, bool VEC>
+__global__ __launch_bounds__(kThreads) void step_kernel(LinAttnParams p) {
+    constexpr int CL = CB / 4, RG = kThreads / CL, N = ROWS / RG;
+    __shared__ float part[kThreads / 64][CB];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int blocks = (p.Dv + CB - 1) / CB;
+    const int64_t item = xcd_order(blockIdx.x, gridDim.x);
+    const int cb = int(item % blocks), h = int(item / blocks % p.H), b = int(item / blocks / p.H);
+    const int j = cb * CB + tid % CL * 4, r0 = tid / CL, Dk = p.Dk, Dv = p.Dv;
+    const int slot = p.index ? p.index[b] : b;
+    bool mine[1] = {slot >= 0 && slot < p.S};
+    float* st = p.s1 + (int64_t(mine[0] ? slot : 0) * p.H + h) * Dk * Dv;
+    const T* q = static_cast<const T*>(p.q) + (int64_t(b) * p.Hq + h / (p.H / p.Hq)) * Dk;
+    const T* k = static_cast<const T*>(p.k) + (int64_t(b) * p.Hk + h / (p.H / p.Hk)) * Dk;
+    const T* v = static_cast<const T*>(p.v) + (int64_t(b) * p.Hv + h / (p.H / p.Hv)) * Dv;
+    Pack<float, 4> s[N];
+    float qi[N], ki[N], vj[4], y[4] = {};
+    if (mine[0] && j < Dv) {
+        #pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int i = r0 + n * RG;
+            if (i < Dk) s[n] = ld_pack<4>(st + i * Dv + j, VEC, Dv - j);
+        }
+    }
+    #pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const int i = r0 + n * RG;
+        qi[n] = i < Dk ? widen(q[i]) : 0.f;
+        ki[n] = i < Dk ? widen(k[i]) : 0.f;
+    }
+    #pragma unroll
+    for (int e = 0; e < 4; ++e) vj[e] = j + e < Dv ? widen(v[j + e]) : 0.f;
+    const float a = expf(p.g_per_token ? p.g[int64_t(b) * p.H + h] : p.g[h]);
+    if (p.index) first_of_slots<1>(p.index, b, &slot, mine, kThreads);
+    if (mine[0] && j < Dv) {
+        #pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int i = r0 + n * RG;
+            if (i >= Dk) continue;
+            float o[4];
+            #pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                o[e] = fmaf(a, s[n].e[e], ki[n] * vj[e]);
+                y[e] = fmaf(qi[n], o[e], y[e]);
+            }
+            st_pack<4>(st + i * Dv + j, o, VEC, Dv - j);
+        }
+    }
+    #pragma unroll
+    for (int e = 0; e < 4; ++e)
+        #pragma unroll
+        for (int m = CL; m < 64; m *= 2) y[e] += __shfl_xor(y[e], m);
+    if (lane < CL)
+        #pragma unroll
+        for (int e = 0; e < 4; ++e) part[wave][lane * 4 + e] = y[e];
+    __syncthreads();
+    if (tid < CB && cb * CB + tid < Dv) {
+        const float sum = p.scale * (part[0][tid] + part[1][tid] + (part[2][tid] + part[3][tid]));
+        const int64_t o = (int64_t(b) * p.H + h) * Dv + cb * CB + tid;
+        if (p.y_bf16) static_cast<bf16_t*>(p.y)[o] = f32_to_bf16(mine[0] ? sum : 0.f);
+        else static_cast<float*>(p.y)[o] = mine[0] ? sum : 0.f;
+    }
+}
+
+int step_columns(const LinAttnParams& p) { return int64_t(p.B) * p.H * ((p.Dv + 63) / 64) >= 512 ? 64 : 16; }
+
+template <typename T, int CB>
+hipError_t step_rows(const LinAttnParams& p, dim3 grid, hipStream_t st) {
+    if (p.Dk <= 64) {
+        if (p.Dv % 4 == 0) step_kernel<T, CB, 64, true><<<grid, kThreads, 0, st>>>(p);
+        else step_kernel<T, CB, 64, false><<<grid, kThreads, 0, st>>>(p);
+    } else {
+        if (p.Dv % 4 == 0) step_kernel<T, CB, 128, true><<<grid, kThreads, 0, st>>>(p);
+        else step_kernel<T, CB, 128, false><<<grid, kThreads, 0, st>>>(p);
+    }
+    return hipGetLastError();
+}
+
+// ---------------------------------------------------------------- how a call is split up
+
+// Sequences in `kinds` sweeps a head are cut into segments where there are fewer heads than the
+// chip takes side by side.
+void plan(const LinAttnParams& p, int kinds, Chunks* w) {
+    const int64_t heads = int64_t(p.B) * p.H * kinds, chunks = (int64_t(p.T) + 63) / 64;
+    int64_t segs = 512 / (heads > 0 ? heads : 1);
+    segs = segs < 1 ? 1 : segs > chunks ? chunks : segs;
+    const int64_t each = segs > 0 ? (chunks + segs - 1) / segs : 1;
+    *w = Chunks{p.B, p.T, p.H, int(each > 0 && chunks > 0 ? (chunks + each - 1) / each : 1), int(each * 64), p.g_per_token, p.g, p.lengths};
+}
+
+struct Carve {   // pieces of a workspace
+    char* base;
+    int64_t at = 0;
+    float* floats(int64_t n) {
+        float* r = reinterpret_cast<float*>(base + at);
+        at += (n * 4 + 255) / 256 * 256;
+        return r;
+    }
+};
+struct ForwardWs {
+    float *states, *kept;
+    int64_t bytes;
+    ForwardWs(const LinAttnParams& p, const Chunks& w, void* ws) {
+        Carve c{static_cast<char*>(ws)};
+        const int64_t n = w.segs > 1 ? int64_t(p.B) * p.H * w.segs : 0;
+        states = c.floats(n * p.Dk * p.Dv);
+        kept = c.floats(n);
+        bytes = c.at;
+    }
+};
+struct BackwardWs {
+    float *qd, *kd, *end, *part, *states[2], *kept[2], *dq, *dk, *dv;
+    int64_t bytes;
+    BackwardWs(const LinAttnParams& p, const Chunks& w, void* ws) {
+        Carve c{static_cast<char*>(ws)};
+        const int64_t bh = int64_t(p.B) * p.H, n = w.segs > 1 ? bh * w.segs : 0;
+        qd = c.floats(bh * p.T);
+        kd = c.floats(bh * p.T);
+        end = c.floats(bh);
+        part = c.floats(bh);
+        for (int i = 0; i < 2; ++i) {
+            states[i] = c.floats(n * p.Dk * p.Dv);
+            kept[i] = c.floats(n);
+        }
+        dq = c.floats(p.Hq < p.H ? bh * p.T * p.Dk : 0);
+        dk = c.floats(p.Hk < p.H ? bh * p.T * p.Dk : 0);
+        dv = c.floats(p.Hv < p.H ? bh * p.T * p.Dv : 0);
+        bytes = c.at;
+    }
+};
+
+hipError_t chain(const Chunks& w, const Chain& f, const Chain& r, int kinds, int elems, hipStream_t st) {
+    // heads by 32768, the most that a grid's second dimension is asked for
+    const int64_t bh = int64_t(w.B) * w.H;
+    for (int64_t h0 = 0; h0 < bh; h0 += 32768) {
+        const uint32_t n = uint32_t(bh - h0 < 32768 ? bh - h0 : 32768);
+        auto from = [&](Chain c) {
+            c.ws += h0 * w.segs * elems;
+            c.kept += h0 * w.segs;
+            c.first = c.first ? c.first + h0 * elems : nullptr;
+            c.last = c.last ? c.last + h0 * elems : nullptr;
+            return c;
+        };
+        chain_kernel<<<dim3((elems + kThreads - 1) / kThreads, n, kinds), kThreads, 0, st>>>(from(f), kinds > 1 ? from(r) : from(f), w.segs, elems);
+    }
+    return hipGetLastError();
+}
+
+hipError_t shared_sum(const float* x, void* out, int64_t rows, int heads, int group, int D, bool bf16, hipStream_t st) {
+    const int64_t n = rows * heads * D;
+    if (D % 4 == 0) shared_sum_kernel<4><<<uint32_t((n / 4 + kThreads - 1) / kThreads), kThreads, 0, st>>>(x, out, n / 4, group, D, bf16);
+    else shared_sum_kernel<1><<<uint32_t((n + kThreads - 1) / kThreads), kThreads, 0, st>>>(x, out, n, group, D, bf16);
+    return hipGetLastError();
+}
+
+#define TRY(call)                            \
+    do {                                     \
+        const hipError_t e_ = (call);        \
+        if (e_ != hipSuccess) return e_;     \
+    } while (0)
+
+}  // namespace
+}  // namespace linattn
+
+using namespace linattn;
+
+int64_t linattn_forward_workspace(const LinAttnParams& p) {
+    Chunks w;
+    plan(p, 1, &w);
+    return ForwardWs(p, w, nullptr).bytes;
+}
+int64_t linattn_backward_workspace(const LinAttnParams& p) {
+    if (int64_t(p.B) * p.T * p.H == 0) return 0;
+    Chunks w;
+    plan(p, 3, &w);
+    return BackwardWs(p, w, nullptr).bytes;
+}
+int64_t linattn_forward_threads(const LinAttnParams& p) {
+    Chunks w;
+    plan(p, 1, &w);
+    return int64_t(p.B) * p.H * w.segs * 512;
+}
+int64_t linattn_step_threads(const LinAttnParams& p) {
+    const int cb = step_columns(p);
+    return int64_t(p.B) * p.H * ((p.Dv + cb - 1) / cb) * kThreads;
+}
+int64_t linattn_backward_threads(const LinAttnParams& p) {
+    Chunks w;
+    plan(p, 3, &w);
+    const int64_t sweeps = int64_t(p.B) * p.H * w.segs * 3 * 512, rows = int64_t(p.B) * p.T;
+    const int64_t dg = int64_t(p.B) * p.H * kDgThreads, sums = rows * p.H * (p.Dk > p.Dv ? p.Dk : p.Dv);
+    return sweeps > dg ? (sweeps > sums ? sweeps : sums) : (dg > sums ? dg : sums);
+}
+
+hipError_t launch_linattn_forward(const LinAttnParams& p, hipStream_t st) {
+    Chunks w;
+    plan(p, 1, &w);
+    const ForwardWs ws(p, w, p.ws);
+    Sweep s{};
+    s.a = {p.q, p.Hq, p.Dk, p.in_bf16};
+    s.b = {p.k, p.Hk, p.Dk, p.in_bf16};
+    s.c = {p.v, p.Hv, p.Dv, p.in_bf16};
+    s.out = p.y; s.out_heads = p.H; s.out_bf16 = p.y_bf16;
+    s.sp = s.si = p.scale; s.su = 1.f;
+    s.ws = ws.states; s.kept = ws.kept;
+    s.s_in = p.s0; s.s_out = p.s1;
+    if (w.segs > 1) {
+        TRY(p.in_bf16 ? parts_bf16(w, s, s, 1, st) : parts_f32(w, s, s, 1, st));
+        TRY(chain(w, {ws.states, ws.kept, p.s0, p.s1}, {}, 1, p.Dk * p.Dv, st));
+    }
+    return p.in_bf16 ? forward_bf16(w, s, st) : forward_f32(w, s, st);
+}
+
+hipError_t launch_linattn_step(const LinAttnParams& p, hipStream_t st) {
+    const int cb = step_columns(p);
+    const dim3 grid(uint32_t(int64_t(p.B) * p.H * ((p.Dv + cb - 1) / cb)));
+    if (cb == 64) return p.in_bf16 ? step_rows<bf16_t, 64>(p, grid, st) : step_rows<float, 64>(p, grid, st);
+    return p.in_bf16 ? step_rows<bf16_t, 16>(p, grid, st) : step_rows<float, 16>(p, grid, st);
+}
+
+hipError_t launch_linattn_backward(const LinAttnParams& p, hipStream_t st) {
+    Chunks w;
+    plan(p, 3, &w);
+    const BackwardWs ws(p, w, p.ws);
+    const int64_t rows = int64_t(p.B) * p.T;
+    const bool bf16 = p.in_bf16 && p.y_bf16;
+    const Operand q{p.q, p.Hq, p.Dk, p.in_bf16}, k{p.k, p.Hk, p.Dk, p.in_bf16}, v{p.v, p.Hv, p.Dv, p.in_bf16}, dy{p.dy, p.H, p.Dv, p.y_bf16};
+    // a gradient goes to its place, or, where heads share one, each head's to the workspace
+    if (p.B == 0) {
+        if (p.dg && !p.g_per_token) dg_heads_kernel<<<(p.H + 63) / 64, 64, 0, st>>>(ws.part, p.dg, 0, p.H);
+        return hipGetLastError();
+    }
+    auto make = [&](const Operand& a, const Operand& b, const Operand& c, void* out, float* each, int heads, bool back, bool transposed) {
+        Sweep s{};
+        s.a = a; s.b = b; s.c = c;
+        const bool shared = heads < p.H;
+        s.out = shared ? each : out; s.out_heads = p.H; s.out_bf16 = !shared && p.in_bf16;
+        s.sp = p.scale; s.si = back ? 1.f : p.scale; s.su = back ? p.scale : 1.f;
+        s.ws = ws.states[back]; s.kept = ws.kept[back];
+        s.s_in = back ? p.ds1 : p.s0;
+        s.back = back; s.transposed = transposed;
+        return s;
+    };
+    Sweep sq = make(dy, v, k, p.dq, ws.dq, p.Hq, false, true);
+    Sweep sk = make(v, dy, q, p.dk, ws.dk, p.Hk, true, true);
+    Sweep sv = make(k, q, dy, p.dv, ws.dv, p.Hv, true, false);
+    if (p.dg) {
+        sq.x = q; sq.dot = ws.qd;
+        sk.x = k; sk.dot = ws.kd;
+        sq.end_grad = p.ds1; sq.end_dot = p.ds1 ? ws.end : nullptr;
+    }
+    if (w.segs > 1) {
+        Sweep f = sv, r = sv;
+        f.b = k; f.c = v; f.back = false; f.su = 1.f; f.ws = ws.states[0]; f.kept = ws.kept[0];
+        TRY(bf16 ? parts_bf16(w, f, r, 2, st) : parts_f32(w, f, r, 2, st));
+        TRY(chain(w, {ws.states[0], ws.kept[0], p.s0, nullptr}, {ws.states[1], ws.kept[1], p.ds1, p.ds0}, 2, p.Dk * p.Dv, st));
+    } else {
+        sv.s_out = p.ds0;
+    }
+    TRY(bf16 ? backward_bf16(w, sq, sk, sv, st) : backward_f32(w, sq, sk, sv, st));
+    if (p.Hq < p.H && rows > 0) TRY(shared_sum(ws.dq, p.dq, rows, p.Hq, p.H / p.Hq, p.Dk, p.in_bf16, st));
+    if (p.Hk < p.H && rows > 0) TRY(shared_sum(ws.dk, p.dk, rows, p.Hk, p.H / p.Hk, p.Dk, p.in_bf16, st));
+    if (p.Hv < p.H && rows > 0) TRY(shared_sum(ws.dv, p.dv, rows, p.Hv, p.H / p.Hv, p.Dv, p.in_bf16, st));
+    if (p.dg) {
+        if (rows > 0) dg_kernel<<<uint32_t(int64_t(p.B) * p.H), kDgThreads, 0, st>>>(ws.qd, ws.kd, sq.end_dot, w, p.dg, ws.part);
+        if (!p.g_per_token) dg_heads_kernel<<<(p.H + 63) / 64, 64, 0, st>>>(ws.part, p.dg, rows > 0 ? p.B : 0, p.H);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace wkv7

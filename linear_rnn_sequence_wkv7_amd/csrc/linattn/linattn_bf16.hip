@@ -1,0 +1,116 @@
+// Linear attention on bf16 operands: v_mfma_f32_16x16x32_bf16.
+//
+// q, k, v (and dy) are bf16 already and go into the products as they are.  What is not, the
+// state, P and c times its decay, is split into two or three bf16 operands whose sum it is (to
+// 2^-17, or exactly): the products and sums are then as good as fp32's, and only what is stored
+// is rounded.  Three operands in the state's update (the state is an fp32 output) and in all of
+// dq's and dk's sums (their products with q and k become the fp32 gradient of g, a difference of
+// nearly equal sums); two in y's, where 2^-17 is far below y's own rounding.
+#include "linattn_core.h"
+
+namespace wkv7 {
+namespace linattn {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
+
+struct Bf16Ops {
+    using elem = bf16_t;
+    using Frag = bf16x8;
+    static constexpr int E = 8, K = 32, L = 64;
+    static constexpr int NPY = 2, NPU = 3;   // operands of a value in y's sums, and in the state's and the gradients'
+
+    static __device__ __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+
+    // Byte offset of a row's 16-byte piece in an LDS tile of D columns.  The pieces of a row trade
+    // places so that neither 16 rows' same piece (row()) nor 4 rows' 4 neighbouring ones (col())
+    // meet in a bank.
+    template <int D>
+    static __device__ __forceinline__ int at(int row, int piece) {
+        if constexpr (D == 128) return row * 256 + (piece ^ ((row & 3) << 2 | (row >> 2 & 3))) * 16;
+        else return row * 128 + (piece ^ ((row >> 1 & 1) << 2 | (row >> 2 & 3))) * 16;
+    }
+    static __device__ __forceinline__ constexpr int row_of(int tile, int c) { return pair_col(tile, c); }
+
+    // Elements 32 m + 8 g .. of a row.
+    template <int D>
+    static __device__ __forceinline__ Frag row(const char* tile, int r, int m, int g) {
+        return *reinterpret_cast<const Frag*>(tile + at<D>(r, 4 * m + g));
+    }
+    // Rows 32 m + 8 g .. of the lane's column.  A transposing read takes 4 neighbouring columns
+    // (from `from`) of 4 rows from 4 lanes each and gives every lane of the 16 its own column.
+    template <int D>
+    static __device__ __forceinline__ Frag col(const char* tile, int m, int from, int, int lane) {
+        const int r = 32 * m + 8 * (lane >> 4) + (lane >> 2 & 3), part = from % 8 * 2;
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(tile + at<D>(r, from / 8) + part));
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(tile + at<D>(r + 4, from / 8) + part));
+        return __builtin_bit_cast(Frag, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+    static __device__ __forceinline__ float get(Frag f, int e) {
+        const u32x4 w = __builtin_bit_cast(u32x4, f);
+        return __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+    }
+
+    // Two values as N words of two bf16: all but the last cut off, the last rounded.
+    template <int N>
+    static __device__ __forceinline__ void split2(float x, float y, uint32_t (&w)[N]) {
+        #pragma unroll
+        for (int p = 0; p < N - 1; ++p) {
+            w[p] = __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302);
+            x -= __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+            y -= __uint_as_float(__float_as_uint(y) & 0xffff0000u);
+        }
+        w[N - 1] = __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(x), static_cast<__bf16>(y)});
+    }
+    template <int N>
+    static __device__ __forceinline__ void split(const float* v, Frag* f) {
+        u32x4 q[N];
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t w[N];
+            split2<N>(v[2 * i], v[2 * i + 1], w);
+            #pragma unroll
+            for (int p = 0; p < N; ++p) q[p][i] = w[p];
+        }
+        #pragma unroll
+        for (int p = 0; p < N; ++p) f[p] = __builtin_bit_cast(Frag, q[p]);
+    }
+    template <int N>
+    static __device__ __forceinline__ void store_p(char* P, int t, int i0, const float* v) {
+        uint32_t lo[N], hi[N];
+        split2<N>(v[0], v[1], lo);
+        split2<N>(v[2], v[3], hi);
+        #pragma unroll
+        for (int p = 0; p < N; ++p) *reinterpret_cast<uint2*>(P + p * L * L * 2 + at<L>(t, i0 / 8) + i0 % 8 * 2) = uint2{lo[p], hi[p]};
+    }
+
+    template <bool WHOLE>
+    struct Piece {
+        Raw<bf16_t, 8, WHOLE> r;
+        __device__ __forceinline__ void load(rsrc_t d, uint32_t off, int n, bool) { r.load(d, off, n); }
+        __device__ __forceinline__ void store(char* p, bool) const {
+            if constexpr (WHOLE) {
+                *reinterpret_cast<u32x4*>(p) = u32x4{r.w[0], r.w[1], r.w[2], r.w[3]};
+            } else {
+                u32x4 w;
+                #pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = r.w[2 * i] | r.w[2 * i + 1] << 16;
+                *reinterpret_cast<u32x4*>(p) = w;
+            }
+        }
+    };
+};
+
+}  // namespace
+
+hipError_t parts_bf16(const Chunks& w, const Sweep& f, const Sweep& r, int kinds, hipStream_t st) { return launch_parts<Bf16Ops>(w, f, r, kinds, st); }
+hipError_t forward_bf16(const Chunks& w, const Sweep& s, hipStream_t st) { return launch_outs<Bf16Ops, Bf16Ops::NPY>(w, s, s, s, 1, st); }
+hipError_t backward_bf16(const Chunks& w, const Sweep& q, const Sweep& k, const Sweep& v, hipStream_t st) { return launch_backward<Bf16Ops>(w, q, k, v, st); }
+
+}  // namespace linattn
+}  // namespace wkv7

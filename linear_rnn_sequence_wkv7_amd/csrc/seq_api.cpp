@@ -1,14 +1,16 @@
 // C-ABI entry points of the selective state space scan, the short causal
-// convolution and the group norm: argument validation (before any HIP call) and
-// dispatch to the kernel launchers.  See include/ssm.h, include/shortconv.h and
-// include/groupnorm.h for the contracts.
+// convolution, the group norm and linear attention: argument validation (before
+// any HIP call) and dispatch to the kernel launchers.  See include/ssm.h,
+// include/shortconv.h, include/groupnorm.h and include/linattn.h for the contracts.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
 #include <cstdint>
 #include <cstring>
 
+#include "../../include/linattn.h"
 #include "../../include/wkv7.h"
+#include "linattn/linattn_internal.h"
 #include "seq_internal.h"
 #include "wkv7_host.h"
 
@@ -191,6 +193,48 @@ int norm_inputs(const NormParams& p, Arrays& a) {
     WKV7_TRY(a.add(p.weight, int64_t(p.C) * 4, "weight", false, false));
     WKV7_TRY(a.add(p.bias, int64_t(p.C) * 4, "bias", false, false));
     WKV7_TRY(a.add(p.gate, row * esize(p.in_bf16), "gate", false, false));
+    a.index(p.lengths, p.B, "lengths");
+    return WKV7_OK;
+}
+
+// ---------------------------------------------------------------- linear attention
+
+int linattn_desc_check(const linattn_desc* d, bool step, LinAttnParams* p) {
+    if (!d) return fail(WKV7_EINVAL, "desc is NULL");
+    if (d->B < 0 || d->T < 0 || d->H < 0 || d->Hq < 0 || d->Hk < 0 || d->Hv < 0)
+        return fail(WKV7_EINVAL, "negative size (B=%d T=%d H=%d Hq=%d Hk=%d Hv=%d)", d->B, d->T, d->H, d->Hq, d->Hk, d->Hv);
+    if (d->Dk <= 0 || d->Dv <= 0) return fail(WKV7_EINVAL, "Dk and Dv must be positive (got %d and %d)", d->Dk, d->Dv);
+    if (d->Dk > 128 || d->Dv > 128) return fail(WKV7_EUNSUPPORTED, "Dk=%d, Dv=%d; up to 128 are supported", d->Dk, d->Dv);
+    const int Hq = d->Hq ? d->Hq : d->H, Hk = d->Hk ? d->Hk : d->H, Hv = d->Hv ? d->Hv : d->H;
+    if (d->H ? d->H % Hq || d->H % Hk || d->H % Hv : Hq || Hk || Hv)
+        return fail(WKV7_EINVAL, "Hq=%d, Hk=%d and Hv=%d must divide H=%d", Hq, Hk, Hv, d->H);
+    WKV7_TRY(check_dtypes(d->in_dtype, d->y_dtype));
+    if (d->g_per_token != 0 && d->g_per_token != 1) return fail(WKV7_EINVAL, "g_per_token must be 0 or 1 (got %d)", d->g_per_token);
+    if (!std::isfinite(d->scale)) return fail(WKV7_EINVAL, "scale must be finite");
+    if (d->reserved != 0) return fail(WKV7_EINVAL, "reserved must be 0 (got %d)", d->reserved);
+    WKV7_TRY(check_lengths(d->lengths, !step));
+    if (step && d->T != 1) return fail(WKV7_EINVAL, "linattn_step needs T == 1 (got %d)", d->T);
+    // Offsets within 64 rows are 32-bit.
+    if (d->H >= (1 << 16)) return fail(WKV7_EUNSUPPORTED, "H=%d; less than 65536 heads are supported", d->H);
+    const int64_t bt = int64_t(d->B) * d->T, state = int64_t(d->H) * d->Dk * d->Dv;
+    if (bt > kMaxElems / 128 / (d->H ? d->H : 1) || int64_t(d->B) * d->H > kMaxItems || (state && d->B > kMaxElems / state) ||
+        (step && state && d->S > kMaxElems / state) || d->T > INT32_MAX - 4096)
+        return fail(WKV7_EUNSUPPORTED, "B=%d, T=%d, H=%d or S=%d too large", d->B, d->T, d->H, d->S);
+    *p = LinAttnParams{};
+    p->B = d->B; p->T = d->T; p->H = d->H; p->Hq = Hq; p->Hk = Hk; p->Hv = Hv; p->Dk = d->Dk; p->Dv = d->Dv; p->S = d->S;
+    p->in_bf16 = d->in_dtype == WKV7_BF16; p->y_bf16 = d->y_dtype == WKV7_BF16; p->g_per_token = d->g_per_token;
+    p->scale = d->scale; p->lengths = d->lengths;
+    return WKV7_OK;
+}
+int64_t linattn_rows(const LinAttnParams& p) { return int64_t(p.B) * p.T; }
+int64_t linattn_state_bytes(const LinAttnParams& p) { return int64_t(p.B) * p.H * p.Dk * p.Dv * 4; }
+int64_t linattn_g_bytes(const LinAttnParams& p) { return (p.g_per_token ? linattn_rows(p) : 1) * p.H * 4; }
+int linattn_inputs(const LinAttnParams& p, Arrays& a) {
+    const int64_t e = esize(p.in_bf16), rows = linattn_rows(p);
+    WKV7_TRY(a.add(p.q, rows * p.Hq * p.Dk * e, "q", true, false));
+    WKV7_TRY(a.add(p.k, rows * p.Hk * p.Dk * e, "k", true, false));
+    WKV7_TRY(a.add(p.v, rows * p.Hv * p.Dv * e, "v", true, false));
+    WKV7_TRY(a.add(p.g, linattn_g_bytes(p), "g", rows > 0, false));
     a.index(p.lengths, p.B, "lengths");
     return WKV7_OK;
 }
@@ -434,6 +478,86 @@ int groupnorm_backward(const groupnorm_desc* desc, const void* x, const float* w
     WKV7_TRY(check_threads(groupnorm_threads(p, true)));
     WKV7_TRY(check_device());
     return finish_launch(launch_groupnorm_backward(p, stream_of(stream)), "groupnorm backward");
+}
+
+int64_t linattn_workspace_bytes(const linattn_desc* desc) {
+    g_last_error[0] = '\0';
+    LinAttnParams p;
+    const int rc = linattn_desc_check(desc, false, &p);
+    return rc ? -rc : linattn_forward_workspace(p);
+}
+
+int linattn_forward(const linattn_desc* desc, const void* q, const void* k, const void* v, const float* g,
+                    const float* state_in, void* y, float* state_out, void* workspace, int64_t workspace_bytes, void* stream) {
+    g_last_error[0] = '\0';
+    LinAttnParams p;
+    WKV7_TRY(linattn_desc_check(desc, false, &p));
+    p.q = q; p.k = k; p.v = v; p.g = g; p.s0 = state_in; p.y = y; p.s1 = state_out; p.ws = workspace;
+    Arrays a;
+    WKV7_TRY(linattn_inputs(p, a));
+    WKV7_TRY(a.add(state_in, linattn_state_bytes(p), "state_in", false, false));
+    WKV7_TRY(a.add(y, linattn_rows(p) * p.H * p.Dv * esize(p.y_bf16), "y", true, true));
+    WKV7_TRY(a.add(state_out, linattn_state_bytes(p), "state_out", false, true));
+    WKV7_TRY(a.workspace(workspace, workspace_bytes, linattn_forward_workspace(p)));
+    WKV7_TRY(a.disjoint(true));
+    if (int64_t(p.B) * p.H == 0 || (p.T == 0 && !state_out)) return WKV7_OK;
+    WKV7_TRY(check_threads(linattn_forward_threads(p)));
+    WKV7_TRY(check_device());
+    return finish_launch(launch_linattn_forward(p, stream_of(stream)), "linattn");
+}
+
+int linattn_step(const linattn_desc* desc, const void* q, const void* k, const void* v, const float* g, float* state,
+                 const int32_t* state_index, void* y, void* stream) {
+    g_last_error[0] = '\0';
+    LinAttnParams p;
+    WKV7_TRY(linattn_desc_check(desc, true, &p));
+    WKV7_TRY(check_index(state_index, p.B, p.S));
+    p.q = q; p.k = k; p.v = v; p.g = g; p.s1 = state; p.index = state_index; p.y = y;
+    Arrays a;
+    const bool some = int64_t(p.B) * p.H > 0;
+    WKV7_TRY(linattn_inputs(p, a));
+    a.index(state_index, p.B, "state_index");
+    WKV7_TRY(a.add(state, some ? int64_t(p.S) * p.H * p.Dk * p.Dv * 4 : 0, "state", true, true));
+    WKV7_TRY(a.add(y, linattn_rows(p) * p.H * p.Dv * esize(p.y_bf16), "y", true, true));
+    WKV7_TRY(a.disjoint());
+    if (!some) return WKV7_OK;
+    WKV7_TRY(check_threads(linattn_step_threads(p)));
+    WKV7_TRY(check_device());
+    return finish_launch(launch_linattn_step(p, stream_of(stream)), "linattn step");
+}
+
+int64_t linattn_backward_workspace_bytes(const linattn_desc* desc) {
+    g_last_error[0] = '\0';
+    LinAttnParams p;
+    const int rc = linattn_desc_check(desc, false, &p);
+    return rc ? -rc : linattn_backward_workspace(p);
+}
+
+int linattn_backward(const linattn_desc* desc, const void* q, const void* k, const void* v, const float* g,
+                     const float* state_in, const void* dy, const float* dstate_out, void* dq, void* dk, void* dv, float* dg,
+                     float* dstate_in, void* workspace, int64_t workspace_bytes, void* stream) {
+    g_last_error[0] = '\0';
+    LinAttnParams p;
+    WKV7_TRY(linattn_desc_check(desc, false, &p));
+    p.q = q; p.k = k; p.v = v; p.g = g; p.s0 = state_in; p.dy = dy; p.ds1 = dstate_out;
+    p.dq = dq; p.dk = dk; p.dv = dv; p.dg = dg; p.ds0 = dstate_in; p.ws = workspace;
+    Arrays a;
+    const int64_t e = esize(p.in_bf16), rows = linattn_rows(p);
+    WKV7_TRY(linattn_inputs(p, a));
+    WKV7_TRY(a.add(state_in, linattn_state_bytes(p), "state_in", false, false));
+    WKV7_TRY(a.add(dy, rows * p.H * p.Dv * esize(p.y_bf16), "dy", true, false));
+    WKV7_TRY(a.add(dstate_out, linattn_state_bytes(p), "dstate_out", false, false));
+    WKV7_TRY(a.add(dq, rows * p.Hq * p.Dk * e, "dq", true, true));
+    WKV7_TRY(a.add(dk, rows * p.Hk * p.Dk * e, "dk", true, true));
+    WKV7_TRY(a.add(dv, rows * p.Hv * p.Dv * e, "dv", true, true));
+    WKV7_TRY(a.add(dg, linattn_g_bytes(p), "dg", false, true));
+    WKV7_TRY(a.add(dstate_in, linattn_state_bytes(p), "dstate_in", false, true));
+    WKV7_TRY(a.workspace(workspace, workspace_bytes, linattn_backward_workspace(p)));
+    WKV7_TRY(a.disjoint());
+    if (p.H == 0) return WKV7_OK;
+    WKV7_TRY(check_threads(linattn_backward_threads(p)));
+    WKV7_TRY(check_device());
+    return finish_launch(launch_linattn_backward(p, stream_of(stream)), "linattn backward");
 }
 
 }  // extern "C"
