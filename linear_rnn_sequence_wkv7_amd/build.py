@@ -26,7 +26,7 @@ ARCH = "gfx950"
 
 SOURCES = ["wkv7_api.cpp", "wkv7_scan.hip", "wkv7_decode.hip", "wkv7_chunked.hip", "wkv7_chunked128.hip",
            "wkv7_twopass128.hip", "wkv7_twopass128_scan.hip", "wkv7_backward.hip", "wkv4.hip",
-           "seq_api.cpp", "ssm_scan.hip", "ssm_backward.hip", "shortconv.hip", "groupnorm.hip",
+           "seq_api.cpp", "ssm_scan.hip", "ssm_backward.hip", "shortconv.hip", "groupnorm.hip", "layernorm.hip",
            "linattn/linattn.hip", "linattn/linattn_bf16.hip", "linattn/linattn_f32.hip"]
 
 COMMON = [

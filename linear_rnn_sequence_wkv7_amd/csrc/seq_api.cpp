@@ -1,15 +1,18 @@
 // C-ABI entry points of the selective state space scan, the short causal
-// convolution, the group norm and linear attention: argument validation (before
-// any HIP call) and dispatch to the kernel launchers.  See include/ssm.h,
-// include/shortconv.h, include/groupnorm.h and include/linattn.h for the contracts.
+// convolution, the group norm, linear attention and the layer norm: argument
+// validation (before any HIP call) and dispatch to the kernel launchers.  See
+// include/ssm.h, include/shortconv.h, include/groupnorm.h, include/linattn.h and
+// include/layernorm.h for the contracts.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
 #include <cstdint>
 #include <cstring>
 
+#include "../../include/layernorm.h"
 #include "../../include/linattn.h"
 #include "../../include/wkv7.h"
+#include "layernorm.h"
 #include "linattn/linattn_internal.h"
 #include "seq_internal.h"
 #include "wkv7_host.h"
@@ -40,13 +43,14 @@ struct Arrays {
     void index(const int32_t* p, int64_t count, const char* name) {
         if (p) it[n++] = {{p, count * 4, name}, false};
     }
-    // Every written array shares no byte with another; with `in_place`, state_out may be state_in itself.
-    int disjoint(bool in_place = false) const {
+    // Every written array shares no byte with another; with `in_place`, state_out may be state_in itself
+    // (or another named pair the same).
+    int disjoint(bool in_place = false, const char* moved = "state_out", const char* from = "state_in") const {
         for (int i = 0; i < n; ++i)
             for (int j = 0; j < n; ++j) {
                 if (i == j || !it[i].written || (it[j].written && j < i)) continue;
                 const Span &x = it[i].s, &y = it[j].s;
-                if (in_place && x.p == y.p && !std::strcmp(x.name, "state_out") && !std::strcmp(y.name, "state_in")) continue;
+                if (in_place && x.p == y.p && !std::strcmp(x.name, moved) && !std::strcmp(y.name, from)) continue;
                 if (overlap(x.p, x.bytes, y.p, y.bytes)) return fail(WKV7_EINVAL, "%s overlaps %s", x.name, y.name);
             }
         return WKV7_OK;
@@ -236,6 +240,26 @@ int linattn_inputs(const LinAttnParams& p, Arrays& a) {
     WKV7_TRY(a.add(p.v, rows * p.Hv * p.Dv * e, "v", true, false));
     WKV7_TRY(a.add(p.g, linattn_g_bytes(p), "g", rows > 0, false));
     a.index(p.lengths, p.B, "lengths");
+    return WKV7_OK;
+}
+
+// ---------------------------------------------------------------- layer norm
+
+int layernorm_desc_check(const layernorm_desc* d, LayerNormParams* p) {
+    if (!d) return fail(WKV7_EINVAL, "desc is NULL");
+    if (d->B < 0 || d->T < 0 || d->C < 0) return fail(WKV7_EINVAL, "negative size (B=%d T=%d C=%d)", d->B, d->T, d->C);
+    if (d->x_dtype != WKV7_F32 && d->x_dtype != WKV7_BF16) return fail(WKV7_EINVAL, "x_dtype %d unknown", d->x_dtype);
+    if (d->h_dtype != WKV7_F32 && d->h_dtype != WKV7_BF16) return fail(WKV7_EINVAL, "h_dtype %d unknown", d->h_dtype);
+    if (d->y_dtype != WKV7_F32 && d->y_dtype != WKV7_BF16) return fail(WKV7_EINVAL, "y_dtype %d unknown", d->y_dtype);
+    if (!std::isfinite(d->eps) || d->eps <= 0.f) return fail(WKV7_EINVAL, "eps must be positive and finite");
+    if (d->reserved != 0) return fail(WKV7_EINVAL, "reserved must be 0 (got %d)", d->reserved);
+    WKV7_TRY(check_lengths(d->lengths, true));
+    if (int64_t(d->B) * d->T > kMaxElems / 64 / (d->C ? d->C : 1) || d->C >= (1 << 24))
+        return fail(WKV7_EUNSUPPORTED, "B=%d, T=%d or C=%d too large", d->B, d->T, d->C);
+    *p = LayerNormParams{};
+    p->B = d->B; p->T = d->T; p->C = d->C;
+    p->x_bf16 = d->x_dtype == WKV7_BF16; p->h_bf16 = d->h_dtype == WKV7_BF16; p->y_bf16 = d->y_dtype == WKV7_BF16;
+    p->eps = d->eps; p->lengths = d->lengths;
     return WKV7_OK;
 }
 
@@ -558,6 +582,73 @@ int linattn_backward(const linattn_desc* desc, const void* q, const void* k, con
     WKV7_TRY(check_threads(linattn_backward_threads(p)));
     WKV7_TRY(check_device());
     return finish_launch(launch_linattn_backward(p, stream_of(stream)), "linattn backward");
+}
+
+int layernorm_forward(const layernorm_desc* desc, const void* x, const void* residual, const float* weight, const float* bias,
+                      void* h, void* y, float* mean, float* rstd, void* stream) {
+    g_last_error[0] = '\0';
+    LayerNormParams p;
+    WKV7_TRY(layernorm_desc_check(desc, &p));
+    p.x = x; p.res = residual; p.weight = weight; p.bias = bias; p.h = h; p.y = y; p.mean = mean; p.rstd = rstd;
+    Arrays a;
+    const int64_t rows = int64_t(p.B) * p.T, n = rows * p.C;
+    if (n > 0 && !residual != !h) return fail(WKV7_EINVAL, "residual and h go together: one of them is NULL");
+    if (!residual && p.x_bf16 != p.h_bf16) return fail(WKV7_EINVAL, "h_dtype differs from x_dtype without a residual");
+    if (!mean != !rstd) return fail(WKV7_EINVAL, "mean and rstd go together: one of them is NULL");
+    WKV7_TRY(a.add(x, n * esize(p.x_bf16), "x", true, false));
+    WKV7_TRY(a.add(residual, n * esize(p.h_bf16), "residual", false, false));
+    WKV7_TRY(a.add(weight, int64_t(p.C) * 4, "weight", false, false));
+    WKV7_TRY(a.add(bias, int64_t(p.C) * 4, "bias", false, false));
+    a.index(p.lengths, p.B, "lengths");
+    WKV7_TRY(a.add(h, n * esize(p.h_bf16), "h", false, true));
+    WKV7_TRY(a.add(y, n * esize(p.y_bf16), "y", true, true));
+    WKV7_TRY(a.add(mean, rows * 4, "mean", false, true));
+    WKV7_TRY(a.add(rstd, rows * 4, "rstd", false, true));
+    WKV7_TRY(a.disjoint(true, "h", "residual"));
+    if (rows == 0 || (p.C == 0 && !mean)) return WKV7_OK;
+    WKV7_TRY(check_threads(layernorm_threads(p, false)));
+    WKV7_TRY(check_device());
+    return finish_launch(launch_layernorm_forward(p, stream_of(stream)), "layernorm");
+}
+
+int64_t layernorm_backward_workspace_bytes(const layernorm_desc* desc) {
+    g_last_error[0] = '\0';
+    LayerNormParams p;
+    const int rc = layernorm_desc_check(desc, &p);
+    return rc ? -rc : layernorm_backward_workspace(p);
+}
+
+int layernorm_backward(const layernorm_desc* desc, const void* h, const float* weight, const float* bias, const void* dy,
+                       const void* dh, const float* mean, const float* rstd, void* dresidual, void* dx, float* dweight,
+                       float* dbias, void* workspace, int64_t workspace_bytes, void* stream) {
+    g_last_error[0] = '\0';
+    LayerNormParams p;
+    WKV7_TRY(layernorm_desc_check(desc, &p));
+    p.h = const_cast<void*>(h); p.weight = weight; p.bias = bias; p.dy = dy; p.dh = dh;
+    p.mean = const_cast<float*>(mean); p.rstd = const_cast<float*>(rstd);
+    p.dres = dresidual; p.dx = dx; p.dweight = dweight; p.dbias = dbias; p.ws = workspace;
+    Arrays a;
+    const int64_t rows = int64_t(p.B) * p.T, n = rows * p.C;
+    if (p.C > 0 && weight && !dweight) return fail(WKV7_EINVAL, "dweight is NULL but weight is given");
+    if (p.C > 0 && bias && !dbias) return fail(WKV7_EINVAL, "dbias is NULL but bias is given");
+    WKV7_TRY(a.add(h, n * esize(p.h_bf16), "h", true, false));
+    WKV7_TRY(a.add(weight, int64_t(p.C) * 4, "weight", false, false));
+    WKV7_TRY(a.add(bias, int64_t(p.C) * 4, "bias", false, false));
+    a.index(p.lengths, p.B, "lengths");
+    WKV7_TRY(a.add(dy, n * esize(p.y_bf16), "dy", true, false));
+    WKV7_TRY(a.add(dh, n * esize(p.h_bf16), "dh", false, false));
+    WKV7_TRY(a.add(mean, n > 0 ? rows * 4 : 0, "mean", true, false));
+    WKV7_TRY(a.add(rstd, n > 0 ? rows * 4 : 0, "rstd", true, false));
+    WKV7_TRY(a.add(dresidual, n * esize(p.h_bf16), "dresidual", true, true));
+    WKV7_TRY(a.add(dx, n * esize(p.x_bf16), "dx", false, true));
+    WKV7_TRY(a.add(dweight, int64_t(p.C) * 4, "dweight", false, true));
+    WKV7_TRY(a.add(dbias, int64_t(p.C) * 4, "dbias", false, true));
+    WKV7_TRY(a.workspace(workspace, workspace_bytes, layernorm_backward_workspace(p)));
+    WKV7_TRY(a.disjoint(true, "dresidual", "dh"));
+    if (p.C == 0) return WKV7_OK;
+    WKV7_TRY(check_threads(layernorm_threads(p, true)));
+    WKV7_TRY(check_device());
+    return finish_launch(launch_layernorm_backward(p, stream_of(stream)), "layernorm backward");
 }
 
 }  // extern "C"
