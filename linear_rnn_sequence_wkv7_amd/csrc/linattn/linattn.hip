@@ -226,7 +226,7 @@ struct Carve {   // pieces of a workspace
     char* base;
     int64_t at = 0;
     float* floats(int64_t n) {
-        float* r = reinterpret_cast<float*>(base + at);
+        float* r = base ? reinterpret_cast<float*>(base + at) : nullptr;   // (a size query has no base)
         at += (n * 4 + 255) / 256 * 256;
         return r;
     }
