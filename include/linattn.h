@@ -40,7 +40,7 @@ extern "C" {
 typedef struct linattn_desc {
     int32_t B;           /* batch, >= 0 */
     int32_t T;           /* tokens, >= 0 (linattn_step: 1) */
-    int32_t H;           /* heads, >= 0 */
+    int32_t H;           /* heads, 0 .. 16384 (more: EUNSUPPORTED) */
     int32_t Hq, Hk, Hv;  /* heads of q, k and v, divisors of H (0 means H) */
     int32_t Dk, Dv;      /* 1 .. 128 (larger: EUNSUPPORTED) */
     int32_t in_dtype;    /* wkv7_dtype of q, k, v */

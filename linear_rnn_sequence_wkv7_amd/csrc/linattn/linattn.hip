@@ -51,62 +51,66 @@ __global__ __launch_bounds__(kThreads) void chain_kernel(Chain f, Chain r, int s
 
 // The gradient of g_t is the sum over u >= t of <q_u, dq_u> - <k_u, dk_u>, and <state, its
 // gradient> behind the last token: what a change of every running sum from t on does.  A
-// workgroup per sequence and head, from the end, 4096 tokens at a time, summed in 64 bits.
-constexpr int kDgThreads = 1024, kDgPer = 4;
-__global__ __launch_bounds__(kDgThreads) void dg_kernel(const float* qd, const float* kd, const float* end, Chunks w, float* dg, float* part) {
+// workgroup takes 2048 tokens of a sequence and head; it adds up the later ones itself (from the
+// caches), so that none waits for another.  In 64 bits.
+constexpr int kDgThreads = 1024, kDgPer = 2, kDgRun = kDgThreads * kDgPer;
+int dg_runs(int T) { return (T + kDgRun - 1) / kDgRun; }
+__device__ __forceinline__ double block_sum(double v, double* sums) {
+    const int lane = threadIdx.x & 63;
+    const double in = running_sum(v, lane);
+    __syncthreads();
+    if (lane == 63) sums[threadIdx.x >> 6] = in;
+    __syncthreads();
+    v = 0.0;
+    for (int i = 0; i < kDgThreads / 64; ++i) v += sums[i];
+    return v;
+}
+__global__ __launch_bounds__(kDgThreads) void dg_kernel(const float* qd, const float* kd, const float* end, Chunks w, int runs, float* dg, float* part) {
     __shared__ double sums[kDgThreads / 64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int h = int(blockIdx.x % w.H);
-    const int64_t b = blockIdx.x / w.H, bh = blockIdx.x;
+    const int run = int(blockIdx.x % runs);   // counted from the end, as the tokens are below
+    const int64_t bh = blockIdx.x / runs, b = bh / w.H;
+    const int h = int(bh % w.H), last = w.T - 1;
     const int len = seq_length(w.lengths, b, w.T);
-    double run = end ? end[bh] : 0.f, total = 0.0;
-    for (int r0 = 0; r0 < w.T; r0 += kDgThreads * kDgPer) {
-        const int r = r0 + tid * kDgPer;   // tokens counted from the end
-        double v[kDgPer], sum = 0.0;
-        #pragma unroll
-        for (int i = 0; i < kDgPer; ++i) {
-            const int t = w.T - 1 - r - i;
-            if (t >= 0) sum += double(qd[bh * w.T + t]) - double(kd[bh * w.T + t]);
-            v[i] = sum;
-        }
-        const double in = running_sum(sum, lane);
-        __syncthreads();
-        if (lane == 63) sums[wave] = in;
-        __syncthreads();
-        double before = run + (in - sum), all = 0.0;
-        for (int i = 0; i < kDgThreads / 64; ++i) {
-            if (i < wave) before += sums[i];
-            all += sums[i];
-        }
-        run += all;
-        #pragma unroll
-        for (int i = 0; i < kDgPer; ++i) {
-            const int t = w.T - 1 - r - i;
-            if (t < 0) continue;
-            const float g = w.g_per_token ? w.g[(b * w.T + t) * w.H + h] : w.g[h];
-            const double d = t >= len || double(g) * 1.4426950408889634074 < kNoDecayLog2 ? 0.0 : before + v[i];
-            if (w.g_per_token) dg[(b * w.T + t) * w.H + h] = float(d);
-            else total += d;
-        }
+    const float *q = qd + bh * w.T, *k = kd + bh * w.T;
+    double later = 0.0;
+    for (int r = tid; r < run * kDgRun; r += kDgThreads) later += double(q[last - r]) - double(k[last - r]);
+    later = block_sum(later, sums) + (end ? end[bh] : 0.f);
+    const int r0 = run * kDgRun + tid * kDgPer;
+    double v[kDgPer], sum = 0.0, total = 0.0;
+    #pragma unroll
+    for (int i = 0; i < kDgPer; ++i) {
+        const int t = last - r0 - i;
+        if (t >= 0) sum += double(q[t]) - double(k[t]);
+        v[i] = sum;
+    }
+    const double in = running_sum(sum, lane);
+    __syncthreads();
+    if (lane == 63) sums[wave] = in;
+    __syncthreads();
+    double before = later + (in - sum);
+    for (int i = 0; i < wave; ++i) before += sums[i];
+    #pragma unroll
+    for (int i = 0; i < kDgPer; ++i) {
+        const int t = last - r0 - i;
+        if (t < 0) continue;
+        const float g = w.g_per_token ? w.g[(b * w.T + t) * w.H + h] : w.g[h];
+        const double d = t >= len || double(g) * 1.4426950408889634074 < kNoDecayLog2 ? 0.0 : before + v[i];
+        if (w.g_per_token) dg[(b * w.T + t) * w.H + h] = float(d);
+        else total += d;
     }
     if (!w.g_per_token) {
-        const double in = running_sum(total, lane);
-        __syncthreads();
-        if (lane == 63) sums[wave] = in;
-        __syncthreads();
-        if (tid == 0) {
-            total = 0.0;
-            for (int i = 0; i < kDgThreads / 64; ++i) total += sums[i];
-            part[bh] = float(total);
-        }
+        total = block_sum(total, sums);
+        if (tid == 0) part[bh * runs + run] = float(total);
     }
 }
-__global__ __launch_bounds__(64) void dg_heads_kernel(const float* part, float* dg, int B, int H) {
-    const int h = blockIdx.x * 64 + threadIdx.x;
-    if (h >= H) return;
+// part [B, H, runs] -> dg [H]; a wave per head.
+__global__ __launch_bounds__(64) void dg_heads_kernel(const float* part, float* dg, int B, int H, int runs) {
+    const int h = blockIdx.x, lane = threadIdx.x;
     double s = 0.0;
-    for (int64_t b = 0; b < B; ++b) s += part[b * H + h];
-    dg[h] = float(s);
+    for (int64_t i = lane; i < int64_t(B) * runs; i += 64) s += part[(i / runs * H + h) * runs + i % runs];
+    s = running_sum(s, lane);
+    if (lane == 63) dg[h] = float(s);
 }
 
 // ---------------------------------------------------------------- sums over shared heads
@@ -212,14 +216,39 @@ hipError_t step_rows(const LinAttnParams& p, dim3 grid, hipStream_t st) {
 
 // ---------------------------------------------------------------- how a call is split up
 
-// Sequences in `kinds` sweeps a head are cut into segments where there are fewer heads than the
-// chip takes side by side.
+// Sequences are cut into segments, computed side by side, where their heads alone do not occupy the
+// chip.  The number is the one with the least time by what was measured (in 0.1 us): a workgroup by
+// itself takes `lat` for a chunk, several on a compute unit `thr` each (at heads of 64 that is 4.2 TB/s,
+// at 128 the vector units are busy too), and about two chunks' time goes before the first; more than one
+// segment costs a pass over two of the operands and the chain of the states.
+//   4 x 4096, 40 heads of 64: 1 segment 211 us, 2 181, 3 136, 4 142, 8 135; 1 x 2048, 32 heads of 128: 1 154,
+//   4 73, 8 56, 16 61; 8 x 1024, 32 heads of 64: 1 55, 2 70.
 void plan(const LinAttnParams& p, int kinds, Chunks* w) {
-    const int64_t heads = int64_t(p.B) * p.H * kinds, chunks = (int64_t(p.T) + 63) / 64;
-    int64_t segs = 512 / (heads > 0 ? heads : 1);
-    segs = segs < 1 ? 1 : segs > chunks ? chunks : segs;
-    const int64_t each = segs > 0 ? (chunks + segs - 1) / segs : 1;
-    *w = Chunks{p.B, p.T, p.H, int(each > 0 && chunks > 0 ? (chunks + each - 1) / each : 1), int(each * 64), p.g_per_token, p.g, p.lengths};
+    const int64_t heads = int64_t(p.B) * p.H, chunks = (int64_t(p.T) + 63) / 64;
+    const bool wide = p.Dk > 64 || p.Dv > 64, both = p.Dk > 64 && p.Dv > 64;
+    const int groups = both ? 2 : 3, lat = both ? 50 : wide ? 40 : 31, thr = both ? 45 : wide ? 32 : 20;
+    auto rounds = [&](int64_t jobs, int64_t segs, int64_t each, int groups, int lat, int thr) {   // the fullest compute unit's
+        int64_t time = 0;
+        for (int64_t k = (jobs * segs + 255) / 256; k > 0; k -= groups) {
+            const int64_t c = k < groups ? k : groups;
+            time += (each + 2) * (c * thr > lat ? c * thr : lat);
+            if (k > 64 * groups) return time * (k / groups);   // many rounds alike
+        }
+        return time;
+    };
+    int64_t best = 1, least = -1;
+    for (int64_t segs = 1; segs <= chunks && segs <= 64 && (segs == 1 || heads * kinds < 768); ++segs) {
+        const int64_t each = (chunks + segs - 1) / segs;
+        if (segs > 1 && (chunks + each - 1) / each != segs) continue;   // the same as fewer
+        int64_t time = rounds(heads * kinds, segs, each, groups, lat, thr);
+        if (segs > 1) time += (kinds > 1 ? 2 : 1) * (rounds(heads, segs, each, 2, both ? 28 : 15, both ? 22 : 9) + 60 + heads * segs * p.Dk * p.Dv / 50000);
+        if (least < 0 || time < least) {
+            least = time;
+            best = segs;
+        }
+    }
+    const int64_t each = chunks > 0 ? (chunks + best - 1) / best : 1;
+    *w = Chunks{p.B, p.T, p.H, int(best), int(each * 64), p.g_per_token, p.g, p.lengths};
 }
 
 struct Carve {   // pieces of a workspace
@@ -251,7 +280,7 @@ struct BackwardWs {
         qd = c.floats(bh * p.T);
         kd = c.floats(bh * p.T);
         end = c.floats(bh);
-        part = c.floats(bh);
+        part = c.floats(bh * dg_runs(p.T));
         for (int i = 0; i < 2; ++i) {
             states[i] = c.floats(n * p.Dk * p.Dv);
             kept[i] = c.floats(n);
@@ -322,7 +351,7 @@ int64_t linattn_backward_threads(const LinAttnParams& p) {
     Chunks w;
     plan(p, 3, &w);
     const int64_t sweeps = int64_t(p.B) * p.H * w.segs * 3 * 512, rows = int64_t(p.B) * p.T;
-    const int64_t dg = int64_t(p.B) * p.H * kDgThreads, sums = rows * p.H * (p.Dk > p.Dv ? p.Dk : p.Dv);
+    const int64_t dg = int64_t(p.B) * p.H * dg_runs(p.T) * kDgThreads, sums = rows * p.H * (p.Dk > p.Dv ? p.Dk : p.Dv);
     return sweeps > dg ? (sweeps > sums ? sweeps : sums) : (dg > sums ? dg : sums);
 }
 
@@ -339,7 +368,7 @@ hipError_t launch_linattn_forward(const LinAttnParams& p, hipStream_t st) {
     s.ws = ws.states; s.kept = ws.kept;
     s.s_in = p.s0; s.s_out = p.s1;
     if (w.segs > 1) {
-        TRY(p.in_bf16 ? parts_bf16(w, s, s, 1, st) : parts_f32(w, s, s, 1, st));
+        TRY(p.in_bf16 ? parts_bf16(w, s, st) : parts_f32(w, s, st));
         TRY(chain(w, {ws.states, ws.kept, p.s0, p.s1}, {}, 1, p.Dk * p.Dv, st));
     }
     return p.in_bf16 ? forward_bf16(w, s, st) : forward_f32(w, s, st);
@@ -361,7 +390,7 @@ hipError_t launch_linattn_backward(const LinAttnParams& p, hipStream_t st) {
     const Operand q{p.q, p.Hq, p.Dk, p.in_bf16}, k{p.k, p.Hk, p.Dk, p.in_bf16}, v{p.v, p.Hv, p.Dv, p.in_bf16}, dy{p.dy, p.H, p.Dv, p.y_bf16};
     // a gradient goes to its place, or, where heads share one, each head's to the workspace
     if (p.B == 0) {
-        if (p.dg && !p.g_per_token) dg_heads_kernel<<<(p.H + 63) / 64, 64, 0, st>>>(ws.part, p.dg, 0, p.H);
+        if (p.dg && !p.g_per_token) dg_heads_kernel<<<p.H, 64, 0, st>>>(ws.part, p.dg, 0, p.H, 1);
         return hipGetLastError();
     }
     auto make = [&](const Operand& a, const Operand& b, const Operand& c, void* out, float* each, int heads, bool back, bool transposed) {
@@ -384,9 +413,10 @@ hipError_t launch_linattn_backward(const LinAttnParams& p, hipStream_t st) {
         sq.end_grad = p.ds1; sq.end_dot = p.ds1 ? ws.end : nullptr;
     }
     if (w.segs > 1) {
-        Sweep f = sv, r = sv;
+        Sweep f = sv;
         f.b = k; f.c = v; f.back = false; f.su = 1.f; f.ws = ws.states[0]; f.kept = ws.kept[0];
-        TRY(bf16 ? parts_bf16(w, f, r, 2, st) : parts_f32(w, f, r, 2, st));
+        TRY(bf16 ? parts_bf16(w, f, st) : parts_f32(w, f, st));
+        TRY(bf16 ? parts_bf16(w, sv, st) : parts_f32(w, sv, st));
         TRY(chain(w, {ws.states[0], ws.kept[0], p.s0, nullptr}, {ws.states[1], ws.kept[1], p.ds1, p.ds0}, 2, p.Dk * p.Dv, st));
     } else {
         sv.s_out = p.ds0;
@@ -396,8 +426,9 @@ hipError_t launch_linattn_backward(const LinAttnParams& p, hipStream_t st) {
     if (p.Hk < p.H && rows > 0) TRY(shared_sum(ws.dk, p.dk, rows, p.Hk, p.H / p.Hk, p.Dk, p.in_bf16, st));
     if (p.Hv < p.H && rows > 0) TRY(shared_sum(ws.dv, p.dv, rows, p.Hv, p.H / p.Hv, p.Dv, p.in_bf16, st));
     if (p.dg) {
-        if (rows > 0) dg_kernel<<<uint32_t(int64_t(p.B) * p.H), kDgThreads, 0, st>>>(ws.qd, ws.kd, sq.end_dot, w, p.dg, ws.part);
-        if (!p.g_per_token) dg_heads_kernel<<<(p.H + 63) / 64, 64, 0, st>>>(ws.part, p.dg, rows > 0 ? p.B : 0, p.H);
+        const int runs = dg_runs(p.T);
+        if (rows > 0) dg_kernel<<<uint32_t(int64_t(p.B) * p.H * runs), kDgThreads, 0, st>>>(ws.qd, ws.kd, sq.end_dot, w, runs, p.dg, ws.part);
+        if (!p.g_per_token) dg_heads_kernel<<<p.H, 64, 0, st>>>(ws.part, p.dg, rows > 0 ? p.B : 0, p.H, rows > 0 ? runs : 1);
     }
     return hipGetLastError();
 }

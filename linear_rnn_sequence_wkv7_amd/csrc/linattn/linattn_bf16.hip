@@ -28,19 +28,30 @@ struct Bf16Ops {
     static __device__ __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
 
     // Byte offset of a row's 16-byte piece in an LDS tile of D columns.  The pieces of a row trade
-    // places so that neither 16 rows' same piece (row()) nor 4 rows' 4 neighbouring ones (col())
-    // meet in a bank.
+    // places so that reads of one piece of 16 rows (row(); they go by lanes 0-3, 12-15, 20-27 and so on)
+    // and of two pieces of rows r .. r + 3 and r + 8 .. r + 11 (col()) use every bank once.
     template <int D>
     static __device__ __forceinline__ int at(int row, int piece) {
-        if constexpr (D == 128) return row * 256 + (piece ^ ((row & 3) << 2 | (row >> 2 & 3))) * 16;
-        else return row * 128 + (piece ^ ((row >> 1 & 1) << 2 | (row >> 2 & 3))) * 16;
+        if constexpr (D == 128) {
+            const int q = row >> 2;
+            return row * 256 + (piece ^ ((row & 3) << 2 | (((q & 1) << 1 | (q >> 1 & 1)) ^ (q & 2)))) * 16;
+        } else {
+            const int u = row >> 1;
+            return row * 128 + (piece ^ ((u << 1 & 7) ^ (u >> 2 & 1) * 5)) * 16;
+        }
     }
-    static __device__ __forceinline__ constexpr int row_of(int tile, int c) { return pair_col(tile, c); }
-
     // Elements 32 m + 8 g .. of a row.
     template <int D>
     static __device__ __forceinline__ Frag row(const char* tile, int r, int m, int g) {
         return *reinterpret_cast<const Frag*>(tile + at<D>(r, 4 * m + g));
+    }
+    // Elements 32 m + 4 g .. and 32 m + 16 + 4 g ..: in the order of two tiles of a state.
+    template <int D>
+    static __device__ __forceinline__ Frag row_of_state(const char* tile, int r, int m, int g) {
+        const int half = g % 2 * 8;
+        const s16x4 lo = *reinterpret_cast<const s16x4*>(tile + at<D>(r, 4 * m + g / 2) + half);
+        const s16x4 hi = *reinterpret_cast<const s16x4*>(tile + at<D>(r, 4 * m + 2 + g / 2) + half);
+        return __builtin_bit_cast(Frag, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     }
     // Rows 32 m + 8 g .. of the lane's column.  A transposing read takes 4 neighbouring columns
     // (from `from`) of 4 rows from 4 lanes each and gives every lane of the 16 its own column.
@@ -89,6 +100,16 @@ struct Bf16Ops {
         for (int p = 0; p < N; ++p) *reinterpret_cast<uint2*>(P + p * L * L * 2 + at<L>(t, i0 / 8) + i0 % 8 * 2) = uint2{lo[p], hi[p]};
     }
 
+    // Four neighbouring columns of a row.
+    template <bool WHOLE>
+    struct Four {
+        Raw<bf16_t, 4, WHOLE> r;
+        __device__ __forceinline__ void load(rsrc_t d, uint32_t off, int n, bool) { r.load(d, off, n); }
+        __device__ __forceinline__ void get(float* v, bool) const {
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = r.get(i);
+        }
+    };
     template <bool WHOLE>
     struct Piece {
         Raw<bf16_t, 8, WHOLE> r;
@@ -108,8 +129,8 @@ struct Bf16Ops {
 
 }  // namespace
 
-hipError_t parts_bf16(const Chunks& w, const Sweep& f, const Sweep& r, int kinds, hipStream_t st) { return launch_parts<Bf16Ops>(w, f, r, kinds, st); }
-hipError_t forward_bf16(const Chunks& w, const Sweep& s, hipStream_t st) { return launch_outs<Bf16Ops, Bf16Ops::NPY>(w, s, s, s, 1, st); }
+hipError_t parts_bf16(const Chunks& w, const Sweep& s, hipStream_t st) { return launch_parts<Bf16Ops>(w, s, st); }
+hipError_t forward_bf16(const Chunks& w, const Sweep& s, hipStream_t st) { return launch_outs<Bf16Ops, Bf16Ops::NPY, false, false>(w, s, s, 1, st); }
 hipError_t backward_bf16(const Chunks& w, const Sweep& q, const Sweep& k, const Sweep& v, hipStream_t st) { return launch_backward<Bf16Ops>(w, q, k, v, st); }
 
 }  // namespace linattn

@@ -23,12 +23,12 @@ struct F32Ops {
         if constexpr (D >= 64) return row * D * 4 + (piece ^ (row & 15)) * 16;
         else return row * 128 + (piece ^ (row >> 1 & 7)) * 16;
     }
-    static __device__ __forceinline__ constexpr int row_of(int tile, int c) { return flat_col(tile, c); }
-
     template <int D>
     static __device__ __forceinline__ Frag row(const char* tile, int r, int m, int g) {
         return *reinterpret_cast<const Frag*>(tile + at<D>(r, 4 * m + g));
     }
+    template <int D>
+    static __device__ __forceinline__ Frag row_of_state(const char* tile, int r, int m, int g) { return row<D>(tile, r, m, g); }
     // Rows 16 m + 4 g .. of column c.
     template <int D>
     static __device__ __forceinline__ Frag col(const char* tile, int m, int, int c, int lane) {
@@ -66,13 +66,21 @@ struct F32Ops {
             if (bf16) v = WHOLE ? u32x4{w0 << 16, w0 & 0xffff0000u, w1 << 16, w1 & 0xffff0000u} : v << 16;
             *reinterpret_cast<u32x4*>(p) = v;
         }
+        __device__ __forceinline__ void get(float* v, bool bf16) const {
+            v[0] = __uint_as_float(bf16 ? w0 << 16 : w0);
+            v[1] = __uint_as_float(bf16 ? (WHOLE ? w0 & 0xffff0000u : w1 << 16) : w1);
+            v[2] = __uint_as_float(bf16 ? (WHOLE ? w1 : w2) << 16 : w2);
+            v[3] = __uint_as_float(bf16 ? (WHOLE ? w1 & 0xffff0000u : w3 << 16) : w3);
+        }
     };
+    template <bool WHOLE>
+    using Four = Piece<WHOLE>;   // four neighbouring columns of a row
 };
 
 }  // namespace
 
-hipError_t parts_f32(const Chunks& w, const Sweep& f, const Sweep& r, int kinds, hipStream_t st) { return launch_parts<F32Ops>(w, f, r, kinds, st); }
-hipError_t forward_f32(const Chunks& w, const Sweep& s, hipStream_t st) { return launch_outs<F32Ops, F32Ops::NPY>(w, s, s, s, 1, st); }
+hipError_t parts_f32(const Chunks& w, const Sweep& s, hipStream_t st) { return launch_parts<F32Ops>(w, s, st); }
+hipError_t forward_f32(const Chunks& w, const Sweep& s, hipStream_t st) { return launch_outs<F32Ops, F32Ops::NPY, false, false>(w, s, s, 1, st); }
 hipError_t backward_f32(const Chunks& w, const Sweep& q, const Sweep& k, const Sweep& v, hipStream_t st) { return launch_backward<F32Ops>(w, q, k, v, st); }
 
 }  // namespace linattn

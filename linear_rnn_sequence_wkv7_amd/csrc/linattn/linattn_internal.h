@@ -66,8 +66,8 @@ struct Sweep {
     bool out_bf16, back, transposed;   // transposed: the state is stored [c.D][a.D]
 };
 
-hipError_t parts_bf16(const Chunks& w, const Sweep& f, const Sweep& r, int kinds, hipStream_t st);
-hipError_t parts_f32(const Chunks& w, const Sweep& f, const Sweep& r, int kinds, hipStream_t st);
+hipError_t parts_bf16(const Chunks& w, const Sweep& s, hipStream_t st);
+hipError_t parts_f32(const Chunks& w, const Sweep& s, hipStream_t st);
 hipError_t forward_bf16(const Chunks& w, const Sweep& s, hipStream_t st);
 hipError_t forward_f32(const Chunks& w, const Sweep& s, hipStream_t st);
 hipError_t backward_bf16(const Chunks& w, const Sweep& q, const Sweep& k, const Sweep& v, hipStream_t st);

@@ -219,7 +219,7 @@ int linattn_desc_check(const linattn_desc* d, bool step, LinAttnParams* p) {
     WKV7_TRY(check_lengths(d->lengths, !step));
     if (step && d->T != 1) return fail(WKV7_EINVAL, "linattn_step needs T == 1 (got %d)", d->T);
     // Offsets within 64 rows are 32-bit.
-    if (d->H >= (1 << 16)) return fail(WKV7_EUNSUPPORTED, "H=%d; less than 65536 heads are supported", d->H);
+    if (d->H > (1 << 14)) return fail(WKV7_EUNSUPPORTED, "H=%d; up to 16384 heads are supported", d->H);
     const int64_t bt = int64_t(d->B) * d->T, state = int64_t(d->H) * d->Dk * d->Dv;
     if (bt > kMaxElems / 128 / (d->H ? d->H : 1) || int64_t(d->B) * d->H > kMaxItems || (state && d->B > kMaxElems / state) ||
         (step && state && d->S > kMaxElems / state) || d->T > INT32_MAX - 4096)

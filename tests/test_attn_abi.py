@@ -37,7 +37,7 @@ TOGETHER = {"layernorm_forward": [("residual", "h"), ("h", "residual"), ("mean",
 def desc(fn, **kw):
     if fn.startswith("linattn"):
         step = fn.endswith("step")
-        d = dict(B=2, T=1 if step else 200, H=4, Hq=2, Hk=1, Hv=4, Dk=24, Dv=40, in_dtype=1, y_dtype=1, g_per_token=1, S=5, scale=1.0)
+        d = dict(B=2, T=1 if step else 4000, H=4, Hq=2, Hk=1, Hv=4, Dk=24, Dv=40, in_dtype=1, y_dtype=1, g_per_token=1, S=5, scale=1.0)
         return L.LinattnDesc(**{**d, **kw})
     return N.LayernormDesc(**{**dict(B=2, T=70, C=64, x_dtype=1, h_dtype=1, y_dtype=1, eps=1e-5), **kw})
 
