@@ -27,40 +27,64 @@ struct Bf16Ops {
 
     static __device__ __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
 
-    // Byte offset of a row's 16-byte piece in an LDS tile of D columns.  The pieces of a row trade
-    // places so that reads of one piece of 16 rows (row(); they go by lanes 0-3, 12-15, 20-27 and so on)
-    // and of two pieces of rows r .. r + 3 and r + 8 .. r + 11 (col()) use every bank once.
+    // The pieces of 16 bytes of a row in an LDS tile of D columns trade places, each with the one whose
+    // number differs by swap(), so that reads of one piece of 16 rows (row(); they go by lanes 0-3, 12-15,
+    // 20-27 and so on) and of two pieces of rows r .. r + 3 and r + 8 .. r + 11 (col()) use every bank once.
+    // (Columns of a state, four pieces' halves of those rows, meet in pairs: 4 of 12 clocks.)
     template <int D>
-    static __device__ __forceinline__ int at(int row, int piece) {
+    static __device__ __forceinline__ uint32_t swap(uint32_t row) {
         if constexpr (D == 128) {
-            const int q = row >> 2;
-            return row * 256 + (piece ^ ((row & 3) << 2 | (((q & 1) << 1 | (q >> 1 & 1)) ^ (q & 2)))) * 16;
+            const uint32_t q = row >> 2;
+            return (row & 3) << 2 | (((q & 1) << 1 | (q >> 1 & 1)) ^ (q & 2));
         } else {
-            const int u = row >> 1;
-            return row * 128 + (piece ^ ((u << 1 & 7) ^ (u >> 2 & 1) * 5)) * 16;
+            const uint32_t u = row >> 1;
+            return (u << 1 & 7) ^ (u >> 2 & 1) * 5;
         }
     }
-    // Elements 32 m + 8 g .. of a row.
     template <int D>
-    static __device__ __forceinline__ Frag row(const char* tile, int r, int m, int g) {
-        return *reinterpret_cast<const Frag*>(tile + at<D>(r, 4 * m + g));
+    static __device__ __forceinline__ uint32_t at(uint32_t row, uint32_t piece) { return row * (2 * D) + (piece ^ swap<D>(row)) * 16; }
+
+    // The first of the four rows of a state that tile a's rows 4 c .. 4 c + 3 are.  In two tiles a group of
+    // lanes has 8 neighbours, which is how row() reads what they are multiplied with.
+    static __device__ __forceinline__ constexpr int row_of(int a, int c) { return 32 * (a / 2) + 8 * c + 4 * (a % 2); }
+
+    // Where a lane reads a tile.  swap() goes by the row's last four bits and the pieces' numbers are
+    // xors, so that another piece is an xor and other rows by 16 an offset away.
+    template <int D>
+    struct Lanes {
+        uint32_t row, half, col[2], state[2];
+        __device__ __forceinline__ Lanes(uint32_t ln) {
+            const uint32_t l = ln & 15, g = ln >> 4, r = 8 * g + (l >> 2);
+            row = at<D>(l, g);
+            half = at<D>(l, g >> 1) + (g & 1) * 8;
+            col[0] = at<D>(r, (l & 3) >> 1) + (l & 1) * 8;
+            col[1] = at<D>(r + 4, (l & 3) >> 1) + (l & 1) * 8;
+            state[0] = at<D>(r, l & 3);
+            state[1] = at<D>(r + 4, l & 3);
+        }
+    };
+    // Elements 32 m + 8 g .. of row 16 t + the lane's.
+    template <int D>
+    static __device__ __forceinline__ Frag row(const char* tile, const Lanes<D>& at, int t, int m) {
+        return *reinterpret_cast<const Frag*>(tile + (at.row ^ m * 64) + t * 32 * D);
     }
-    // Elements 32 m + 4 g .. and 32 m + 16 + 4 g ..: in the order of two tiles of a state.
-    template <int D>
-    static __device__ __forceinline__ Frag row_of_state(const char* tile, int r, int m, int g) {
-        const int half = g % 2 * 8;
-        const s16x4 lo = *reinterpret_cast<const s16x4*>(tile + at<D>(r, 4 * m + g / 2) + half);
-        const s16x4 hi = *reinterpret_cast<const s16x4*>(tile + at<D>(r, 4 * m + 2 + g / 2) + half);
+    // Rows 32 m + 8 g .. of a column.  A transposing read takes 4 neighbouring columns of 4 rows from 4 lanes
+    // each and gives every lane of the 16 its own column.
+    static __device__ __forceinline__ Frag transposed(const char* lo4, const char* hi4) {
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(lo4));
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(hi4));
         return __builtin_bit_cast(Frag, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     }
-    // Rows 32 m + 8 g .. of the lane's column.  A transposing read takes 4 neighbouring columns
-    // (from `from`) of 4 rows from 4 lanes each and gives every lane of the 16 its own column.
+    // Column 16 t + the lane's.
     template <int D>
-    static __device__ __forceinline__ Frag col(const char* tile, int m, int from, int, int lane) {
-        const int r = 32 * m + 8 * (lane >> 4) + (lane >> 2 & 3), part = from % 8 * 2;
-        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(tile + at<D>(r, from / 8) + part));
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(tile + at<D>(r + 4, from / 8) + part));
-        return __builtin_bit_cast(Frag, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    static __device__ __forceinline__ Frag col(const char* tile, const Lanes<D>& at, int t, int m) {
+        return transposed(tile + (at.col[0] ^ t * 32) + m * 64 * D, tile + (at.col[1] ^ t * 32) + m * 64 * D);
+    }
+    // The column that row_of(a) gives the lane.
+    template <int D>
+    static __device__ __forceinline__ Frag col_of_state(const char* tile, const Lanes<D>& at, int a, int m) {
+        const int more = m * 64 * D + a % 2 * 8;
+        return transposed(tile + (at.state[0] ^ a / 2 * 64) + more, tile + (at.state[1] ^ a / 2 * 64) + more);
     }
     static __device__ __forceinline__ float get(Frag f, int e) {
         const u32x4 w = __builtin_bit_cast(u32x4, f);
@@ -91,13 +115,14 @@ struct Bf16Ops {
         #pragma unroll
         for (int p = 0; p < N; ++p) f[p] = __builtin_bit_cast(Frag, q[p]);
     }
+    // P of row 16 t + the lane's, columns 16 i + 4 g ..
     template <int N>
-    static __device__ __forceinline__ void store_p(char* P, int t, int i0, const float* v) {
+    static __device__ __forceinline__ void store_p(char* P, const Lanes<L>& at, int t, int i, const float* v) {
         uint32_t lo[N], hi[N];
         split2<N>(v[0], v[1], lo);
         split2<N>(v[2], v[3], hi);
         #pragma unroll
-        for (int p = 0; p < N; ++p) *reinterpret_cast<uint2*>(P + p * L * L * 2 + at<L>(t, i0 / 8) + i0 % 8 * 2) = uint2{lo[p], hi[p]};
+        for (int p = 0; p < N; ++p) *reinterpret_cast<uint2*>(P + p * L * L * 2 + (at.half ^ i * 32) + t * 32 * L) = uint2{lo[p], hi[p]};
     }
 
     // Four neighbouring columns of a row.

@@ -144,7 +144,7 @@ struct State {
         const int j = 16 * wave + (lane & 15), si = transposed ? 1 : dc, sj = transposed ? da : 1;
         #pragma unroll
         for (int a = 0; a < NA; ++a) {
-            const int i = 16 * a + 4 * (lane >> 4);
+            const int i = O::row_of(a, lane >> 4);
             const uint32_t off = uint32_t(i * si + j * sj) * 4;
             #pragma unroll
             for (int r = 0; r < 4; ++r) {
@@ -195,8 +195,8 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
     using St = State<O, DA>;
     constexpr int L = O::L, K = O::K, NL = L / 16, NA = St::NA, kThreads = 4 * DC, kWaves = DC / 16;
     constexpr bool kTight = !(O::E == 8 && DA == 64 && DC == 64 && WHOLE);   // registers are short: less is kept and overlapped
-    constexpr bool kShort = OUT && O::E == 8 && DA == 128 && DC == 128 && WHOLE && NP == 3;   // shorter: the next rows are loaded late, too
-    constexpr bool kKeep = WHOLE && !(O::E == 8 && DA == 128 && DC == 128 && NP == 2);
+    constexpr bool kShort = OUT && O::E == 8 && DA == 128 && DC == 128 && WHOLE && NP == 3;   // shorter: the next c is loaded late, too
+    constexpr bool kKeep = WHOLE && O::E == 8 && !(DA == 128 && DC == 128);
     constexpr bool kLateX = kShort || (DA == 128 && DC == 128);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     float* tabs = reinterpret_cast<float*>(smem + Lay::TAB);
@@ -279,11 +279,9 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
             for (int i = tid; i < NP * L * L * Lay::es / 16; i += kThreads) *reinterpret_cast<uint4*>(smem + Lay::P + 16 * i) = uint4{0, 0, 0, 0};
         }
         stage();
-        if constexpr (!kShort) {
-            if constexpr (!kLateX) fetch_x(count(0, c0, 0));
-            fetch_ab(count(0, c0, 1));
-            fetch_c(count(0, c0, 1));
-        }
+        if constexpr (!kLateX) fetch_x(count(0, c0, 0));
+        fetch_ab(count(0, c0, 1));
+        if constexpr (!kShort) fetch_c(count(0, c0, 1));
     }
     auto put_dots = [&](int c, int n) {   // of the chunk at c, behind a barrier
         if (!dot || tid >= n) return;
@@ -302,8 +300,10 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
 
         f32x4 out[NL];
         typename O::Frag cf[L / K];
-        auto load_cf = [&](int m, uint32_t ln) { cf[m] = O::template col<DC>(smem + Lay::C, m, 16 * wave + 4 * (ln & 3), 16 * wave + (ln & 15), ln); };
         const uint32_t ln = fresh<kTight>(lane), l16 = ln & 15, g4 = ln >> 4;
+        const typename O::template Lanes<DA> at_a(ln);
+        const typename O::template Lanes<DC> at_c(ln);
+        const typename O::template Lanes<L> at_p(ln);
         if constexpr (OUT) {
             // P: lane has row t, four neighbouring i
             constexpr int kTiles = NL * (NL + 1) / 2;
@@ -316,7 +316,7 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
                 f32x4 acc = {0.f, 0.f, 0.f, 0.f};
                 #pragma unroll
                 for (int m = 0; m < DA / K; ++m)
-                    acc = O::mma(O::template row<DA>(smem + Lay::B, 16 * ii + l16, m, g4), O::template row<DA>(smem + Lay::A, 16 * ti + l16, m, g4), acc);
+                    acc = O::mma(O::template row<DA>(smem + Lay::B, at_a, ii, m), O::template row<DA>(smem + Lay::A, at_a, ti, m), acc);
                 const int t = 16 * ti + l16, i0 = 16 * ii + 4 * g4;
                 const float xh = tab[t], xl = tab[64 + t];
                 const f32x4 ih = *reinterpret_cast<const f32x4*>(tab + i0), il = *reinterpret_cast<const f32x4*>(tab + 64 + i0);
@@ -326,7 +326,7 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
                     const float e = __builtin_amdgcn_exp2f((xh - ih[r]) + (xl - il[r]));
                     v[r] = (BACK ? i0 + r >= t : i0 + r <= t) ? sp * acc[r] * e : 0.f;
                 }
-                O::template store_p<NP>(smem + Lay::P, t, i0, v);
+                O::template store_p<NP>(smem + Lay::P, at_p, ti, ii, v);
                 if constexpr (kTight) hold();
             }
             // what the state before the chunk gives
@@ -341,7 +341,7 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
                 O::template split<NP>(v, sf);
                 #pragma unroll
                 for (int ti = 0; ti < NL; ++ti) {
-                    const typename O::Frag af = O::template row_of_state<DA>(smem + Lay::A, 16 * ti + l16, m, g4);
+                    const typename O::Frag af = O::template row<DA>(smem + Lay::A, at_a, ti, m);
                     #pragma unroll
                     for (int p = 0; p < NP; ++p) out[ti] = O::mma(sf[p], af, out[ti]);
                 }
@@ -350,10 +350,6 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
             for (int ti = 0; ti < NL; ++ti) out[ti] *= tab[128 + 16 * ti + l16];
             if constexpr (kTight) hold();
         }
-        if constexpr (kShort && NP < 3) {
-            fetch_ab(count(ch, c0, 1));
-            hold();
-        }
         // the state behind the chunk: c times its decay to the chunk's end
         const float all = tab[256];
         if constexpr (!OUT) kept *= all;
@@ -361,7 +357,8 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
         for (int a = 0; a < NA; ++a) S.s[a] *= all;
         #pragma unroll
         for (int m = 0; m < L / K; ++m) {
-            load_cf(m, ln);
+            cf[m] = O::template col<DC>(smem + Lay::C, at_c, wave, m);
+            const typename O::template Lanes<DA> at_b(fresh<O::E == 4>(ln));   // (32 addresses of single floats are not worth keeping)
             typename O::Frag cs[O::NPU];
             float v[O::E];
             #pragma unroll
@@ -369,14 +366,13 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
             O::template split<O::NPU>(v, cs);
             #pragma unroll
             for (int a = 0; a < NA; ++a) {
-                const typename O::Frag bf = O::template col<DA>(smem + Lay::B, m, 16 * a + 4 * (l16 & 3), 16 * a + l16, ln);
+                const typename O::Frag bf = O::template col_of_state<DA>(smem + Lay::B, at_b, a, m);
                 #pragma unroll
                 for (int p = 0; p < O::NPU; ++p) S.s[a] = O::mma(bf, cs[p], S.s[a]);
             }
         }
         if constexpr (kShort) {
             hold();
-            if constexpr (NP == 3) fetch_ab(count(ch, c0, 1));
             fetch_c(count(ch, c0, 1));
         }
         if constexpr (kLateX) fetch_x(n);
@@ -384,12 +380,12 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
         if constexpr (OUT) {
             #pragma unroll
             for (int m = 0; m < L / K; ++m) {
-                if constexpr (kTight) load_cf(m, ln);   // again
+                if constexpr (kTight) cf[m] = O::template col<DC>(smem + Lay::C, at_c, wave, m);   // again
                 #pragma unroll
                 for (int ti = BACK ? 0 : m * K / 16; ti < (BACK ? (m + 1) * K / 16 : NL); ++ti)
                     #pragma unroll
                     for (int p = 0; p < NP; ++p)
-                        out[ti] = O::mma(cf[m], O::template row<L>(smem + Lay::P + p * L * L * Lay::es, 16 * ti + l16, m, g4), out[ti]);
+                        out[ti] = O::mma(cf[m], O::template row<L>(smem + Lay::P + p * L * L * Lay::es, at_p, ti, m), out[ti]);
             }
         }
         stage();
@@ -416,11 +412,9 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
         g1 = g2;
         settle(g1);
         if (wave == kTabWave) g2 = fetch_g(c0 + 3 * STEP, count(ch, c0, 3));
-        if constexpr (!kShort) {
-            if constexpr (!kLateX) fetch_x(count(ch, c0, 1));
-            fetch_ab(count(ch, c0, 2));
-            fetch_c(count(ch, c0, 2));
-        }
+        if constexpr (!kLateX) fetch_x(count(ch, c0, 1));
+        fetch_ab(count(ch, c0, 2));
+        if constexpr (!kShort) fetch_c(count(ch, c0, 2));
         if constexpr (OUT) {
             const int j = 16 * wave + 4 * g4;
             const rsrc_t d = xo.rows(n);

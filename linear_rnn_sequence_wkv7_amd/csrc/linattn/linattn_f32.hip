@@ -18,31 +18,40 @@ struct F32Ops {
         for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
         return c;
     }
+    // A row's pieces of 16 bytes trade places, as in linattn_bf16.hip.
     template <int D>
-    static __device__ __forceinline__ int at(int row, int piece) {
-        if constexpr (D >= 64) return row * D * 4 + (piece ^ (row & 15)) * 16;
-        else return row * 128 + (piece ^ (row >> 1 & 7)) * 16;
+    static __device__ __forceinline__ uint32_t at(uint32_t row, uint32_t piece) {
+        return row * (4 * D) + (piece ^ (D >= 64 ? row & 15 : row >> 1 & 7)) * 16;
     }
+    static __device__ __forceinline__ constexpr int row_of(int a, int c) { return 16 * a + 4 * c; }
+
     template <int D>
-    static __device__ __forceinline__ Frag row(const char* tile, int r, int m, int g) {
-        return *reinterpret_cast<const Frag*>(tile + at<D>(r, 4 * m + g));
+    struct Lanes {
+        uint32_t row, col;
+        __device__ __forceinline__ Lanes(uint32_t ln) : row(at<D>(ln & 15, ln >> 4)), col(at<D>(ln >> 4 << 2, (ln & 15) >> 2) + (ln & 3) * 4) {}
+    };
+    // Elements 16 m + 4 g .. of row 16 t + the lane's.
+    template <int D>
+    static __device__ __forceinline__ Frag row(const char* tile, const Lanes<D>& at, int t, int m) {
+        return *reinterpret_cast<const Frag*>(tile + (at.row ^ m * 64) + t * 64 * D);
     }
+    // Rows 16 m + 4 g .. of column 16 t + the lane's (D >= 64: a row's last two bits go into its pieces' numbers as they are).
     template <int D>
-    static __device__ __forceinline__ Frag row_of_state(const char* tile, int r, int m, int g) { return row<D>(tile, r, m, g); }
-    // Rows 16 m + 4 g .. of column c.
-    template <int D>
-    static __device__ __forceinline__ Frag col(const char* tile, int m, int, int c, int lane) {
+    static __device__ __forceinline__ Frag col(const char* tile, const Lanes<D>& at, int t, int m) {
         Frag f;
         #pragma unroll
-        for (int e = 0; e < 4; ++e) f[e] = *reinterpret_cast<const float*>(tile + at<D>(16 * m + 4 * (lane >> 4) + e, c / 4) + c % 4 * 4);
+        for (int e = 0; e < 4; ++e) f[e] = *reinterpret_cast<const float*>(tile + (at.col ^ (t * 64 | e * 16)) + (m * 64 + e * 4) * D);
         return f;
     }
+    template <int D>
+    static __device__ __forceinline__ Frag col_of_state(const char* tile, const Lanes<D>& at, int a, int m) { return col<D>(tile, at, a, m); }
     static __device__ __forceinline__ float get(Frag f, int e) { return f[e]; }
     template <int N>
     static __device__ __forceinline__ void split(const float* v, Frag* f) { f[0] = Frag{v[0], v[1], v[2], v[3]}; }
+    // P of row 16 t + the lane's, columns 16 i + 4 g ..
     template <int N>
-    static __device__ __forceinline__ void store_p(char* P, int t, int i0, const float* v) {
-        *reinterpret_cast<Frag*>(P + at<L>(t, i0 / 4)) = Frag{v[0], v[1], v[2], v[3]};
+    static __device__ __forceinline__ void store_p(char* P, const Lanes<L>& at, int t, int i, const float* v) {
+        *reinterpret_cast<Frag*>(P + (at.row ^ i * 64) + t * 64 * L) = Frag{v[0], v[1], v[2], v[3]};
     }
 
     template <bool WHOLE>
