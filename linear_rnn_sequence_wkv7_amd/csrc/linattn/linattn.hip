@@ -248,7 +248,10 @@ void plan(const LinAttnParams& p, int kinds, Chunks* w) {
         }
     }
     const int64_t each = chunks > 0 ? (chunks + best - 1) / best : 1;
-    *w = Chunks{p.B, p.T, p.H, int(best), int(each * 64), p.g_per_token, p.g, p.lengths};
+    *w = Chunks{p.B, p.T, p.H, int(best), int(each * 64), p.g_per_token, p.g, p.lengths, false};
+    // A launch that chains the states pays once there are more of them than a workgroup reads meanwhile; and
+    // where a state is moved in place, since a segment's workgroup would write it while others still read it.
+    w->chained = best > 8 || (best > 1 && p.s0 && p.s0 == p.s1);
 }
 
 struct Carve {   // pieces of a workspace
@@ -369,7 +372,7 @@ hipError_t launch_linattn_forward(const LinAttnParams& p, hipStream_t st) {
     s.s_in = p.s0; s.s_out = p.s1;
     if (w.segs > 1) {
         TRY(p.in_bf16 ? parts_bf16(w, s, st) : parts_f32(w, s, st));
-        TRY(chain(w, {ws.states, ws.kept, p.s0, p.s1}, {}, 1, p.Dk * p.Dv, st));
+        if (w.chained) TRY(chain(w, {ws.states, ws.kept, p.s0, p.s1}, {}, 1, p.Dk * p.Dv, st));
     }
     return p.in_bf16 ? forward_bf16(w, s, st) : forward_f32(w, s, st);
 }
@@ -417,10 +420,9 @@ hipError_t launch_linattn_backward(const LinAttnParams& p, hipStream_t st) {
         f.b = k; f.c = v; f.back = false; f.su = 1.f; f.ws = ws.states[0]; f.kept = ws.kept[0];
         TRY(bf16 ? parts_bf16(w, f, st) : parts_f32(w, f, st));
         TRY(bf16 ? parts_bf16(w, sv, st) : parts_f32(w, sv, st));
-        TRY(chain(w, {ws.states[0], ws.kept[0], p.s0, nullptr}, {ws.states[1], ws.kept[1], p.ds1, p.ds0}, 2, p.Dk * p.Dv, st));
-    } else {
-        sv.s_out = p.ds0;
+        if (w.chained) TRY(chain(w, {ws.states[0], ws.kept[0], p.s0, nullptr}, {ws.states[1], ws.kept[1], p.ds1, p.ds0}, 2, p.Dk * p.Dv, st));
     }
+    sv.s_out = p.ds0;
     TRY(bf16 ? backward_bf16(w, sq, sk, sv, st) : backward_f32(w, sq, sk, sv, st));
     if (p.Hq < p.H && rows > 0) TRY(shared_sum(ws.dq, p.dq, rows, p.Hq, p.H / p.Hq, p.Dk, p.in_bf16, st));
     if (p.Hk < p.H && rows > 0) TRY(shared_sum(ws.dk, p.dk, rows, p.Hk, p.H / p.Hk, p.Dk, p.in_bf16, st));

@@ -210,8 +210,22 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
 
     St S;
     {
-        const float* from = w.segs > 1 ? (OUT ? s.ws + (bh * w.segs + seg) * elems : nullptr) : (s.s_in ? s.s_in + bh * elems : nullptr);
-        S.load(from, da, dc, s.transposed, wave, lane);
+        const float* first = s.s_in ? s.s_in + bh * elems : nullptr;
+        const float* parts = OUT && w.segs > 1 ? s.ws + bh * w.segs * int64_t(elems) : nullptr;
+        if (parts && w.chained) first = parts + int64_t(seg) * elems;
+        S.load(OUT || w.segs == 1 ? first : nullptr, da, dc, s.transposed, wave, lane);
+        if (parts && !w.chained) {   // what the segments before this one add, one after another
+            for (int i = 0; i < (BACK ? w.segs - 1 - seg : seg); ++i) {
+                const int at = BACK ? w.segs - 1 - i : i;
+                St U;
+                U.load(parts + int64_t(at) * elems, da, dc, s.transposed, wave, lane);
+                const float k = s.kept[bh * w.segs + at];
+                #pragma unroll
+                for (int a = 0; a < NA; ++a)
+                    #pragma unroll
+                    for (int r = 0; r < 4; ++r) S.s[a][r] = fmaf(S.s[a][r], k, U.s[a][r]);
+            }
+        }
     }
     float kept = 1.f;   // what is left of a state behind the segment
 
@@ -444,7 +458,7 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
             if (dot)
                 for (int i = end + tid; i < t1; i += kThreads) s.dot[bh * w.T + i] = 0.f;
         }
-        if (w.segs == 1 && s.s_out) S.store(s.s_out + bh * elems, da, dc, s.transposed, wave, lane);
+        if (s.s_out && !w.chained && seg == (BACK ? 0 : w.segs - 1)) S.store(s.s_out + bh * elems, da, dc, s.transposed, wave, lane);
         if (DOTS && s.end_dot && seg == (BACK ? 0 : w.segs - 1)) {   // <the last state, its gradient>
             float d = S.dot(s.end_grad + bh * elems, da, dc, s.transposed, wave, lane);
             #pragma unroll
@@ -475,7 +489,7 @@ __global__ __launch_bounds__(4 * DC, DA == 128 && DC == 64 ? 3 : WHOLE || O::E =
 // that are not in whole pieces come in single elements, of which each takes a register).
 template <typename O, int DA, int DC, int NP, bool WHOLE>
 constexpr int waves_per_simd() {
-    constexpr int lds = 160 * 1024 / Layout<O, DA, DC, NP>::END * (DC / 64), regs = DA == 128 ? (DC == 128 && (WHOLE || O::E == 4) ? 4 : 2) : (WHOLE || O::E == 4) ? 4 : DC == 128 ? 2 : 3;
+    constexpr int lds = 160 * 1024 / Layout<O, DA, DC, NP>::END * (DC / 64), regs = DA == 128 ? (DC == 128 && WHOLE ? 4 : 2) : (WHOLE || O::E == 4) ? 4 : DC == 128 ? 2 : 3;
     return lds < regs ? lds : regs;
 }
 struct Pair {

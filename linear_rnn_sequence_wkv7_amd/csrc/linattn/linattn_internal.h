@@ -49,16 +49,17 @@ struct Chunks {
     bool g_per_token;
     const float* g;
     const int32_t* lengths;
+    bool chained;             // the states before the segments are there; else each adds up the parts before it
 };
 struct Sweep {
     Operand a, b, c;
     Operand x;                // with dot: [B, H, T] sums of out x over the columns, before out is rounded
     void* out;                // [B, T, out_heads, c.D]
     float* dot;
-    float* ws;                // [B, H, segs, Dk, Dv]: what segments add; then the state before each
+    float* ws;                // [B, H, segs, Dk, Dv]: what segments add; chained: then the state before each
     float* kept;              // [B, H, segs]: what is left of a state behind each
-    const float* s_in;        // [B, H, Dk, Dv] or null, where there is one segment
-    float* s_out;
+    const float* s_in;        // [B, H, Dk, Dv] or null
+    float* s_out;             // (unless chained)
     const float* end_grad;    // with end_dot [B, H]: <state behind the last token, end_grad>
     float* end_dot;
     float sp, si, su;
