@@ -14,10 +14,9 @@ constexpr int kThreads = 256;
 // ---------------------------------------------------------------- chain of segments
 
 struct Chain {
-    float* ws;            // [B, H, segs, Dk, Dv]: what the segments add; becomes the state before each
+    float* ws;            // [B, H, segs, Dk, Dv]: what the segments add (but the last); becomes the state before each
     const float* kept;    // [B, H, segs]
     const float* first;   // [B, H, Dk, Dv] or null
-    float* last;
 };
 // A thread per element of a state.  Eight segments' parts are read before the first is needed.
 __global__ __launch_bounds__(kThreads) void chain_kernel(Chain f, Chain r, int segs, int elems) {
@@ -34,25 +33,24 @@ __global__ __launch_bounds__(kThreads) void chain_kernel(Chain f, Chain r, int s
         #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int at = back ? segs - 1 - i0 - i : i0 + i;
-            u[i] = i0 + i < segs ? p[int64_t(at) * elems] : 0.f;
+            u[i] = i0 + i < segs - 1 ? p[int64_t(at) * elems] : 0.f;
         }
         #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if (i0 + i >= segs) break;
             const int at = back ? segs - 1 - i0 - i : i0 + i;
             p[int64_t(at) * elems] = s;
-            s = fmaf(k[at], s, u[i]);
+            if (i0 + i < segs - 1) s = fmaf(k[at], s, u[i]);
         }
     }
-    if (c.last) c.last[bh * elems + e] = s;
 }
 
 // ---------------------------------------------------------------- gradient of g
 
 // The gradient of g_t is the sum over u >= t of <q_u, dq_u> - <k_u, dk_u>, and <state, its
 // gradient> behind the last token: what a change of every running sum from t on does.  A
-// workgroup takes 2048 tokens of a sequence and head; it adds up the later ones itself (from the
-// caches), so that none waits for another.  In 64 bits.
+// workgroup takes 2048 tokens of a sequence and head; of more, a launch before it has added up each
+// 2048, so that none waits for another.  In 64 bits.
 constexpr int kDgThreads = 1024, kDgPer = 2, kDgRun = kDgThreads * kDgPer;
 int dg_runs(int T) { return (T + kDgRun - 1) / kDgRun; }
 __device__ __forceinline__ double block_sum(double v, double* sums) {
@@ -65,7 +63,22 @@ __device__ __forceinline__ double block_sum(double v, double* sums) {
     for (int i = 0; i < kDgThreads / 64; ++i) v += sums[i];
     return v;
 }
-__global__ __launch_bounds__(kDgThreads) void dg_kernel(const float* qd, const float* kd, const float* end, Chunks w, int runs, float* dg, float* part) {
+// runs [B, H, runs]: each run's sum.
+__global__ __launch_bounds__(kDgThreads) void dg_runs_kernel(const float* qd, const float* kd, int T, int runs, double* out) {
+    __shared__ double sums[kDgThreads / 64];
+    const int run = int(blockIdx.x % runs), last = T - 1;
+    const int64_t bh = blockIdx.x / runs;
+    const float *q = qd + bh * T, *k = kd + bh * T;
+    double v = 0.0;
+    #pragma unroll
+    for (int i = 0; i < kDgPer; ++i) {
+        const int t = last - run * kDgRun - i * kDgThreads - int(threadIdx.x);
+        if (t >= 0) v += double(q[t]) - double(k[t]);
+    }
+    v = block_sum(v, sums);
+    if (threadIdx.x == 0) out[blockIdx.x] = v;
+}
+__global__ __launch_bounds__(kDgThreads) void dg_kernel(const float* qd, const float* kd, const float* end, const double* run_sums, Chunks w, int runs, float* dg, float* part) {
     __shared__ double sums[kDgThreads / 64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int run = int(blockIdx.x % runs);   // counted from the end, as the tokens are below
@@ -74,7 +87,7 @@ __global__ __launch_bounds__(kDgThreads) void dg_kernel(const float* qd, const f
     const int len = seq_length(w.lengths, b, w.T);
     const float *q = qd + bh * w.T, *k = kd + bh * w.T;
     double later = 0.0;
-    for (int r = tid; r < run * kDgRun; r += kDgThreads) later += double(q[last - r]) - double(k[last - r]);
+    for (int r = tid; r < run; r += kDgThreads) later += run_sums[bh * runs + r];
     later = block_sum(later, sums) + (end ? end[bh] : 0.f);
     const int r0 = run * kDgRun + tid * kDgPer;
     double v[kDgPer], sum = 0.0, total = 0.0;
@@ -241,7 +254,7 @@ void plan(const LinAttnParams& p, int kinds, Chunks* w) {
         const int64_t each = (chunks + segs - 1) / segs;
         if (segs > 1 && (chunks + each - 1) / each != segs) continue;   // the same as fewer
         int64_t time = rounds(heads * kinds, segs, each, groups, lat, thr);
-        if (segs > 1) time += (kinds > 1 ? 2 : 1) * (rounds(heads, segs, each, 2, both ? 28 : 15, both ? 22 : 9) + 60 + heads * segs * p.Dk * p.Dv / 50000);
+        if (segs > 1) time += (kinds > 1 ? 2 : 1) * (rounds(heads, segs - 1, each, 2, both ? 28 : 15, both ? 22 : 9) + 60 + heads * segs * p.Dk * p.Dv / 50000);
         if (least < 0 || time < least) {
             least = time;
             best = segs;
@@ -276,6 +289,7 @@ struct ForwardWs {
 };
 struct BackwardWs {
     float *qd, *kd, *end, *part, *states[2], *kept[2], *dq, *dk, *dv;
+    double* runs;
     int64_t bytes;
     BackwardWs(const LinAttnParams& p, const Chunks& w, void* ws) {
         Carve c{static_cast<char*>(ws)};
@@ -284,6 +298,7 @@ struct BackwardWs {
         kd = c.floats(bh * p.T);
         end = c.floats(bh);
         part = c.floats(bh * dg_runs(p.T));
+        runs = reinterpret_cast<double*>(c.floats(dg_runs(p.T) > 1 ? bh * dg_runs(p.T) * 2 : 0));
         for (int i = 0; i < 2; ++i) {
             states[i] = c.floats(n * p.Dk * p.Dv);
             kept[i] = c.floats(n);
@@ -304,7 +319,6 @@ hipError_t chain(const Chunks& w, const Chain& f, const Chain& r, int kinds, int
             c.ws += h0 * w.segs * elems;
             c.kept += h0 * w.segs;
             c.first = c.first ? c.first + h0 * elems : nullptr;
-            c.last = c.last ? c.last + h0 * elems : nullptr;
             return c;
         };
         chain_kernel<<<dim3((elems + kThreads - 1) / kThreads, n, kinds), kThreads, 0, st>>>(from(f), kinds > 1 ? from(r) : from(f), w.segs, elems);
@@ -372,7 +386,7 @@ hipError_t launch_linattn_forward(const LinAttnParams& p, hipStream_t st) {
     s.s_in = p.s0; s.s_out = p.s1;
     if (w.segs > 1) {
         TRY(p.in_bf16 ? parts_bf16(w, s, st) : parts_f32(w, s, st));
-        if (w.chained) TRY(chain(w, {ws.states, ws.kept, p.s0, p.s1}, {}, 1, p.Dk * p.Dv, st));
+        if (w.chained) TRY(chain(w, {ws.states, ws.kept, p.s0}, {}, 1, p.Dk * p.Dv, st));
     }
     return p.in_bf16 ? forward_bf16(w, s, st) : forward_f32(w, s, st);
 }
@@ -420,7 +434,7 @@ hipError_t launch_linattn_backward(const LinAttnParams& p, hipStream_t st) {
         f.b = k; f.c = v; f.back = false; f.su = 1.f; f.ws = ws.states[0]; f.kept = ws.kept[0];
         TRY(bf16 ? parts_bf16(w, f, st) : parts_f32(w, f, st));
         TRY(bf16 ? parts_bf16(w, sv, st) : parts_f32(w, sv, st));
-        if (w.chained) TRY(chain(w, {ws.states[0], ws.kept[0], p.s0, nullptr}, {ws.states[1], ws.kept[1], p.ds1, p.ds0}, 2, p.Dk * p.Dv, st));
+        if (w.chained) TRY(chain(w, {ws.states[0], ws.kept[0], p.s0}, {ws.states[1], ws.kept[1], p.ds1}, 2, p.Dk * p.Dv, st));
     }
     sv.s_out = p.ds0;
     TRY(bf16 ? backward_bf16(w, sq, sk, sv, st) : backward_f32(w, sq, sk, sv, st));
@@ -429,7 +443,9 @@ hipError_t launch_linattn_backward(const LinAttnParams& p, hipStream_t st) {
     if (p.Hv < p.H && rows > 0) TRY(shared_sum(ws.dv, p.dv, rows, p.Hv, p.H / p.Hv, p.Dv, p.in_bf16, st));
     if (p.dg) {
         const int runs = dg_runs(p.T);
-        if (rows > 0) dg_kernel<<<uint32_t(int64_t(p.B) * p.H * runs), kDgThreads, 0, st>>>(ws.qd, ws.kd, sq.end_dot, w, runs, p.dg, ws.part);
+        const uint32_t jobs = uint32_t(int64_t(p.B) * p.H * runs);
+        if (runs > 1) dg_runs_kernel<<<jobs, kDgThreads, 0, st>>>(ws.qd, ws.kd, p.T, runs, ws.runs);
+        if (rows > 0) dg_kernel<<<jobs, kDgThreads, 0, st>>>(ws.qd, ws.kd, sq.end_dot, ws.runs, w, runs, p.dg, ws.part);
         if (!p.g_per_token) dg_heads_kernel<<<p.H, 64, 0, st>>>(ws.part, p.dg, rows > 0 ? p.B : 0, p.H, rows > 0 ? runs : 1);
     }
     return hipGetLastError();

@@ -175,10 +175,10 @@ struct State {
 // for them (`kinds`) fastest, in runs of neighbours for each XCD.
 struct Place {
     int kind, seg, h, b;
-    __device__ __forceinline__ Place(const Chunks& w, int kinds) {
+    __device__ __forceinline__ Place(const Chunks& w, int segs, int kinds) {
         uint32_t i = uint32_t(xcd_order(blockIdx.x, gridDim.x));   // less than 2^32 threads
         kind = int(i % kinds); i /= kinds;
-        seg = int(i % w.segs); i /= w.segs;
+        seg = int(i % segs); i /= segs;
         h = int(i % w.H);
         b = int(i / w.H);
     }
@@ -213,7 +213,7 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
         const float* first = s.s_in ? s.s_in + bh * elems : nullptr;
         const float* parts = OUT && w.segs > 1 ? s.ws + bh * w.segs * int64_t(elems) : nullptr;
         if (parts && w.chained) first = parts + int64_t(seg) * elems;
-        S.load(OUT || w.segs == 1 ? first : nullptr, da, dc, s.transposed, wave, lane);
+        S.load(OUT ? first : nullptr, da, dc, s.transposed, wave, lane);
         if (parts && !w.chained) {   // what the segments before this one add, one after another
             for (int i = 0; i < (BACK ? w.segs - 1 - seg : seg); ++i) {
                 const int at = BACK ? w.segs - 1 - i : i;
@@ -458,7 +458,7 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
             if (dot)
                 for (int i = end + tid; i < t1; i += kThreads) s.dot[bh * w.T + i] = 0.f;
         }
-        if (s.s_out && !w.chained && seg == (BACK ? 0 : w.segs - 1)) S.store(s.s_out + bh * elems, da, dc, s.transposed, wave, lane);
+        if (s.s_out && seg == (BACK ? 0 : w.segs - 1)) S.store(s.s_out + bh * elems, da, dc, s.transposed, wave, lane);
         if (DOTS && s.end_dot && seg == (BACK ? 0 : w.segs - 1)) {   // <the last state, its gradient>
             float d = S.dot(s.end_grad + bh * elems, da, dc, s.transposed, wave, lane);
             #pragma unroll
@@ -478,12 +478,12 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
     }
 }
 
-// What the segments add to a state.
+// What the segments add to a state; but the last, behind which none follows.
 template <typename O, int DA, int DC, bool BACK, bool WHOLE>
 __global__ __launch_bounds__(4 * DC, DA == 128 && DC == 64 ? 3 : WHOLE || O::E == 4 || DA == 64 ? 4 : 2) void parts_kernel(Chunks w, Sweep s) {
     __shared__ alignas(16) char smem[Layout<O, DA, DC, 0>::END];
-    const Place at(w, 1);
-    sweep<O, DA, DC, 0, BACK, false, WHOLE>(w, s, at.b, at.h, at.seg, smem);
+    const Place at(w, w.segs - 1, 1);
+    sweep<O, DA, DC, 0, BACK, false, WHOLE>(w, s, at.b, at.h, at.seg + BACK, smem);
 }
 // Waves to a SIMD: as many workgroups as their LDS allows, and no more than their registers do (rows
 // that are not in whole pieces come in single elements, of which each takes a register).
@@ -499,7 +499,7 @@ struct Pair {
 template <typename O, int DA, int DC, int NP, bool BACK, bool DOTS, bool WHOLE>
 __global__ __launch_bounds__(4 * DC, (waves_per_simd<O, DA, DC, NP, WHOLE>())) void outs_kernel(Chunks w, Pair s, int kinds) {
     __shared__ alignas(16) char smem[Layout<O, DA, DC, NP>::END];
-    const Place at(w, kinds);
+    const Place at(w, w.segs, kinds);
     sweep<O, DA, DC, NP, BACK, DOTS, WHOLE>(w, s.s[at.kind], at.b, at.h, at.seg, smem);
 }
 
@@ -510,7 +510,7 @@ struct Three {
 template <typename O, int D, bool WHOLE>
 __global__ __launch_bounds__(4 * D, (waves_per_simd<O, D, D, O::NPU, WHOLE>())) void grads_kernel(Chunks w, Three s) {
     __shared__ alignas(16) char smem[Layout<O, D, D, O::NPU>::END];
-    const Place at(w, 3);
+    const Place at(w, w.segs, 3);
     if (at.kind == 0) sweep<O, D, D, O::NPU, false, true, WHOLE>(w, s.s[0], at.b, at.h, at.seg, smem);
     else sweep<O, D, D, O::NPU, true, true, WHOLE>(w, s.s[at.kind], at.b, at.h, at.seg, smem);
 }
@@ -529,7 +529,7 @@ inline bool same_width(int d, int e) { return (d <= 64) == (e <= 64); }
 template <typename O>
 inline hipError_t launch_parts(const Chunks& w, const Sweep& s, hipStream_t st) {
     return with_widths<O>(s.a.D, s.c.D, [&](auto da, auto dc, auto whole) {
-        const dim3 grid(uint32_t(int64_t(w.B) * w.H * w.segs));
+        const dim3 grid(uint32_t(int64_t(w.B) * w.H * (w.segs - 1)));
         if (s.back) parts_kernel<O, da, dc, true, whole><<<grid, 4 * dc, 0, st>>>(w, s);
         else parts_kernel<O, da, dc, false, whole><<<grid, 4 * dc, 0, st>>>(w, s);
         return hipGetLastError();
