@@ -231,15 +231,19 @@ hipError_t step_rows(const LinAttnParams& p, dim3 grid, hipStream_t st) {
 
 // Sequences are cut into segments, computed side by side, where their heads alone do not occupy the
 // chip.  The number is the one with the least time by what was measured (in 0.1 us): a workgroup by
-// itself takes `lat` for a chunk, several on a compute unit `thr` each (at heads of 64 that is 4.2 TB/s,
-// at 128 the vector units are busy too), and about two chunks' time goes before the first; more than one
-// segment costs a pass over two of the operands and the chain of the states.
-//   4 x 4096, 40 heads of 64: 1 segment 211 us, 2 181, 3 136, 4 142, 8 135; 1 x 2048, 32 heads of 128: 1 154,
-//   4 73, 8 56, 16 61; 8 x 1024, 32 heads of 64: 1 55, 2 70.
+// itself takes `lat` for a chunk, several on a compute unit `thr` each, and about two chunks' time goes
+// before the first; more than one segment costs a pass over two of the operands and the joining of the states.
+// us by the number of segments, bf16:
+//   forward   1 x 2048, 32 heads of 128   1: 156   4: 70    6: 59   8: 52   16: 60
+//             4 x 4096, 40 heads of 64    1: 223   2: 193   3: 133  4: 148  8: 135
+//             8 x 1024, 32 heads of 64    1: 52    2: 50    4: 59
+//             1 x 65536, 16 heads of 64   8: 537   16: 287  32: 205
+//   backward  2 x 2048, 32 heads of 64    1: 132   2: 129   4: 94   8: 96   16: 115
+//             4 x 1024, 32 heads of 128   1: 149   2: 186   4: 211
 void plan(const LinAttnParams& p, int kinds, Chunks* w) {
     const int64_t heads = int64_t(p.B) * p.H, chunks = (int64_t(p.T) + 63) / 64;
     const bool wide = p.Dk > 64 || p.Dv > 64, both = p.Dk > 64 && p.Dv > 64;
-    const int groups = both ? 2 : 3, lat = both ? 50 : wide ? 40 : 31, thr = both ? 45 : wide ? 32 : 20;
+    const int groups = both ? 2 : 3, lat = both ? 45 : wide ? 36 : 28, thr = both ? 36 : wide ? 28 : 20;
     auto rounds = [&](int64_t jobs, int64_t segs, int64_t each, int groups, int lat, int thr) {   // the fullest compute unit's
         int64_t time = 0;
         for (int64_t k = (jobs * segs + 255) / 256; k > 0; k -= groups) {
@@ -254,7 +258,7 @@ void plan(const LinAttnParams& p, int kinds, Chunks* w) {
         const int64_t each = (chunks + segs - 1) / segs;
         if (segs > 1 && (chunks + each - 1) / each != segs) continue;   // the same as fewer
         int64_t time = rounds(heads * kinds, segs, each, groups, lat, thr);
-        if (segs > 1) time += (kinds > 1 ? 2 : 1) * (rounds(heads, segs - 1, each, 2, both ? 28 : 15, both ? 22 : 9) + 60 + heads * segs * p.Dk * p.Dv / 50000);
+        if (segs > 1) time += (kinds > 1 ? 2 : 1) * (rounds(heads, segs - 1, each, 2, both ? 28 : 12, both ? 22 : 8) + heads * segs * p.Dk * p.Dv / 200000) + 60;
         if (least < 0 || time < least) {
             least = time;
             best = segs;
@@ -262,9 +266,12 @@ void plan(const LinAttnParams& p, int kinds, Chunks* w) {
     }
     const int64_t each = chunks > 0 ? (chunks + best - 1) / best : 1;
     *w = Chunks{p.B, p.T, p.H, int(best), int(each * 64), p.g_per_token, p.g, p.lengths, false};
-    // A launch that chains the states pays once there are more of them than a workgroup reads meanwhile; and
-    // where a state is moved in place, since a segment's workgroup would write it while others still read it.
-    w->chained = best > 8 || (best > 1 && p.s0 && p.s0 == p.s1);
+    // Either each workgroup adds up the states of the segments before its own or, if there are more, a launch
+    // does it for all (and where a state is moved in place, since a segment's workgroup would write it while
+    // others still read it).  The gradients read two of three states transposed, a fourth of the speed.  1 x
+    // 4096, 16 heads of 64: forward 8 segments 44 us without the launch, 43 with it, 16 35 and 32; backward 2
+    // 205 and 208, 4 120 and 119, 8 93 and 84.  1 x 2048, 32 heads of 128, forward: 8 52 and 57, 16 68 and 60.
+    w->chained = best > (kinds > 1 ? 2 : 8) || (best > 1 && p.s0 && p.s0 == p.s1);
 }
 
 struct Carve {   // pieces of a workspace
