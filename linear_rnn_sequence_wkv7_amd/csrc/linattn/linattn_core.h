@@ -208,25 +208,6 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
     const int da = s.a.D, dc = s.c.D, elems = da * dc;
     const float si = s.si, su = s.su, sp = s.sp;
 
-    St S;
-    {
-        const float* first = s.s_in ? s.s_in + bh * elems : nullptr;
-        const float* parts = OUT && w.segs > 1 ? s.ws + bh * w.segs * int64_t(elems) : nullptr;
-        if (parts && w.chained) first = parts + int64_t(seg) * elems;
-        S.load(OUT ? first : nullptr, da, dc, s.transposed, wave, lane);
-        if (parts && !w.chained) {   // what the segments before this one add, one after another
-            for (int i = 0; i < (BACK ? w.segs - 1 - seg : seg); ++i) {
-                const int at = BACK ? w.segs - 1 - i : i;
-                St U;
-                U.load(parts + int64_t(at) * elems, da, dc, s.transposed, wave, lane);
-                const float k = s.kept[bh * w.segs + at];
-                #pragma unroll
-                for (int a = 0; a < NA; ++a)
-                    #pragma unroll
-                    for (int r = 0; r < 4; ++r) S.s[a][r] = fmaf(S.s[a][r], k, U.s[a][r]);
-            }
-        }
-    }
     float kept = 1.f;   // what is left of a state behind the segment
 
     auto bf16 = [](const Operand& x) { return O::E == 8 || x.bf16; };   // known where every operand is
@@ -279,11 +260,33 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
     float g1 = 0.f, g2 = 0.f;
     const float gc = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(nch > 0 && !w.g_per_token ? w.g[h] : 0.f)));
     auto fetch_g = [&](int c, int n) { return load_g(w, gc, row_t0 + c, n, h, int(fresh(lane))); };
+    float g0 = 0.f;
     if (nch > 0) {
         fetch_ab(count(0, c0, 0));
         fetch_c(count(0, c0, 0));
+        if (wave == kTabWave) g0 = fetch_g(c0, count(0, c0, 0));
+    }
+    St S;
+    {
+        const float* first = s.s_in ? s.s_in + bh * elems : nullptr;
+        const float* parts = OUT && w.segs > 1 ? s.ws + bh * w.segs * int64_t(elems) : nullptr;
+        if (parts && w.chained) first = parts + int64_t(seg) * elems;
+        S.load(OUT ? first : nullptr, da, dc, s.transposed, wave, lane);
+        if (parts && !w.chained) {   // what the segments before this one add, one after another
+            for (int i = 0; i < (BACK ? w.segs - 1 - seg : seg); ++i) {
+                const int at = BACK ? w.segs - 1 - i : i;
+                St U;
+                U.load(parts + int64_t(at) * elems, da, dc, s.transposed, wave, lane);
+                const float k = s.kept[bh * w.segs + at];
+                #pragma unroll
+                for (int a = 0; a < NA; ++a)
+                    #pragma unroll
+                    for (int r = 0; r < 4; ++r) S.s[a][r] = fmaf(S.s[a][r], k, U.s[a][r]);
+            }
+        }
+    }
+    if (nch > 0) {
         if (wave == kTabWave) {
-            const float g0 = fetch_g(c0, count(0, c0, 0));
             g1 = fetch_g(c0 + STEP, count(0, c0, 1));
             g2 = fetch_g(c0 + 2 * STEP, count(0, c0, 2));
             make_tables<BACK>(tabs, g0, si, su, lane);
