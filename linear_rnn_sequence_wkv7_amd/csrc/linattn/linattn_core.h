@@ -47,6 +47,17 @@ constexpr int kTab = 4 * 64 + 16;
 // keeps registers free for more waves.
 __device__ __forceinline__ void hold() { __builtin_amdgcn_sched_barrier(0); }
 
+// N fragments of READS LDS reads each, that MMAS products use: reads are issued AHEAD fragments before their products.
+template <int AHEAD, int READS, int MMAS, int N>
+__device__ __forceinline__ void pace() {
+    #pragma unroll
+    for (int i = 0; i < N + AHEAD; ++i) {
+        if (i < N) __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+        if (i >= AHEAD) __builtin_amdgcn_sched_group_barrier(0x008, MMAS, 0);
+    }
+    hold();
+}
+
 template <typename O, int DA, int DC, int NPP>
 struct Layout {
     static constexpr int L = O::L, es = int(sizeof(typename O::elem));
@@ -197,6 +208,7 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
     constexpr bool kTight = !(O::E == 8 && DA == 64 && DC == 64 && WHOLE);   // registers are short: less is kept and overlapped
     constexpr bool kShort = OUT && O::E == 8 && DA == 128 && DC == 128 && WHOLE && NP == 3;   // shorter: the next c is loaded late, too
     constexpr bool kKeep = WHOLE && O::E == 8 && !(DA == 128 && DC == 128);
+    constexpr bool kPace = O::E == 8;
     constexpr bool kLateX = kShort || (DA == 128 && DC == 128);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     float* tabs = reinterpret_cast<float*>(smem + Lay::TAB);
@@ -381,12 +393,14 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
             #pragma unroll
             for (int e = 0; e < O::E; ++e) v[e] = O::get(cf[m], e) * tab[192 + K * m + O::E * g4 + e];
             O::template split<O::NPU>(v, cs);
+            if constexpr (kPace) hold();
             #pragma unroll
             for (int a = 0; a < NA; ++a) {
                 const typename O::Frag bf = O::template col_of_state<DA>(smem + Lay::B, at_b, a, m);
                 #pragma unroll
                 for (int p = 0; p < O::NPU; ++p) S.s[a] = O::mma(bf, cs[p], S.s[a]);
             }
+            if constexpr (kPace) pace<OUT ? 1 : 2, 2, O::NPU, NA>();
         }
         if constexpr (kShort) {
             hold();
