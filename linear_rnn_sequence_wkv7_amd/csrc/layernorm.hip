@@ -402,6 +402,7 @@ __global__ __launch_bounds__(1024) void ln_sum_kernel(const float* part, int64_t
     const int64_t at = int64_t(blockIdx.x) * 32 + x;
     float s = 0.f;
     if (at < 2 * int64_t(C))
+        #pragma unroll 8
         for (int64_t g = y; g < groups; g += 32) s += part[g * 2 * C + at];
     lds[y][x] = s;
     __syncthreads();

@@ -265,7 +265,8 @@ void plan(const LinAttnParams& p, int kinds, Chunks* w) {
         }
     }
     const int64_t each = chunks > 0 ? (chunks + best - 1) / best : 1;
-    *w = Chunks{p.B, p.T, p.H, int(best), int(each * 64), p.g_per_token, p.g, p.lengths, false};
+    const int least_heads = p.Hq < p.Hk ? (p.Hq < p.Hv ? p.Hq : p.Hv) : (p.Hk < p.Hv ? p.Hk : p.Hv), group = p.H ? p.H / least_heads : 1;
+    *w = Chunks{p.B, p.T, p.H, group, int(best), int(each * 64), p.g_per_token, p.g, p.lengths, false};
     // Either each workgroup adds up the states of the segments before its own or, if there are more, a launch
     // does it for all (and where a state is moved in place, since a segment's workgroup would write it while
     // others still read it).  The gradients read two of three states transposed, a fourth of the speed.  1 x

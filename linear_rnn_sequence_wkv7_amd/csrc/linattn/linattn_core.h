@@ -61,7 +61,9 @@ __device__ __forceinline__ void pace() {
 template <typename O, int DA, int DC, int NPP>
 struct Layout {
     static constexpr int L = O::L, es = int(sizeof(typename O::elem));
-    static constexpr int A = 0, B = A + (NPP ? L * DA * es : 0), C = B + L * DA * es, P = C + L * DC * es;
+    static constexpr int A = 0, B = A + (NPP ? L * DA * es : 0), C = B + L * DA * es;
+    static constexpr int NEXT = NPP ? 0 : L * (DA + DC) * es;   // where no out is computed the next chunk's rows have a place of their own
+    static constexpr int P = C + L * DC * es + NEXT;
     static constexpr int TAB = P + NPP * L * L * es;
     static constexpr int DOT = TAB + 2 * kTab * 4;        // float [waves][64], behind them one of each
     static constexpr int END = DOT + (DC / 16 * 64 + 16) * 4;
@@ -182,16 +184,20 @@ struct State {
     }
 };
 
-// The workgroup's place in the launch: segments of a head, heads, sequences, and what is computed
-// for them (`kinds`) fastest, in runs of neighbours for each XCD.
+// The workgroup's place in the launch, in runs of neighbours for each XCD: the heads that share an operand
+// fastest, then what is computed for them (`kinds`), segments, heads, sequences, so that rows that several
+// read come from the XCD's L2.  The gradients of 2 x 16384 tokens, 32 heads of 128 sharing q and k in
+// fours read 1.75 GB in this order; with heads slowest 3.0, and 3 % slower.
 struct Place {
     int kind, seg, h, b;
     __device__ __forceinline__ Place(const Chunks& w, int segs, int kinds) {
         uint32_t i = uint32_t(xcd_order(blockIdx.x, gridDim.x));   // less than 2^32 threads
+        const int in = int(i % w.group); i /= w.group;
         kind = int(i % kinds); i /= kinds;
         seg = int(i % segs); i /= segs;
-        h = int(i % w.H);
-        b = int(i / w.H);
+        const int groups = w.H / w.group;
+        h = int(i % groups) * w.group + in;
+        b = int(i / groups);
     }
 };
 
@@ -258,10 +264,11 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
             xx.move(STEP);
         }
     };
-    auto stage = [&] {
-        if constexpr (OUT) ra.stage(smem + Lay::A, a16);
-        rb.stage(smem + Lay::B, b16);
-        rc.stage(smem + Lay::C, c16);
+    auto stage = [&](int ch) {
+        char* tile = smem + (ch & 1) * Lay::NEXT;
+        if constexpr (OUT) ra.stage(tile + Lay::A, a16);
+        rb.stage(tile + Lay::B, b16);
+        rc.stage(tile + Lay::C, c16);
     };
     // how many tokens the chunk `ahead` of the one at c0 has, or 0
     auto count = [&](int ch, int c0, int ahead) { return ch + ahead < nch ? min(L, tokens - c0 - ahead * STEP) : 0; };
@@ -307,7 +314,7 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
         if constexpr (OUT && K > 16) {   // the blocks of P that a wider contraction reads past the diagonal
             for (int i = tid; i < NP * L * L * Lay::es / 16; i += kThreads) *reinterpret_cast<uint4*>(smem + Lay::P + 16 * i) = uint4{0, 0, 0, 0};
         }
-        stage();
+        stage(0);
         if constexpr (!kLateX) fetch_x(count(0, c0, 0));
         fetch_ab(count(0, c0, 1));
         if constexpr (!kShort) fetch_c(count(0, c0, 1));
@@ -323,6 +330,7 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
     for (int ch = 0; ch < nch; ++ch) {
         const int n = count(ch, c0, 0);
         const float* tab = tabs + (ch & 1) * kTab;
+        const char* tile = smem + (ch & 1) * Lay::NEXT;
         __syncthreads();
         if (OUT && ch > 0) put_dots(c0 - STEP, count(ch - 1, c0 - STEP, 0));
         if (wave == kTabWave) make_tables<BACK>(tabs + (ch + 1 & 1) * kTab, g1, si, su, lane);
@@ -386,7 +394,7 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
         for (int a = 0; a < NA; ++a) S.s[a] *= all;
         #pragma unroll
         for (int m = 0; m < L / K; ++m) {
-            cf[m] = O::template col<DC>(smem + Lay::C, at_c, wave, m);
+            cf[m] = O::template col<DC>(tile + Lay::C, at_c, wave, m);
             const typename O::template Lanes<DA> at_b(fresh<O::E == 4>(ln));   // (32 addresses of single floats are not worth keeping)
             typename O::Frag cs[O::NPU];
             float v[O::E];
@@ -396,7 +404,7 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
             if constexpr (kPace) hold();
             #pragma unroll
             for (int a = 0; a < NA; ++a) {
-                const typename O::Frag bf = O::template col_of_state<DA>(smem + Lay::B, at_b, a, m);
+                const typename O::Frag bf = O::template col_of_state<DA>(tile + Lay::B, at_b, a, m);
                 #pragma unroll
                 for (int p = 0; p < O::NPU; ++p) S.s[a] = O::mma(bf, cs[p], S.s[a]);
             }
@@ -407,8 +415,8 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
             fetch_c(count(ch, c0, 1));
         }
         if constexpr (kLateX) fetch_x(n);
-        __syncthreads();
         if constexpr (OUT) {
+            __syncthreads();
             #pragma unroll
             for (int m = 0; m < L / K; ++m) {
                 if constexpr (kTight) cf[m] = O::template col<DC>(smem + Lay::C, at_c, wave, m);   // again
@@ -419,7 +427,7 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
                         out[ti] = O::mma(cf[m], O::template row<L>(smem + Lay::P + p * L * L * Lay::es, at_p, ti, m), out[ti]);
             }
         }
-        stage();
+        stage(ch + 1);
         if constexpr (DOTS) {   // over a wave's columns by halves: the group of 16 lanes then has tile 0, 2, 1 or 3 (0, 0, 1, 1 of two)
             float v[NL], x[4];
             #pragma unroll

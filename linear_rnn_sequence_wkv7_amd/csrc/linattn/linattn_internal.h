@@ -45,6 +45,7 @@ struct Operand {   // [B, T, heads, D]
 };
 struct Chunks {
     int B, T, H;
+    int group;                // how many consecutive heads share an operand
     int segs, seg_tokens;     // sequences are computed in parts side by side, of a multiple of 64 tokens
     bool g_per_token;
     const float* g;
@@ -59,7 +60,7 @@ struct Sweep {
     float* ws;                // [B, H, segs, Dk, Dv]: what segments add; chained: then the state before each
     float* kept;              // [B, H, segs]: what is left of a state behind each
     const float* s_in;        // [B, H, Dk, Dv] or null
-    float* s_out;             // (unless chained)
+    float* s_out;             // or null
     const float* end_grad;    // with end_dot [B, H]: <state behind the last token, end_grad>
     float* end_dot;
     float sp, si, su;
