@@ -416,10 +416,14 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
         }
         if constexpr (kLateX) fetch_x(n);
         if constexpr (OUT) {
+            if constexpr (kTight) {   // again, and in front of the barrier, behind which other waves write the next chunk there
+                hold();
+                #pragma unroll
+                for (int m = 0; m < L / K; ++m) cf[m] = O::template col<DC>(tile + Lay::C, at_c, wave, m);
+            }
             __syncthreads();
             #pragma unroll
             for (int m = 0; m < L / K; ++m) {
-                if constexpr (kTight) cf[m] = O::template col<DC>(smem + Lay::C, at_c, wave, m);   // again
                 #pragma unroll
                 for (int ti = BACK ? 0 : m * K / 16; ti < (BACK ? (m + 1) * K / 16 : NL); ++ti)
                     #pragma unroll

@@ -291,6 +291,21 @@ def test_attention_between_guards(case):
     same("y in place", y2, y), same("state in place", state, s)
 
 
+@pytest.mark.parametrize("B,T,H", [(0, 5, 2), (2, 0, 3), (2, 5, 0), (0, 0, 0)])
+@pytest.mark.parametrize("constant", [False, True])
+def test_attention_of_nothing(B, T, H, constant):
+    """Without tokens the state and its gradient pass through, and constant decays have a gradient of 0."""
+    la = mods()[1]
+    t = torch()
+    q, g = t.ones(B, T, H, 8, device="cuda"), t.zeros(*(() if constant else (B, T)), H, device="cuda")
+    st, ds = t.randn(B, H, 8, 8, device="cuda"), t.randn(B, H, 8, 8, device="cuda")
+    y, s = la.linattn_forward(q, q, q, g, state=st)
+    gr = la.linattn_backward(q, q, q, g, q.clone(), state=st, dstate=ds)
+    t.cuda.synchronize()
+    assert y.shape == q.shape and all(gr[k].shape == q.shape for k in "qkv")
+    assert t.equal(s, st) and t.equal(gr["state"], ds) and bool((gr["g"] == 0).all()) and gr["g"].shape == g.shape
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("B,H,Dk,Dv", [(3, 2, 5, 7), (1, 4, 64, 64), (2, 3, 128, 100), (300, 4, 32, 64)])
 def test_steps_between_guards(B, H, Dk, Dv, dtype):

@@ -71,6 +71,31 @@ def test_one_long_sequence():
         check("d" + n, part(gr[n]), ref[n], tol[n])
 
 
+@pytest.mark.parametrize("D,shared", [(128, 4), (64, 1), (96, 2)])
+def test_a_full_chip_repeats(D, shared):
+    """Every compute unit with several workgroups for long, which drift apart within a chunk as far as the barriers
+    let them: results repeat to the bit, forward and backward, and no row is further from the fp32 kernels' (other
+    matrix instructions, chunks of half the length) than y's rounding, 2^-9 of a row's norm, and 2^-16 for each of
+    the two operands that y splits in two."""
+    t = torch()
+    B, T, H = 2, 8192, 32
+    q, k, v, dy = (normal(i, B, T, n, D) for i, n in enumerate((H // shared, H // shared, H, H)))
+    g = decays(4, B, T, H)
+    runs = [(mod().linattn_forward(q, k, v, g, scale=0.1), mod().linattn_backward(q, k, v, g, dy, scale=0.1)) for _ in range(3)]
+    wide = [(mod().linattn_forward(q.float(), k.float(), v.float(), g, scale=0.1), mod().linattn_backward(q.float(), k.float(), v.float(), g, dy.float(), scale=0.1))
+            for _ in range(2)]
+    t.cuda.synchronize()
+    for all_runs in (runs, wide):
+        (y, st), gr = all_runs[0]
+        for (y2, st2), gr2 in all_runs[1:]:
+            assert t.equal(y, y2) and t.equal(st, st2)
+            for n in gr:
+                assert t.equal(gr[n], gr2[n]), n
+    for got, want in [(runs[0][0][0], wide[0][0][0])] + [(runs[0][1][n], wide[0][1][n]) for n in "qkv"]:
+        off = (got.float() - want).norm(dim=-1) / want.norm(dim=-1)
+        assert float(off.max()) < 2.0 ** -8, float(off.max())
+
+
 def test_step_on_a_large_pool():
     B, S, H, D = 3, 8300, 16, 128
     pool = normal(0, S, H, D, D, dtype="f32")
