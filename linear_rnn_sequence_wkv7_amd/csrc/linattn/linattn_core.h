@@ -176,6 +176,11 @@ struct State {
         const rsrc_t d = buf_rsrc(p, da * dc * 4);
         each([&](float& x, uint32_t off) { __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), d, off, 0, 0); }, da, dc, transposed, wave, lane);
     }
+    // As it is held, in whole pieces.
+    __device__ __forceinline__ void leave(float* p, int wave, int lane) {
+        #pragma unroll
+        for (int a = 0; a < NA; ++a) *reinterpret_cast<f32x4*>(p + ((wave * NA + a) * 64 + lane) * 4) = s[a];
+    }
     __device__ __forceinline__ float dot(const float* p, int da, int dc, bool transposed, int wave, int lane) {
         const rsrc_t d = buf_rsrc(p, da * dc * 4);
         float sum = 0.f;
@@ -331,6 +336,10 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
         const int n = count(ch, c0, 0);
         const float* tab = tabs + (ch & 1) * kTab;
         const char* tile = smem + (ch & 1) * Lay::NEXT;
+        if constexpr (DOTS) {
+            const int t = t0 + c0 + (BACK ? L : 0);
+            if (s.marks && t % kMark == 0 && t < len) S.leave(s.marks + (bh * w.runs + t / kMark) * (DA * DC), wave, lane);
+        }
         __syncthreads();
         if (OUT && ch > 0) put_dots(c0 - STEP, count(ch - 1, c0 - STEP, 0));
         if (wave == kTabWave) make_tables<BACK>(tabs + (ch + 1 & 1) * kTab, g1, si, su, lane);
@@ -488,6 +497,7 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
                 for (int i = end + tid; i < t1; i += kThreads) s.dot[bh * w.T + i] = 0.f;
         }
         if (s.s_out && seg == (BACK ? 0 : w.segs - 1)) S.store(s.s_out + bh * elems, da, dc, s.transposed, wave, lane);
+        if (DOTS && BACK && s.marks && seg == 0) S.leave(s.marks + bh * w.runs * (DA * DC), wave, lane);
         if (DOTS && s.end_dot && seg == (BACK ? 0 : w.segs - 1)) {   // <the last state, its gradient>
             float d = S.dot(s.end_grad + bh * elems, da, dc, s.transposed, wave, lane);
             #pragma unroll

@@ -38,6 +38,8 @@ namespace linattn {
 
 constexpr double kNoDecayLog2 = -2000.0;   // a log2 of a decay below this counts as -inf: it is 0 in fp32 by far
 
+constexpr int kMark = 512;   // tokens; a multiple of every chunk's
+
 struct Operand {   // [B, T, heads, D]
     const void* p;
     int heads, D;
@@ -46,6 +48,7 @@ struct Operand {   // [B, T, heads, D]
 struct Chunks {
     int B, T, H;
     int group;                // how many consecutive heads share an operand
+    int runs;                 // of kMark tokens, the last one shorter
     int segs, seg_tokens;     // sequences are computed in parts side by side, of a multiple of 64 tokens
     bool g_per_token;
     const float* g;
@@ -63,6 +66,7 @@ struct Sweep {
     float* s_out;             // or null
     const float* end_grad;    // with end_dot [B, H]: <state behind the last token, end_grad>
     float* end_dot;
+    float* marks;             // [B, H, runs, widths' product] or null: the state in front of every run, as waves hold it
     float sp, si, su;
     int out_heads;
     bool out_bf16, back, transposed;   // transposed: the state is stored [c.D][a.D]
