@@ -24,6 +24,12 @@
 // is at once the operand of S^T a_t (the order of a contraction is free as long as both
 // operands agree), so it never goes through LDS.  out is computed transposed, so that a lane
 // has neighbouring columns of one token and stores them as one piece.
+//
+// Bound by no unit alone: vector work (splits into bf16, decays, addresses) and the matrix cores, which a
+// wave does in turn, and the waits at two barriers a chunk.  y of 8 x 1024 tokens, 32 heads of 64, bf16: 47 us
+// (2.9 TB/s); its three gradients 105 (vector units 45 %, matrix cores 22 %, LDS 31 % busy).  Of 2 x 16384
+// tokens, 32 heads of 128, q and k shared by four: 400 and 1085 us, 56, 32 and 30 %.  One workgroup by itself on a
+// compute unit takes 3 us for a chunk at heads of 64 and 5 at 128.
 #pragma once
 
 #include "../seq_device.h"
