@@ -19,7 +19,7 @@
  *
  * Chunks of 64 tokens (32 where an array is fp32) are computed together, so a token that
  * is not finite, and products past fp32's range, reach every output of their chunk and the
- * ones behind it.  A growing state (g > 0) has to grow by a finite factor over a chunk.
+ * ones behind it (the gradient of g: of their 512 tokens and the ones before).  A growing state (g > 0) has to grow by a finite factor over a chunk.
  * g = -inf empties the state; a g below about -1386 counts as -inf.
  *
  * Ragged batches (desc->lengths): tokens t >= lengths[b] of sequence b are padding: they

@@ -291,6 +291,30 @@ def test_attention_between_guards(case):
     same("y in place", y2, y), same("state in place", state, s)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,lengths,Dk,Dv,state", [(512, [512, 511, 1], 20, 33, True), (513, [513, 512, 0], 40, 24, False), (1100, [1100, 1024, 1025], 24, 70, True),
+                                                   (1024, None, 72, 20, True)])
+@pytest.mark.parametrize("per_token", [True, False])
+def test_gradients_of_decays_over_long_runs(T, lengths, Dk, Dv, state, per_token, dtype):
+    """The gradient of g is summed in runs of 512 tokens: lengths at and beside their ends, with states and
+    without, emptied ones among them.  The bound of one sum over all later tokens holds for the runs, too: a
+    state's product with its gradient has no terms that the sum's magnitudes do not have."""
+    la = mods()[1]
+    t = torch()
+    B, n = 3, 2
+    x = U.attn_inputs(T, B, T, n, Dk, Dv, Hk=1, dtype=dtype, per_token=per_token, state=state, rate=0.1)
+    if per_token:
+        x["g"][:, 300, 0] = -np.inf
+    rng = np.random.default_rng(T)
+    dy, ds = S.as_dtype(rng.standard_normal((B, T, n, Dv)), dtype), rng.standard_normal((B, n, Dk, Dv)).astype(np.float32)
+    g = la.linattn_backward(*(to_dev(x[k]) for k in "qkvg"), to_dev(dy), scale=0.3, state=None if not state else to_dev(x["state"]), dstate=to_dev(ds),
+                            lengths=lens(lengths))
+    t.cuda.synchronize()
+    ref, tol = U.attn_grad_bounds(x, dy, ds, 0.3, lengths)
+    for k in ("g", "state", "q", "k", "v"):
+        S.check("d" + k, to_host(g[k]), ref[k], tol[k], bf16=g[k].dtype == t.bfloat16)
+
+
 @pytest.mark.parametrize("B,T,H", [(0, 5, 2), (2, 0, 3), (2, 5, 0), (0, 0, 0)])
 @pytest.mark.parametrize("constant", [False, True])
 def test_attention_of_nothing(B, T, H, constant):
