@@ -26,9 +26,9 @@
 // has neighbouring columns of one token and stores them as one piece.
 //
 // Bound by no unit alone: vector work (splits into bf16, decays, addresses) and the matrix cores, which a
-// wave does in turn, and the waits at two barriers a chunk.  y of 8 x 1024 tokens, 32 heads of 64, bf16: 47 us
-// (2.9 TB/s); its three gradients 105 (vector units 45 %, matrix cores 22 %, LDS 31 % busy).  Of 2 x 16384
-// tokens, 32 heads of 128, q and k shared by four: 400 and 1085 us, 56, 32 and 30 %.  One workgroup by itself on a
+// wave does in turn, and the waits at two barriers a chunk.  y of 8 x 1024 tokens, 32 heads of 64, bf16: 52 us
+// (2.7 TB/s); its three gradients 105 (vector units 45 %, matrix cores 22 %, LDS 31 % busy).  Of 2 x 16384
+// tokens, 32 heads of 128, q and k shared by four: 434 and 1085 us, 56, 32 and 30 %.  One workgroup by itself on a
 // compute unit takes 3 us for a chunk at heads of 64 and 5 at 128.
 #pragma once
 
@@ -223,7 +223,7 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
     using St = State<O, DA>;
     constexpr int L = O::L, K = O::K, NL = L / 16, NA = St::NA, kThreads = 4 * DC, kWaves = DC / 16;
     constexpr bool kTight = !(O::E == 8 && DA == 64 && DC == 64 && WHOLE);   // registers are short: less is kept and overlapped
-    constexpr bool kShort = OUT && O::E == 8 && DA == 128 && DC == 128 && WHOLE && NP == 3;   // shorter: the next c is loaded late, too
+    constexpr bool kShort = OUT && O::E == 8 && DA == 128 && DC == 128 && WHOLE;   // shorter: the next c is loaded late, too
     constexpr bool kKeep = WHOLE && O::E == 8 && !(DA == 128 && DC == 128);
     constexpr bool kPace = O::E == 8;
     constexpr bool kLateX = kShort || (DA == 128 && DC == 128);
@@ -411,19 +411,19 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
         for (int m = 0; m < L / K; ++m) {
             cf[m] = O::template col<DC>(tile + Lay::C, at_c, wave, m);
             const typename O::template Lanes<DA> at_b(fresh<O::E == 4>(ln));   // (32 addresses of single floats are not worth keeping)
-            typename O::Frag cs[O::NPU];
+            typename O::Frag cs[O::NP];
             float v[O::E];
             #pragma unroll
             for (int e = 0; e < O::E; ++e) v[e] = O::get(cf[m], e) * tab[192 + K * m + O::E * g4 + e];
-            O::template split<O::NPU>(v, cs);
+            O::template split<O::NP>(v, cs);
             if constexpr (kPace) hold();
             #pragma unroll
             for (int a = 0; a < NA; ++a) {
                 const typename O::Frag bf = O::template col_of_state<DA>(tile + Lay::B, at_b, a, m);
                 #pragma unroll
-                for (int p = 0; p < O::NPU; ++p) S.s[a] = O::mma(bf, cs[p], S.s[a]);
+                for (int p = 0; p < O::NP; ++p) S.s[a] = O::mma(bf, cs[p], S.s[a]);
             }
-            if constexpr (kPace) pace<OUT ? 1 : 2, 2, O::NPU, NA>();
+            if constexpr (kPace) pace<OUT ? 1 : 2, 2, O::NP, NA>();
         }
         if constexpr (kShort) {
             hold();
@@ -553,11 +553,11 @@ struct Three {
 };
 // dq, dk and dv side by side, where keys and values are of one width.
 template <typename O, int D, bool WHOLE>
-__global__ __launch_bounds__(4 * D, (waves_per_simd<O, D, D, O::NPU, WHOLE>())) void grads_kernel(Chunks w, Three s) {
-    __shared__ alignas(16) char smem[Layout<O, D, D, O::NPU>::END];
+__global__ __launch_bounds__(4 * D, (waves_per_simd<O, D, D, O::NP, WHOLE>())) void grads_kernel(Chunks w, Three s) {
+    __shared__ alignas(16) char smem[Layout<O, D, D, O::NP>::END];
     const Place at(w, w.segs, 3);
-    if (at.kind == 0) sweep<O, D, D, O::NPU, false, true, WHOLE>(w, s.s[0], at.b, at.h, at.seg, smem);
-    else sweep<O, D, D, O::NPU, true, true, WHOLE>(w, s.s[at.kind], at.b, at.h, at.seg, smem);
+    if (at.kind == 0) sweep<O, D, D, O::NP, false, true, WHOLE>(w, s.s[0], at.b, at.h, at.seg, smem);
+    else sweep<O, D, D, O::NP, true, true, WHOLE>(w, s.s[at.kind], at.b, at.h, at.seg, smem);
 }
 
 // Heads are computed at 64 or 128, with zeros behind a smaller one's values; WHOLE: rows in whole 16-byte pieces.
@@ -595,9 +595,9 @@ inline hipError_t launch_backward(const Chunks& w, const Sweep& q, const Sweep& 
             grads_kernel<O, d, whole><<<dim3(uint32_t(int64_t(w.B) * w.H * w.segs * 3)), 4 * d, 0, st>>>(w, Three{{q, k, v}});
             return hipGetLastError();
         });
-    hipError_t e = launch_outs<O, O::NPU, false, true>(w, q, q, 1, st);
-    if (e == hipSuccess) e = launch_outs<O, O::NPU, true, true>(w, k, k, 1, st);
-    return e != hipSuccess ? e : launch_outs<O, O::NPU, true, true>(w, v, v, 1, st);
+    hipError_t e = launch_outs<O, O::NP, false, true>(w, q, q, 1, st);
+    if (e == hipSuccess) e = launch_outs<O, O::NP, true, true>(w, k, k, 1, st);
+    return e != hipSuccess ? e : launch_outs<O, O::NP, true, true>(w, v, v, 1, st);
 }
 
 }  // namespace linattn

@@ -10,7 +10,7 @@ struct F32Ops {
     using elem = float;
     using Frag = f32x4;
     static constexpr int E = 4, K = 16, L = 32;
-    static constexpr int NPY = 1, NPU = 1;
+    static constexpr int NP = 1;
 
     // Four products of depth 4: element e of the lanes' groups is the e-th one's contraction.
     static __device__ __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c) {
@@ -89,7 +89,7 @@ struct F32Ops {
 }  // namespace
 
 hipError_t parts_f32(const Chunks& w, const Sweep& s, hipStream_t st) { return launch_parts<F32Ops>(w, s, st); }
-hipError_t forward_f32(const Chunks& w, const Sweep& s, hipStream_t st) { return launch_outs<F32Ops, F32Ops::NPY, false, false>(w, s, s, 1, st); }
+hipError_t forward_f32(const Chunks& w, const Sweep& s, hipStream_t st) { return launch_outs<F32Ops, F32Ops::NP, false, false>(w, s, s, 1, st); }
 hipError_t backward_f32(const Chunks& w, const Sweep& q, const Sweep& k, const Sweep& v, hipStream_t st) { return launch_backward<F32Ops>(w, q, k, v, st); }
 
 }  // namespace linattn
