@@ -72,7 +72,7 @@ int linattn_forward(const linattn_desc* desc, const void* q, const void* k, cons
 int linattn_step(const linattn_desc* desc, const void* q, const void* k, const void* v, const float* g,
                  float* state, const int32_t* state_index, void* y, void* stream);
 
-/* Workspace bytes of linattn_backward; 0 when there is nothing to compute.  Host only. */
+/* Workspace bytes of linattn_backward; 0 when B T H is 0, and then none is touched.  Host only. */
 int64_t linattn_backward_workspace_bytes(const linattn_desc* desc);
 
 /* The gradients of <dy, y> + <dstate_out, state_out> for linattn_forward with these inputs.

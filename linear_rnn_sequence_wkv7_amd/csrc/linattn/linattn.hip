@@ -410,8 +410,8 @@ hipError_t launch_linattn_step(const LinAttnParams& p, hipStream_t st) {
 hipError_t launch_linattn_backward(const LinAttnParams& p, hipStream_t st) {
     Chunks w;
     plan(p, 3, &w);
-    const BackwardWs ws(p, w, p.ws);
     const int64_t rows = int64_t(p.B) * p.T;
+    const BackwardWs ws(p, w, rows > 0 ? p.ws : nullptr);   // without tokens none is needed: what is given may be of any size
     const bool bf16 = p.in_bf16 && p.y_bf16;
     const Operand q{p.q, p.Hq, p.Dk, p.in_bf16}, k{p.k, p.Hk, p.Dk, p.in_bf16}, v{p.v, p.Hv, p.Dv, p.in_bf16}, dy{p.dy, p.H, p.Dv, p.y_bf16};
     // a gradient goes to its place, or, where heads share one, each head's to the workspace
