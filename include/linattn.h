@@ -72,7 +72,9 @@ int linattn_forward(const linattn_desc* desc, const void* q, const void* k, cons
 int linattn_step(const linattn_desc* desc, const void* q, const void* k, const void* v, const float* g,
                  float* state, const int32_t* state_index, void* y, void* stream);
 
-/* Workspace bytes of linattn_backward; 0 when B T H is 0, and then none is touched.  Host only. */
+/* Workspace bytes of linattn_backward; 0 when B T H is 0, and then none is touched.  Among them, for every further
+ * 512 tokens behind the first, two states of each sequence and head (at widths of 64 or 128; whether or not dg is asked
+ * for), and a head's gradients in fp32 where heads share q, k or v.  Host only. */
 int64_t linattn_backward_workspace_bytes(const linattn_desc* desc);
 
 /* The gradients of <dy, y> + <dstate_out, state_out> for linattn_forward with these inputs.

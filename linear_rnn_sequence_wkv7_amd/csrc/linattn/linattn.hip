@@ -53,7 +53,8 @@ __global__ __launch_bounds__(kThreads) void chain_kernel(Chain f, Chain r, int s
 // differences is off by its terms' rounding, and a sum over the rest of the sequence by the root of its length
 // times that.  So the sum runs to the next of the marks, kMark tokens apart, where the sweeps leave the state and
 // its gradient, and their product is what all behind it comes to.  The mark in front gives the sum over the run
-// between them once more: what it is off by there is taken back evenly over the run's tokens.  8 x 1024 tokens, 32
+// between them once more (the first run's mark is the state that was given): what it is off by there is taken back
+// evenly over the run's tokens.  8 x 1024 tokens, 32
 // heads of 64: a relative error of 7.9e-7, with one sum over the sequence 1.9e-6, for 1 % of the call's time
 // (heads of 128, whose states are larger: 4 %).  In 64 bits.
 __device__ __forceinline__ double block_sum(double v, double* sums, int threads) {
@@ -66,11 +67,11 @@ __device__ __forceinline__ double block_sum(double v, double* sums, int threads)
     for (int i = 0; i < threads / 64; ++i) v += sums[i];
     return v;
 }
-// products [B, H, runs]: <state, its gradient> at the marks, `elems` of both in one order.
+// products [B, H, runs - 1]: <state, its gradient> at the marks, `elems` of both in one order.
 __global__ __launch_bounds__(kThreads) void mark_kernel(const float* state, const float* grad, Chunks w, int elems, double* products) {
     __shared__ double sums[kThreads / 64];
-    const int run = int(blockIdx.x % w.runs);
-    const int64_t bh = blockIdx.x / w.runs, at = int64_t(blockIdx.x) * elems;
+    const int run = int(blockIdx.x % (w.runs - 1)) + 1;
+    const int64_t bh = blockIdx.x / (w.runs - 1), at = int64_t(blockIdx.x) * elems;
     double v = 0.0;
     if (run * kMark < seq_length(w.lengths, bh / w.H, w.T))
         #pragma unroll 4
@@ -81,8 +82,10 @@ __global__ __launch_bounds__(kThreads) void mark_kernel(const float* state, cons
     v = block_sum(v, sums, kThreads);
     if (threadIdx.x == 0) products[blockIdx.x] = v;
 }
-// A thread per token, from a run's last to its first.
-__global__ __launch_bounds__(kMark) void dg_kernel(const float* qd, const float* kd, const float* end, const double* products, Chunks w, float* dg, float* part) {
+// A thread per token, from a run's last to its first.  start, end [B, H]: <state, its gradient> in front of the
+// first token and behind the last, or null (0).
+__global__ __launch_bounds__(kMark) void dg_kernel(const float* qd, const float* kd, const double* start, const double* end, const double* products, Chunks w,
+                                                   float* dg, float* part) {
     __shared__ double sums[kMark / 64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int run = int(blockIdx.x % w.runs);
@@ -98,8 +101,9 @@ __global__ __launch_bounds__(kMark) void dg_kernel(const float* qd, const float*
         if (i < wave) before += sums[i];
         all += sums[i];
     }
-    const double behind = len - first > kMark ? products[blockIdx.x + 1] : end ? end[bh] : 0.f;
-    const double off = all + behind - (products ? products[blockIdx.x] : 0.0);
+    const double* marks = products + bh * (w.runs - 1);   // of run 1 and on
+    const double behind = len - first > kMark ? marks[run] : end ? end[bh] : 0.0;
+    const double off = all + behind - (run > 0 ? marks[run - 1] : start ? start[bh] : 0.0);
     double total = 0.0;
     if (t < w.T) {
         const float g = w.g_per_token ? w.g[(b * w.T + t) * w.H + h] : w.g[h];
@@ -295,19 +299,21 @@ struct ForwardWs {
     }
 };
 struct BackwardWs {
-    float *qd, *kd, *end, *part, *states[2], *kept[2], *dq, *dk, *dv;
-    double* products;
-    float* marked[2];   // [B, H, runs, mark_elems]: states, and their gradients
+    float *qd, *kd, *part, *states[2], *kept[2], *dq, *dk, *dv;
+    double *start, *end, *products;
+    float* marked[2];   // [B, H, runs - 1, mark_elems]: states, and their gradients
     int64_t bytes;
     BackwardWs(const LinAttnParams& p, const Chunks& w, void* ws) {
         Carve c{static_cast<char*>(ws)};
-        const int64_t bh = int64_t(p.B) * p.H, n = w.segs > 1 ? bh * w.segs : 0;
+        const int64_t bh = int64_t(p.B) * p.H, n = w.segs > 1 ? bh * w.segs : 0, marks = w.runs > 1 ? bh * (w.runs - 1) : 0;
+        auto doubles = [&](int64_t n) { return reinterpret_cast<double*>(c.floats(2 * n)); };
         qd = c.floats(bh * p.T);
         kd = c.floats(bh * p.T);
-        end = c.floats(bh);
         part = c.floats(bh * w.runs);
-        products = reinterpret_cast<double*>(c.floats(bh * w.runs * 2));
-        for (float*& m : marked) m = c.floats(bh * w.runs * mark_elems(p));
+        start = doubles(bh);
+        end = doubles(bh);
+        products = doubles(marks);
+        for (float*& m : marked) m = c.floats(marks * mark_elems(p));
         for (int i = 0; i < 2; ++i) {
             states[i] = c.floats(n * p.Dk * p.Dv);
             kept[i] = c.floats(n);
@@ -436,11 +442,12 @@ hipError_t launch_linattn_backward(const LinAttnParams& p, hipStream_t st) {
     if (p.dg) {
         sq.x = q; sq.dot = ws.qd;
         sk.x = k; sk.dot = ws.kd;
-        if (w.runs > 1 || p.s0) {   // (else the only mark is the state 0)
+        if (w.runs > 1) {
             sq.marks = ws.marked[0];
             sk.marks = ws.marked[1];
         }
-        sq.end_grad = p.ds1; sq.end_dot = p.ds1 ? ws.end : nullptr;
+        sq.end_with = p.ds1; sq.end_dot = p.ds1 ? ws.end : nullptr;
+        sk.end_with = p.s0; sk.end_dot = p.s0 ? ws.start : nullptr;
     }
     if (w.segs > 1) {
         Sweep f = sv;
@@ -456,8 +463,8 @@ hipError_t launch_linattn_backward(const LinAttnParams& p, hipStream_t st) {
     if (p.Hv < p.H && rows > 0) TRY(shared_sum(ws.dv, p.dv, rows, p.Hv, p.H / p.Hv, p.Dv, p.in_bf16, st));
     if (p.dg) {
         const uint32_t jobs = uint32_t(int64_t(p.B) * p.H * w.runs);
-        if (sk.marks && rows > 0) mark_kernel<<<jobs, kThreads, 0, st>>>(ws.marked[0], ws.marked[1], w, mark_elems(p), ws.products);
-        if (rows > 0) dg_kernel<<<jobs, kMark, 0, st>>>(ws.qd, ws.kd, sq.end_dot, sk.marks ? ws.products : nullptr, w, p.dg, ws.part);
+        if (w.runs > 1) mark_kernel<<<jobs - jobs / w.runs, kThreads, 0, st>>>(ws.marked[0], ws.marked[1], w, mark_elems(p), ws.products);
+        if (rows > 0) dg_kernel<<<jobs, kMark, 0, st>>>(ws.qd, ws.kd, sk.end_dot, sq.end_dot, ws.products, w, p.dg, ws.part);
         if (!p.g_per_token) dg_heads_kernel<<<p.H, 64, 0, st>>>(ws.part, p.dg, rows > 0 ? p.B : 0, p.H, rows > 0 ? w.runs : 1);
     }
     return hipGetLastError();

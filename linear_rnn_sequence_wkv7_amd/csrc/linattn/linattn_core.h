@@ -71,7 +71,7 @@ struct Layout {
     static constexpr int NEXT = NPP ? 0 : L * (DA + DC) * es;   // where no out is computed the next chunk's rows have a place of their own
     static constexpr int P = C + L * DC * es + NEXT;
     static constexpr int TAB = P + NPP * L * L * es;
-    static constexpr int DOT = TAB + 2 * kTab * 4;        // float [waves][64], behind them one of each
+    static constexpr int DOT = TAB + 2 * kTab * 4;        // float [waves][64], behind them a double of each
     static constexpr int END = DOT + (DC / 16 * 64 + 16) * 4;
 };
 
@@ -187,10 +187,10 @@ struct State {
         #pragma unroll
         for (int a = 0; a < NA; ++a) *reinterpret_cast<f32x4*>(p + ((wave * NA + a) * 64 + lane) * 4) = s[a];
     }
-    __device__ __forceinline__ float dot(const float* p, int da, int dc, bool transposed, int wave, int lane) {
+    __device__ __forceinline__ double dot(const float* p, int da, int dc, bool transposed, int wave, int lane) {
         const rsrc_t d = buf_rsrc(p, da * dc * 4);
-        float sum = 0.f;
-        each([&](float& x, uint32_t off) { sum = fmaf(x, __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(d, off, 0, 0)), sum); }, da, dc, transposed, wave, lane);
+        double sum = 0.0;
+        each([&](float& x, uint32_t off) { sum += double(x) * __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(d, off, 0, 0)); }, da, dc, transposed, wave, lane);
         return sum;
     }
 };
@@ -344,7 +344,7 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
         const char* tile = smem + (ch & 1) * Lay::NEXT;
         if constexpr (DOTS) {
             const int t = t0 + c0 + (BACK ? L : 0);
-            if (s.marks && t % kMark == 0 && t < len) S.leave(s.marks + (bh * w.runs + t / kMark) * (DA * DC), wave, lane);
+            if (s.marks && t % kMark == 0 && t > 0 && t < len) S.leave(s.marks + (bh * (w.runs - 1) + t / kMark - 1) * (DA * DC), wave, lane);
         }
         __syncthreads();
         if (OUT && ch > 0) put_dots(c0 - STEP, count(ch - 1, c0 - STEP, 0));
@@ -503,18 +503,15 @@ __device__ void sweep(const Chunks& w, const Sweep& s, int b, int h, int seg, ch
                 for (int i = end + tid; i < t1; i += kThreads) s.dot[bh * w.T + i] = 0.f;
         }
         if (s.s_out && seg == (BACK ? 0 : w.segs - 1)) S.store(s.s_out + bh * elems, da, dc, s.transposed, wave, lane);
-        if (DOTS && BACK && s.marks && seg == 0) S.leave(s.marks + bh * w.runs * (DA * DC), wave, lane);
-        if (DOTS && s.end_dot && seg == (BACK ? 0 : w.segs - 1)) {   // <the last state, its gradient>
-            float d = S.dot(s.end_grad + bh * elems, da, dc, s.transposed, wave, lane);
-            #pragma unroll
-            for (int m = 1; m < 64; m *= 2) d += __shfl_xor(d, m);
-            float* sums = dots + kWaves * 64;
-            if (lane == 0) sums[wave] = d;
+        if (DOTS && s.end_dot && seg == (BACK ? 0 : w.segs - 1)) {
+            const double d = running_sum(S.dot(s.end_with + bh * elems, da, dc, s.transposed, wave, lane), lane);
+            double* sums = reinterpret_cast<double*>(dots + kWaves * 64);
+            if (lane == 63) sums[wave] = d;
             __syncthreads();
             if (tid == 0) {
-                d = 0.f;
-                for (int i = 0; i < kWaves; ++i) d += sums[i];
-                s.end_dot[bh] = d;
+                double all = 0.0;
+                for (int i = 0; i < kWaves; ++i) all += sums[i];
+                s.end_dot[bh] = all;
             }
         }
     } else {

@@ -64,9 +64,9 @@ struct Sweep {
     float* kept;              // [B, H, segs]: what is left of a state behind each
     const float* s_in;        // [B, H, Dk, Dv] or null
     float* s_out;             // or null
-    const float* end_grad;    // with end_dot [B, H]: <state behind the last token, end_grad>
-    float* end_dot;
-    float* marks;             // [B, H, runs, widths' product] or null: the state in front of every run, as waves hold it
+    const float* end_with;    // with end_dot [B, H]: <the state that s_out would get, end_with>
+    double* end_dot;
+    float* marks;             // [B, H, runs - 1, widths' product] or null: the state in front of every run but the first, as waves hold it
     float sp, si, su;
     int out_heads;
     bool out_bf16, back, transposed;   // transposed: the state is stored [c.D][a.D]
