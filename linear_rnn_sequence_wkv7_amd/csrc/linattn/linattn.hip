@@ -341,10 +341,12 @@ hipError_t chain(const Chunks& w, const Chain& f, const Chain& r, int kinds, int
     return hipGetLastError();
 }
 
+int64_t shared_sum_threads(int64_t rows, int heads, int D) { return (rows * heads * D / (D % 4 ? 1 : 4) + kThreads - 1) / kThreads * kThreads; }
 hipError_t shared_sum(const float* x, void* out, int64_t rows, int heads, int group, int D, bool bf16, hipStream_t st) {
     const int64_t n = rows * heads * D;
-    if (D % 4 == 0) shared_sum_kernel<4><<<uint32_t((n / 4 + kThreads - 1) / kThreads), kThreads, 0, st>>>(x, out, n / 4, group, D, bf16);
-    else shared_sum_kernel<1><<<uint32_t((n + kThreads - 1) / kThreads), kThreads, 0, st>>>(x, out, n, group, D, bf16);
+    const uint32_t grid = uint32_t(shared_sum_threads(rows, heads, D) / kThreads);
+    if (D % 4 == 0) shared_sum_kernel<4><<<grid, kThreads, 0, st>>>(x, out, n / 4, group, D, bf16);
+    else shared_sum_kernel<1><<<grid, kThreads, 0, st>>>(x, out, n, group, D, bf16);
     return hipGetLastError();
 }
 
@@ -382,9 +384,15 @@ int64_t linattn_step_threads(const LinAttnParams& p) {
 int64_t linattn_backward_threads(const LinAttnParams& p) {
     Chunks w;
     plan(p, 3, &w);
-    const int64_t sweeps = int64_t(p.B) * p.H * w.segs * 3 * 512, rows = int64_t(p.B) * p.T;
-    const int64_t dg = int64_t(p.B) * p.H * w.runs * kMark, sums = rows * p.H * (p.Dk > p.Dv ? p.Dk : p.Dv);
-    return sweeps > dg ? (sweeps > sums ? sweeps : sums) : (dg > sums ? dg : sums);
+    // the sweeps together, the gradient of g, and the sums over heads that share an operand
+    int64_t most = int64_t(p.B) * p.H * w.segs * 3 * 512;
+    auto at_least = [&](int64_t n) { most = n > most ? n : most; };
+    at_least(int64_t(p.B) * p.H * w.runs * kMark);
+    auto sums = [&](int heads, int D) { at_least(heads < p.H ? shared_sum_threads(int64_t(p.B) * p.T, heads, D) : 0); };
+    sums(p.Hq, p.Dk);
+    sums(p.Hk, p.Dk);
+    sums(p.Hv, p.Dv);
+    return most;
 }
 
 hipError_t launch_linattn_forward(const LinAttnParams& p, hipStream_t st) {

@@ -44,3 +44,27 @@ def test_without_tokens_no_workspace_is_written(Dk, Dv, size, dtype, constant):
     y, s = la.linattn_forward(*args, state=st, workspace=ws)
     t.cuda.synchronize()
     assert bool((whole == 255).all()) and t.equal(s, st)
+
+
+def test_gradients_of_more_than_2_32_elements():
+    """The state is emptied 150 tokens before the end, so that the oracle needs no more than those."""
+    from linear_rnn_sequence_wkv7_amd import linattn as la
+    from tests import attn_util as A
+    from tests.test_gpu_attn_large import decays
+    from tests.test_gpu_seq_large import check, host, normal
+    t = torch()
+    T, H, D, N = 1050000, 64, 64, 150
+    q, k, v, dy, g = *(normal(i, 1, T, H, D) for i in range(4)), decays(4, 1, T, H)
+    assert q.numel() > 1 << 32
+    g[:, T - N] = -1e5
+    ds = normal(6, 1, H, D, D, dtype="f32")
+    gr = la.linattn_backward(q, k, v, g, dy, scale=0.2, dstate=ds)
+    t.cuda.synchronize()
+    hs, last = slice(H - 2, H), slice(T - N, T)
+    part = lambda x: x[:, last, hs]
+    x = {**{n: host(part(a)) for n, a in (("q", q), ("k", k), ("v", v), ("g", g))}, "state": None}
+    ref, tol = A.attn_grad_bounds(x, host(part(dy)), host(ds[:, hs]), 0.2)
+    for n in ("q", "k", "v", "g"):
+        check("d" + n, part(gr[n]), ref[n], tol[n])
+    del q, k, v, dy, g, gr
+    t.cuda.empty_cache()
