@@ -155,7 +155,7 @@ struct Bf16Ops {
 }  // namespace
 
 hipError_t parts_bf16(const Chunks& w, const Sweep& s, hipStream_t st) { return launch_parts<Bf16Ops>(w, s, st); }
-hipError_t forward_bf16(const Chunks& w, const Sweep& s, hipStream_t st) { return launch_outs<Bf16Ops, Bf16Ops::NP, false, false>(w, s, s, 1, st); }
+hipError_t forward_bf16(const Chunks& w, const Sweep& s, hipStream_t st) { return launch_outs<Bf16Ops, false, false>(w, s, st); }
 hipError_t backward_bf16(const Chunks& w, const Sweep& q, const Sweep& k, const Sweep& v, hipStream_t st) { return launch_backward<Bf16Ops>(w, q, k, v, st); }
 
 }  // namespace linattn

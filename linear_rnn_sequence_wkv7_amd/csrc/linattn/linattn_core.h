@@ -534,15 +534,12 @@ constexpr int waves_per_simd() {
     constexpr int lds = 160 * 1024 / Layout<O, DA, DC, NP>::END * (DC / 64), regs = DA == 128 ? (DC == 128 && WHOLE ? 4 : 2) : (WHOLE || O::E == 4) ? 4 : DC == 128 ? 2 : 3;
     return lds < regs ? lds : regs;
 }
-struct Pair {
-    Sweep s[2];
-};
-// One or two outputs of the same widths side by side.
+// One output.
 template <typename O, int DA, int DC, int NP, bool BACK, bool DOTS, bool WHOLE>
-__global__ __launch_bounds__(4 * DC, (waves_per_simd<O, DA, DC, NP, WHOLE>())) void outs_kernel(Chunks w, Pair s, int kinds) {
+__global__ __launch_bounds__(4 * DC, (waves_per_simd<O, DA, DC, NP, WHOLE>())) void outs_kernel(Chunks w, Sweep s) {
     __shared__ alignas(16) char smem[Layout<O, DA, DC, NP>::END];
-    const Place at(w, w.segs, kinds);
-    sweep<O, DA, DC, NP, BACK, DOTS, WHOLE>(w, s.s[at.kind], at.b, at.h, at.seg, smem);
+    const Place at(w, w.segs, 1);
+    sweep<O, DA, DC, NP, BACK, DOTS, WHOLE>(w, s, at.b, at.h, at.seg, smem);
 }
 
 struct Three {
@@ -577,12 +574,15 @@ inline hipError_t launch_parts(const Chunks& w, const Sweep& s, hipStream_t st) 
         return hipGetLastError();
     });
 }
-template <typename O, int NP, bool BACK, bool DOTS>
-inline hipError_t launch_outs(const Chunks& w, const Sweep& x, const Sweep& y, int kinds, hipStream_t st) {
-    return with_widths<O>(x.a.D, x.c.D, [&](auto da, auto dc, auto whole) {
-        const dim3 grid(uint32_t(int64_t(w.B) * w.H * w.segs * kinds));
-        outs_kernel<O, da, dc, NP, BACK, DOTS, whole><<<grid, 4 * dc, 0, st>>>(w, Pair{{x, y}}, kinds);
-        return hipGetLastError();
+template <typename O, bool BACK, bool DOTS>
+inline hipError_t launch_outs(const Chunks& w, const Sweep& s, hipStream_t st) {
+    return with_widths<O>(s.a.D, s.c.D, [&](auto da, auto dc, auto whole) {
+        if constexpr (DOTS && da == dc) {
+            return hipErrorInvalidValue;   // grads_kernel's
+        } else {
+            outs_kernel<O, da, dc, O::NP, BACK, DOTS, whole><<<dim3(uint32_t(int64_t(w.B) * w.H * w.segs)), 4 * dc, 0, st>>>(w, s);
+            return hipGetLastError();
+        }
     });
 }
 template <typename O>
@@ -592,9 +592,9 @@ inline hipError_t launch_backward(const Chunks& w, const Sweep& q, const Sweep& 
             grads_kernel<O, d, whole><<<dim3(uint32_t(int64_t(w.B) * w.H * w.segs * 3)), 4 * d, 0, st>>>(w, Three{{q, k, v}});
             return hipGetLastError();
         });
-    hipError_t e = launch_outs<O, O::NP, false, true>(w, q, q, 1, st);
-    if (e == hipSuccess) e = launch_outs<O, O::NP, true, true>(w, k, k, 1, st);
-    return e != hipSuccess ? e : launch_outs<O, O::NP, true, true>(w, v, v, 1, st);
+    hipError_t e = launch_outs<O, false, true>(w, q, st);
+    if (e == hipSuccess) e = launch_outs<O, true, true>(w, k, st);
+    return e != hipSuccess ? e : launch_outs<O, true, true>(w, v, st);
 }
 
 }  // namespace linattn

@@ -89,7 +89,7 @@ struct F32Ops {
 }  // namespace
 
 hipError_t parts_f32(const Chunks& w, const Sweep& s, hipStream_t st) { return launch_parts<F32Ops>(w, s, st); }
-hipError_t forward_f32(const Chunks& w, const Sweep& s, hipStream_t st) { return launch_outs<F32Ops, F32Ops::NP, false, false>(w, s, s, 1, st); }
+hipError_t forward_f32(const Chunks& w, const Sweep& s, hipStream_t st) { return launch_outs<F32Ops, false, false>(w, s, st); }
 hipError_t backward_f32(const Chunks& w, const Sweep& q, const Sweep& k, const Sweep& v, hipStream_t st) { return launch_backward<F32Ops>(w, q, k, v, st); }
 
 }  // namespace linattn
