@@ -19,8 +19,19 @@
  *
  * Chunks of 64 tokens (32 where an array is fp32) are computed together, so a token that
  * is not finite, and products past fp32's range, reach every output of their chunk and the
- * ones behind it (the gradient of g: of their 512 tokens and the ones before).  A growing state (g > 0) has to grow by a finite factor over a chunk.
- * g = -inf empties the state; a g below about -1386 counts as -inf.
+ * ones behind it (the gradients of k and v: and the ones before it; that of g: of their 512
+ * tokens and the ones before).  A growing state (g > 0) has to grow by a finite factor over a
+ * chunk.  g = -inf empties a state of finite values; a g below about -1386 counts as -inf.
+ *
+ * Products and sums are fp32's for every type (a state is fp32, y and the gradients of q, k and
+ * v are rounded once, to their type).  The gradient of g is a difference of two numbers of a
+ * token, <q, dq> and <k, dk>, added up over up to 512 tokens, and is off by about 2^-19 of their
+ * size whatever the difference comes to: by 1e-6 of itself where the state is kept for long,
+ * 1e-5 where a token leaves exp(-2) of it, 2e-4 at exp(-5) and 4e-2 at exp(-10); further down it
+ * has no right digits (its size is then below 2^-19 of the products').
+ *
+ * Heads of which Dk or Dv is no multiple of 8 (bf16 arrays only) or 4 are read one element at a
+ * time, and take two to three times as long (a fifth to a half more where an array is fp32).
  *
  * Ragged batches (desc->lengths): tokens t >= lengths[b] of sequence b are padding: they
  * leave the state as it was, their y is 0, and their gradients are 0; nothing about their

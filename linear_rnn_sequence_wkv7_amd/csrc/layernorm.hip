@@ -314,7 +314,9 @@ __global__ __launch_bounds__(group_threads(R)) void ln_backward_kernel(LayerNorm
     }
 }
 
-// Rows past the registers of a workgroup: read again for each pass, out of the caches.
+// Rows past the registers of a workgroup, and those past 8185 channels that are no multiple of 8: read again for each
+// pass, element by element, out of the caches.  8192 rows in bf16 with a residual, of 9001 channels: forward 334 us,
+// backward 451 (of 9008, in registers: 127 and 181).
 constexpr int kLong = 1024;
 __device__ __forceinline__ float block_sum(float x, float* lds) {
     x = wave_sum(x);

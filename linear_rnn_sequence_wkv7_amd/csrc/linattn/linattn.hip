@@ -18,7 +18,7 @@ struct Chain {
     const float* kept;    // [B, H, segs]
     const float* first;   // [B, H, Dk, Dv] or null
 };
-// A thread per element of a state.  Eight segments' parts are read before the first is needed.  16 segments of
+// A thread per element of a state.  Eight segments' parts are read before the first is needed.  8 segments of
 // 64 heads' states and gradients of 128 x 128 take 25 us.
 __global__ __launch_bounds__(kThreads) void chain_kernel(Chain f, Chain r, int segs, int elems) {
     const bool back = blockIdx.z;
@@ -234,12 +234,14 @@ hipError_t step_rows(const LinAttnParams& p, dim3 grid, hipStream_t st) {
 // itself takes `lat` for a chunk, several on a compute unit `thr` each, and about two chunks' time goes
 // before the first; more than one segment costs a pass over two of the operands and the joining of the states.
 // us by the number of segments, bf16:
-//   forward   1 x 2048, 32 heads of 128   1: 156   4: 70    6: 59   8: 52   16: 60
-//             4 x 4096, 40 heads of 64    1: 223   2: 193   3: 133  4: 148  8: 135
-//             8 x 1024, 32 heads of 64    1: 52    2: 50    4: 59
-//             1 x 65536, 16 heads of 64   8: 537   16: 287  32: 205
-//   backward  2 x 2048, 32 heads of 64    1: 132   2: 129   4: 94   8: 96   16: 115
-//             4 x 1024, 32 heads of 128   1: 149   2: 186   4: 211
+//   forward   1 x 2048, 32 heads of 128   1: 172   4: 73    6: 60   8: 52   16: 60
+//             4 x 4096, 40 heads of 64    1: 232   2: 202   3: 136  4: 153  8: 142
+//             8 x 1024, 32 heads of 64    1: 52    2: 50    4: 57
+//             1 x 65536, 16 heads of 64   8: 546   16: 295  32: 213
+//   backward  2 x 2048, 32 heads of 64    1: 123   2: 122   4: 90   8: 96   16: 114
+//             4 x 1024, 32 heads of 128   1: 157   2: 190   4: 224
+// The gradients are counted as one launch.  Of keys and values on different sides of 64 they are three, one
+// after another, of a third of the workgroups each, which the rule does not know.
 void plan(const LinAttnParams& p, int kinds, Chunks* w) {
     const int64_t heads = int64_t(p.B) * p.H, chunks = (int64_t(p.T) + 63) / 64;
     const bool wide = p.Dk > 64 || p.Dv > 64, both = p.Dk > 64 && p.Dv > 64;
@@ -270,8 +272,8 @@ void plan(const LinAttnParams& p, int kinds, Chunks* w) {
     // Either each workgroup adds up the states of the segments before its own or, if there are more, a launch
     // does it for all (and where a state is moved in place, since a segment's workgroup would write it while
     // others still read it).  The gradients read two of three states transposed, a fourth of the speed.  1 x
-    // 4096, 16 heads of 64: forward 8 segments 44 us without the launch, 43 with it, 16 35 and 32; backward 2
-    // 205 and 208, 4 120 and 119, 8 93 and 84.  1 x 2048, 32 heads of 128, forward: 8 52 and 57, 16 68 and 60.
+    // 4096, 16 heads of 64: forward 8 segments 43 us without the launch, 42 with it, 16 35 and 31; backward 2
+    // 189 and 194, 4 111 and 109, 8 89 and 77.  1 x 2048, 32 heads of 128, forward: 8 52 and 55, 16 70 and 60.
     w->chained = best > (kinds > 1 ? 2 : 8) || (best > 1 && p.s0 && p.s0 == p.s1);
 }
 

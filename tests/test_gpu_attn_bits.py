@@ -65,3 +65,25 @@ def test_y_is_rounded_once(Dk, Dv, value, dtype):
     assert bool((forward(dtype, Dk, Dv, 70, "bf16", state=state, keys=False) == NEAR_TIES[value]).all())
     y = forward(dtype, Dk, Dv, min(Dv, 32), "bf16", scale=value)
     assert set(y.unique().tolist()) <= {0.0, NEAR_TIES[value]} and float(y[0, 0]) == NEAR_TIES[value]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("g", [-0.01, -0.5, -2.0, -5.0, -10.0, -20.0])
+def test_gradient_of_decays_is_off_by_its_terms_rounding(g, D, dtype):
+    """Whatever the decay leaves of the difference: a term's sum of about 30 accumulations is off by the root of that many
+    roundings, and the terms are added from either end of up to 512 tokens, 11 times one's error in the middle of a
+    random walk that is held at both: 6 * 11 * sqrt(2) units, less than 2^-17 of <q, dq>, as norms."""
+    from linear_rnn_sequence_wkv7_amd import linattn
+    from oracle import attn_oracle as O
+    from oracle.seq_oracle import as_f64
+    from tests import attn_util as A
+    from tests import seq_util as S
+    from tests.gpu_util import to_dev, to_host
+    x = A.attn_inputs(1, 1, 512, 2, D, D, dtype=dtype, rate=0.0)
+    x["g"][:] = np.float32(g)
+    dy = S.as_dtype(np.random.default_rng(2).standard_normal((1, 512, 2, D)), dtype)
+    got = linattn.linattn_backward(*(to_dev(x[n]) for n in "qkvg"), to_dev(dy), scale=D ** -0.5)["g"]
+    ref = O.attn_backward(x["q"], x["k"], x["v"], x["g"], dy, D ** -0.5)
+    terms = (as_f64(x["q"]) * ref["q"]).sum(-1)
+    assert np.linalg.norm(to_host(got) - ref["g"]) <= 2.0 ** -17 * np.linalg.norm(terms)
