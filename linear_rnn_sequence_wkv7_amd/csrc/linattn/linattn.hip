@@ -54,9 +54,9 @@ __global__ __launch_bounds__(kThreads) void chain_kernel(Chain f, Chain r, int s
 // times that.  So the sum runs to the next of the marks, kMark tokens apart, where the sweeps leave the state and
 // its gradient, and their product is what all behind it comes to.  The mark in front gives the sum over the run
 // between them once more (the first run's mark is the state that was given): what it is off by there is taken back
-// evenly over the run's tokens.  8 x 1024 tokens, 32
-// heads of 64: a relative error of 7.9e-7, with one sum over the sequence 1.9e-6, for 1 % of the call's time
-// (heads of 128, whose states are larger: 4 %).  In 64 bits.
+// evenly over the run's tokens.  8 x 1024 tokens, 32 heads of 64 that decay by exp(-0.05) to exp(-0.8) a token: a
+// relative error of 7.6e-7, with one sum over the sequence 1.9e-6, for 1 % of the call's time (heads of 128, whose
+// states are larger: 4 %).  In 64 bits.
 __device__ __forceinline__ double block_sum(double v, double* sums, int threads) {
     const int lane = threadIdx.x & 63;
     const double in = running_sum(v, lane);

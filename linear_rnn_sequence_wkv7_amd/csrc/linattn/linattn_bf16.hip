@@ -4,8 +4,8 @@
 // state, P and c times its decay, is split into three bf16 operands whose sum it is: the
 // products and sums are then as good as fp32's, and only what is stored is rounded.  (Two
 // operands, 2^-17 off, move a bf16 y by a step in one of a thousand places, and an fp32 y by
-// more than all else; y of 4 x 4096 tokens, 40 heads of 64: 125 us with them, 131 with three;
-// 1 x 2048, 32 heads of 128: 51 and 54; 8 x 1024, 32 heads of 64: 47 and 52.)
+// more than all else; replays of y of 4 x 4096 tokens, 40 heads of 64, take 125 us with them,
+// 131 with three; of 1 x 2048, 32 heads of 128, 51 and 54; of 8 x 1024, 32 heads of 64, 47 and 52.)
 #include "linattn_core.h"
 
 namespace wkv7 {

@@ -26,10 +26,11 @@
 // has neighbouring columns of one token and stores them as one piece.
 //
 // Bound by no unit alone: vector work (splits into bf16, decays, addresses) and the matrix cores, which a
-// wave does in turn, and the waits at two barriers a chunk.  y of 8 x 1024 tokens, 32 heads of 64, bf16: 52 us
-// (2.7 TB/s); its three gradients 105 (vector units 45 %, matrix cores 22 %, LDS 31 % busy).  Of 2 x 16384
-// tokens, 32 heads of 128, q and k shared by four: 434 and 1085 us, 56, 32 and 30 %.  One workgroup by itself on a
-// compute unit takes 3 us for a chunk at heads of 64 and 5 at 128.
+// wave does in turn, and the waits at two barriers a chunk.  Replays of one call, whose inputs the caches hold in
+// part: y of 8 x 1024 tokens, 32 heads of 64, bf16, 52 us (2.7 TB/s), its three gradients 105 (vector units 45 %,
+// matrix cores 22 %, LDS 31 % busy); of 2 x 16384 tokens, 32 heads of 128, q and k shared by four, y with the segments'
+// pass 434 us (62, 37 and 35 %) and the gradients 1085 (56, 32 and 30 %).  One workgroup by itself on a compute unit
+// takes 3 us for a chunk at heads of 64 and 5 at 128.
 #pragma once
 
 #include "../seq_device.h"
